@@ -17,8 +17,13 @@
  *   pa_decode_cascade      decode of a batch sharing a prompt prefix: the
  *                          shared blocks read once per KV head
  *   pa_copy_blocks         block copies of copy-on-write, all layers at once
- *   *_fp8                  the cache write, decode and split-KV decode
- *                          over an FP8 (E4M3) cache with per-KV-head scales
+ *   pa_rope_and_cache      the cache write with per-head norms of the new
+ *                          queries and keys and their rotation by position
+ *   pa_verify_drafts       drafted tokens accepted or rejected against the
+ *                          target's probabilities, and the token after them
+ *   *_fp8                  the cache writes, decode, split-KV decode and
+ *                          multi-token attention over an FP8 (E4M3) cache
+ *                          with per-KV-head scales
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -57,9 +62,9 @@
  * pa_device_error, which reads device memory synchronously.  The decode
  * kernels are launched with programmatic stream serialization: when the
  * kernel before them in the stream is a cache write of this library
- * (pa_reshape_and_cache, pa_reshape_and_cache_fp8), they start while it
- * finishes and read seq_lens, block_tables and query_start meanwhile -- the
- * cache writes never touch those -- and touch the caches, q and out only
+ * (pa_reshape_and_cache, pa_rope_and_cache, and their _fp8 forms), they start
+ * while it finishes and read seq_lens, block_tables and query_start meanwhile --
+ * the cache writes never touch those -- and touch the caches, q and out only
  * after it has completed.  After any other kernel they start as usual.
  *
  * Errors.  Calls return PA_OK (0) or a negative pa_status; nothing is
@@ -105,6 +110,8 @@ typedef enum {
                                       a query row range of pa_decode_multi was invalid */
 #define PA_DEVERR_SLOT       0x4u  /* a slot >= num_blocks*block_size was skipped */
 #define PA_DEVERR_TIMEOUT    0x8u  /* a wait on an asynchronous copy exceeded its limit */
+#define PA_DEVERR_POSITION   0x10u /* a position outside the rotation table: its token was skipped */
+#define PA_DEVERR_TOKEN      0x20u /* a drafted token outside the vocabulary was rejected */
 
 /*
  * pa_reshape_and_cache -- write the step's new keys and values into the cache.
@@ -128,6 +135,52 @@ int pa_reshape_and_cache(const void *k, const void *v, void *k_cache,
                          int32_t head_dim, int64_t k_token_stride,
                          int64_t v_token_stride, int64_t num_blocks,
                          int32_t block_size, int32_t dtype, void *stream);
+
+/*
+ * pa_rope_and_cache -- the step's cache write with what precedes it in the
+ * attention layer, in one pass: norms of the new queries and keys for each
+ * head, their rotation by position, q to q_out and k and v to their slots.
+ *
+ * For every token t, query head h and KV head j, with x one head's head_dim
+ * elements of q or k:
+ *   norm      with a weight row (q_weight for q, k_weight for k; [head_dim] of
+ *             `dtype`; NULL: no norm):  x <- x / sqrt(mean(x^2) + eps) * weight
+ *   rotation  of the first rot_dim elements (0: none), as rot_dim / 2 pairs:
+ *             (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) when interleaved
+ *             is not 0.  Pair i becomes (a cos - b sin, b cos + a sin) with
+ *             cos = rope_table[p][i], sin = rope_table[p][rot_dim/2 + i] and
+ *             p = positions[t].  Elements past rot_dim pass.
+ * q_out[t][h] is the result for q, and the slot of t receives the result for
+ * k in k_cache and v[t][j] bit for bit in v_cache.  Arithmetic is fp32 with one
+ * rounding at the end.
+ *
+ * rope_table is float32 [num_positions][rot_dim], contiguous.  q and q_out are
+ * [num_tokens][num_heads][head_dim] with heads contiguous and token strides of
+ * their own; q_out may be q itself with the same stride (in place), and may not
+ * overlap q, k or v otherwise.  num_heads == 0 writes keys and values only
+ * (q, q_out and q_weight are not looked at then).
+ *
+ * A token with a negative slot (padding) has its q_out row written and nothing
+ * in the caches; a slot past the pool likewise, with PA_DEVERR_SLOT.  A position
+ * outside [0, num_positions) skips the token altogether, with
+ * PA_DEVERR_POSITION unless it is a padding token.
+ *
+ * Requirements: block_size == 16; head_dim a multiple of 16, at most 256;
+ * rot_dim a multiple of 16, at most head_dim; num_heads, num_kv_heads <= 65535;
+ * eps >= 0 and finite if there is a weight; all pointers but positions and
+ * slot_mapping 16-byte aligned, token strides >= one token's heads with a byte
+ * size that is a multiple of 16.  Two tokens with the same slot race.
+ */
+int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v,
+                      void *k_cache, void *v_cache, const void *q_weight,
+                      const void *k_weight, float eps, const float *rope_table,
+                      int64_t num_positions, int32_t rot_dim, int32_t interleaved,
+                      const int64_t *positions, const int64_t *slot_mapping,
+                      int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int64_t q_token_stride,
+                      int64_t q_out_token_stride, int64_t k_token_stride,
+                      int64_t v_token_stride, int64_t num_blocks,
+                      int32_t block_size, int32_t dtype, void *stream);
 
 /*
  * pa_decode -- decode-step paged attention.
@@ -269,6 +322,56 @@ int pa_decode_multi(void *out, const void *q, const void *k_cache,
                     float scale, int32_t dtype, void *stream);
 
 /*
+ * pa_verify_drafts -- verification of drafted tokens, the step after
+ * pa_decode_multi in speculative decoding: "vLLM: Architecture, PagedAttention &
+ * Internals", *Speculative decoding* (the target scores the drafted tokens and
+ * the one after them in a single pass; drafts are kept up to the first one the
+ * target rejects).
+ *
+ * The rows are those of pa_decode_multi: sequence s owns rows query_start[s] ..
+ * query_start[s+1]-1, n of them; tokens[r] is row r's input token, so row
+ * query_start[s] is the token accepted last and row query_start[s] + i, i = 1 ..
+ * n-1, is draft i.  target_probs row r is the target's distribution of the
+ * token that follows row r; draft_probs row r is the distribution that draft
+ * tokens[r] was drawn from (rows query_start[s] are not read).  With
+ * draft_probs NULL the drafts come without probabilities (copied from the
+ * prompt, or greedy) and their probability is 1.
+ *
+ * Draft i at row r is accepted while accept_uniform[r] * draft_probs[r][x] <
+ * target_probs[r-1][x], x = tokens[r] (the product is exact).  With a the number
+ * accepted, the next token is drawn from the weights
+ *   w_v = max(target_probs[r-1][v] - draft_probs[r][v], 0)   a rejected draft r
+ *         (or target_probs[r-1] with w_x = 0 without draft probabilities; if
+ *         nothing is left, target_probs[r-1] itself);
+ *   w_v = target_probs[last row][v]                          if all are accepted.
+ * The difference is rounded to binary32, sums are taken as in binary64:
+ * the token is the first v with w_0 + .. + w_v > u * sum(w), u =
+ * sample_uniform[s] clamped to [0, 1] (at u = 1 the last v with a weight).  Entries
+ * that are negative or NaN count as 0, and an infinite entry leaves weight 0;
+ * a row without any weight gives token -1.  Sums must stay inside the binary32
+ * range.
+ *
+ * out_tokens, int32 [num_seqs][max_query_len], receives the a accepted drafts,
+ * the token drawn, then -1; num_accepted[s] receives a.  A sequence without
+ * rows gets -1 throughout and 0; one whose row range is out of bounds,
+ * decreasing or longer than max_query_len likewise, with PA_DEVERR_SEQ_LEN.  A
+ * drafted token outside [0, vocab_size) is rejected, with PA_DEVERR_TOKEN if it
+ * is the first one rejected.
+ *
+ * accept_uniform is float32 [num_rows] (rows query_start[s] are not read),
+ * sample_uniform float32 [num_seqs].  target_probs and draft_probs are of
+ * `dtype`, rows contiguous with strides >= vocab_size of any alignment.
+ * num_seqs == 0 launches nothing.
+ */
+int pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted,
+                     const void *target_probs, const void *draft_probs,
+                     const int32_t *tokens, const float *accept_uniform,
+                     const float *sample_uniform, const int32_t *query_start,
+                     int32_t num_seqs, int32_t num_rows, int32_t max_query_len,
+                     int32_t vocab_size, int64_t target_row_stride,
+                     int64_t draft_row_stride, int32_t dtype, void *stream);
+
+/*
  * pa_copy_blocks -- the GPU half of copy-on-write.
  *
  * Defined in "vLLM: Architecture, PagedAttention & Internals", *Copy-on-write
@@ -331,6 +434,25 @@ int pa_reshape_and_cache_fp8(const void *k, const void *v, void *k_cache,
                              int32_t block_size, int32_t dtype, void *stream);
 
 /*
+ * pa_rope_and_cache_fp8 -- pa_rope_and_cache into E4M3 caches: the result x for
+ * k, and v itself, of KV head j are stored as E4M3(x / scale_j), rounded as in
+ * pa_reshape_and_cache_fp8 (the quotient of the fp32 result).  q_out stays in
+ * `dtype`.
+ */
+int pa_rope_and_cache_fp8(void *q_out, const void *q, const void *k, const void *v,
+                          void *k_cache, void *v_cache, const float *k_scale,
+                          const float *v_scale, const void *q_weight,
+                          const void *k_weight, float eps, const float *rope_table,
+                          int64_t num_positions, int32_t rot_dim,
+                          int32_t interleaved, const int64_t *positions,
+                          const int64_t *slot_mapping, int64_t num_tokens,
+                          int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                          int64_t q_token_stride, int64_t q_out_token_stride,
+                          int64_t k_token_stride, int64_t v_token_stride,
+                          int64_t num_blocks, int32_t block_size, int32_t dtype,
+                          void *stream);
+
+/*
  * pa_decode_fp8 / pa_decode_partitioned_fp8 -- pa_decode and
  * pa_decode_partitioned over E4M3 caches: K_s[t] = value(code) * k_scale[j]
  * and V_s[t] = value(code) * v_scale[j] for KV head j, the attention itself
@@ -360,6 +482,23 @@ int pa_decode_partitioned_fp8(void *out, const void *q, const void *k_cache,
                               int32_t partition_size, int32_t max_seq_len,
                               void *workspace, size_t workspace_bytes,
                               void *stream);
+
+/*
+ * pa_decode_multi_fp8 -- pa_decode_multi over E4M3 caches: several new tokens
+ * per sequence (drafts to verify, or a chunk of a prompt), causal among
+ * themselves, K_s[t] and V_s[t] dequantised as in pa_decode_fp8.  `dtype` is the
+ * type of q and out, PA_BF16 or PA_F16 (q is rounded to f16: |q| < 65504).
+ * Rows, query_start, errors and requirements as pa_decode_multi.
+ */
+int pa_decode_multi_fp8(void *out, const void *q, const void *k_cache,
+                        const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int32_t *block_tables,
+                        const int32_t *seq_lens, const int32_t *query_start,
+                        int32_t num_seqs, int32_t num_q_rows, int32_t max_query_len,
+                        int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int64_t num_blocks, int32_t block_size,
+                        int32_t max_blocks_per_seq, int64_t q_row_stride,
+                        float scale, int32_t dtype, void *stream);
 
 /*
  * pa_decode_cascade_workspace_size -- bytes of workspace pa_decode_cascade
@@ -479,7 +618,8 @@ int pa_device_error(uint32_t *flags, int clear);
  */
 int pa_test_stall_next_decode(void);
 
-/* ABI version of this header (increments on any signature change or addition). */
+/* ABI version of this header (increments when the signature or the meaning of a
+ * declared function changes; functions may be added without). */
 int pa_abi_version(void);
 
 #ifdef __cplusplus

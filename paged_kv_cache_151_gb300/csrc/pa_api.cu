@@ -660,6 +660,178 @@ int pa_decode_partitioned_fp8(void *out, const void *q, const void *k_cache,
 
 }  // extern "C"
 
+// ---- multi-token queries over E4M3 caches -----------------------------------
+
+extern "C" int pa_decode_multi_fp8(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, const int32_t *seq_lens,
+    const int32_t *query_start, int32_t num_seqs, int32_t num_q_rows, int32_t max_query_len,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+    int32_t block_size, int32_t max_blocks_per_seq, int64_t q_row_stride, float scale,
+    int32_t dtype, void *stream) {
+    int rc = check_decode_args(out, q, k_cache, v_cache, block_tables, seq_lens, num_seqs,
+                               num_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                               max_blocks_per_seq, q_row_stride, scale, dtype);
+    if (rc != PA_OK) return rc;
+    if (num_q_rows < 0 || max_query_len < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_q_rows == 0) return PA_OK;
+    if (!query_start || !k_scale || !v_scale) return PA_ERR_INVALID_ARG;
+    if (dtype != PA_BF16 && dtype != PA_F16) return PA_ERR_UNSUPPORTED;
+    if (!q_rows_aligned(q, q_row_stride, dtype) || !aligned16(out)) return PA_ERR_INVALID_ARG;
+    const int G = num_heads / num_kv_heads;
+    const int64_t rows = (int64_t)(max_query_len < num_q_rows ? max_query_len : num_q_rows) * G;
+    if (rows == 0) return PA_OK;
+    pa::DecodeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.out = out; p.q = q; p.k_cache = k_cache; p.v_cache = v_cache;
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.block_tables = block_tables; p.seq_lens = seq_lens;
+    p.query_start = query_start;
+    p.max_query_len = max_query_len;
+    p.num_q_rows = num_q_rows;
+    p.num_blocks = num_blocks; p.q_seq_stride = q_row_stride;
+    p.num_seqs = num_seqs; p.num_heads = num_heads; p.num_kv_heads = num_kv_heads;
+    p.max_blocks = max_blocks_per_seq;
+    p.scale_log2 = scale * pa::LOG2E;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    if (!prepare_maps(p, PA_E4M3, head_dim)) return PA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long unit_bound = (long long)num_seqs * num_kv_heads * ((rows + 15) / 16);
+    cudaError_t e = dtype == PA_BF16
+                        ? pa::decode_multi_fp8_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
+                        : pa::decode_multi_fp8_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st);
+    if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- the cache write with norms and rotation ---------------------------------
+
+namespace {
+
+bool strided16(int64_t stride, int es) { return (stride * es) % 16 == 0; }
+
+int rope_common(pa::RopeParams &p, bool fp8, int64_t num_blocks, int32_t block_size, int32_t dtype,
+                void *stream) {
+    if (p.num_tokens < 0 || p.num_heads < 0 || p.num_kv_heads <= 0 || p.head_dim <= 0 ||
+        num_blocks < 0 || p.rot_dim < 0 || p.rot_dim > p.head_dim || p.num_positions < 0)
+        return PA_ERR_INVALID_ARG;
+    const int es = elem_size(dtype);
+    if (es == 0) return PA_ERR_UNSUPPORTED;
+    if (block_size != 16) return PA_ERR_UNSUPPORTED;
+    if (p.head_dim % 16 || p.head_dim > 256 || p.rot_dim % 16) return PA_ERR_UNSUPPORTED;
+    if (p.num_heads > 65535 || p.num_kv_heads > 65535 || p.num_tokens > (int64_t)INT32_MAX ||
+        num_blocks > (int64_t)INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (p.num_tokens == 0) return PA_OK;
+    if (!p.k || !p.v || !p.k_cache || !p.v_cache || !p.slot_mapping) return PA_ERR_INVALID_ARG;
+    if (p.num_heads > 0 && (!p.q || !p.q_out)) return PA_ERR_INVALID_ARG;
+    if (p.rot_dim > 0 && (!p.rope_table || !p.positions)) return PA_ERR_INVALID_ARG;
+    if (fp8 && (!p.k_scale || !p.v_scale)) return PA_ERR_INVALID_ARG;
+    if ((p.q_weight || p.k_weight) && !(p.eps >= 0.f && p.eps <= 3.4e38f)) return PA_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)p.num_heads * p.head_dim, kv_row = (int64_t)p.num_kv_heads * p.head_dim;
+    if (p.k_stride < kv_row || p.v_stride < kv_row) return PA_ERR_INVALID_ARG;
+    if (p.num_heads > 0 && (p.q_stride < q_row || p.q_out_stride < q_row)) return PA_ERR_INVALID_ARG;
+    // every access is 16 bytes wide
+    if (!aligned16(p.k) || !aligned16(p.v) || !aligned16(p.k_cache) || !aligned16(p.v_cache) ||
+        !strided16(p.k_stride, es) || !strided16(p.v_stride, es))
+        return PA_ERR_INVALID_ARG;
+    if (p.num_heads > 0 && (!aligned16(p.q) || !aligned16(p.q_out) || !strided16(p.q_stride, es) ||
+                            !strided16(p.q_out_stride, es)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(p.q_weight) || !aligned16(p.k_weight)) return PA_ERR_INVALID_ARG;
+    if (p.rot_dim > 0 && !aligned16(p.rope_table)) return PA_ERR_INVALID_ARG;
+    p.num_slots = num_blocks * 16;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    cudaError_t e = pa::rope_and_cache(p, dtype, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_rope_and_cache(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                      void *v_cache, const void *q_weight, const void *k_weight, float eps,
+                      const float *rope_table, int64_t num_positions, int32_t rot_dim,
+                      int32_t interleaved, const int64_t *positions, const int64_t *slot_mapping,
+                      int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                      int32_t head_dim, int64_t q_token_stride, int64_t q_out_token_stride,
+                      int64_t k_token_stride, int64_t v_token_stride, int64_t num_blocks,
+                      int32_t block_size, int32_t dtype, void *stream) {
+    pa::RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q_out = q_out; p.q = q; p.k = k; p.v = v; p.k_cache = k_cache; p.v_cache = v_cache;
+    p.q_weight = q_weight; p.k_weight = k_weight; p.eps = eps;
+    p.rope_table = rope_table; p.num_positions = num_positions; p.rot_dim = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.positions = positions; p.slot_mapping = slot_mapping; p.num_tokens = num_tokens;
+    p.num_heads = num_heads; p.num_kv_heads = num_kv_heads; p.head_dim = head_dim;
+    p.q_stride = q_token_stride; p.q_out_stride = q_out_token_stride;
+    p.k_stride = k_token_stride; p.v_stride = v_token_stride;
+    return rope_common(p, false, num_blocks, block_size, dtype, stream);
+}
+
+int pa_rope_and_cache_fp8(void *q_out, const void *q, const void *k, const void *v, void *k_cache,
+                          void *v_cache, const float *k_scale, const float *v_scale,
+                          const void *q_weight, const void *k_weight, float eps,
+                          const float *rope_table, int64_t num_positions, int32_t rot_dim,
+                          int32_t interleaved, const int64_t *positions,
+                          const int64_t *slot_mapping, int64_t num_tokens, int32_t num_heads,
+                          int32_t num_kv_heads, int32_t head_dim, int64_t q_token_stride,
+                          int64_t q_out_token_stride, int64_t k_token_stride,
+                          int64_t v_token_stride, int64_t num_blocks, int32_t block_size,
+                          int32_t dtype, void *stream) {
+    pa::RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q_out = q_out; p.q = q; p.k = k; p.v = v; p.k_cache = k_cache; p.v_cache = v_cache;
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.q_weight = q_weight; p.k_weight = k_weight; p.eps = eps;
+    p.rope_table = rope_table; p.num_positions = num_positions; p.rot_dim = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.positions = positions; p.slot_mapping = slot_mapping; p.num_tokens = num_tokens;
+    p.num_heads = num_heads; p.num_kv_heads = num_kv_heads; p.head_dim = head_dim;
+    p.q_stride = q_token_stride; p.q_out_stride = q_out_token_stride;
+    p.k_stride = k_token_stride; p.v_stride = v_token_stride;
+    return rope_common(p, true, num_blocks, block_size, dtype, stream);
+}
+
+// ---- verification of drafted tokens -------------------------------------------
+
+int pa_verify_drafts(int32_t *out_tokens, int32_t *num_accepted, const void *target_probs,
+                     const void *draft_probs, const int32_t *tokens, const float *accept_uniform,
+                     const float *sample_uniform, const int32_t *query_start, int32_t num_seqs,
+                     int32_t num_rows, int32_t max_query_len, int32_t vocab_size,
+                     int64_t target_row_stride, int64_t draft_row_stride, int32_t dtype,
+                     void *stream) {
+    if (num_seqs < 0 || num_rows < 0 || max_query_len < 0 || vocab_size <= 0)
+        return PA_ERR_INVALID_ARG;
+    const int es = elem_size(dtype);
+    if (es == 0) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!num_accepted || !query_start || (max_query_len > 0 && !out_tokens)) return PA_ERR_INVALID_ARG;
+    if (num_rows > 0 && (!target_probs || !tokens || !accept_uniform || !sample_uniform))
+        return PA_ERR_INVALID_ARG;
+    if (target_row_stride < vocab_size || (draft_probs && draft_row_stride < vocab_size))
+        return PA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(target_probs) | reinterpret_cast<uintptr_t>(draft_probs)) % es)
+        return PA_ERR_INVALID_ARG;
+    pa::VerifyParams p;
+    std::memset(&p, 0, sizeof p);
+    p.out_tokens = out_tokens; p.num_accepted = num_accepted;
+    p.target = target_probs; p.draft = draft_probs; p.tokens = tokens;
+    p.accept_u = accept_uniform; p.sample_u = sample_uniform; p.query_start = query_start;
+    p.target_stride = target_row_stride; p.draft_stride = draft_row_stride;
+    p.num_seqs = num_seqs; p.num_rows = num_rows; p.max_query_len = max_query_len;
+    p.vocab = vocab_size;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    cudaError_t e = pa::verify_drafts(p, dtype, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
+
 // ---- split-KV decode without any allocation ---------------------------------
 //
 // Some callers cannot call cudaMalloc at the point where they decode: code

@@ -21,6 +21,8 @@ constexpr unsigned ERR_BLOCK_ID = 0x1u;
 constexpr unsigned ERR_SEQ_LEN = 0x2u;
 constexpr unsigned ERR_SLOT = 0x4u;
 constexpr unsigned ERR_TIMEOUT = 0x8u;
+constexpr unsigned ERR_POSITION = 0x10u;
+constexpr unsigned ERR_TOKEN = 0x20u;
 
 // Wall-clock limit of any wait on an asynchronous copy (ns).
 constexpr unsigned long long WAIT_LIMIT_NS = 1000000000ull;

@@ -330,4 +330,228 @@ struct WarpAttnF8 {
     }
 };
 
+// Sixteen query rows at once: the (query token, head) pairs of a multi-token
+// query that share one KV head, each with its own causal limit, in the
+// layouts of WarpAttnF8.  Lane (g, t) scores rows g ("lo") and g + 8 ("hi");
+// the value product takes the rows as two tiles of eight columns, which share
+// the V fragments, so a block's codes are converted once for 16 rows.
+template <typename T, int D>
+struct WarpAttnF8x16 {
+    static_assert(sizeof(T) == 2, "q and out are 16-bit");
+    static_assert(D == 64 || D == 128, "head_dim");
+    static constexpr int KK = D / 32;
+    static constexpr int MT = D / 16;
+    static constexpr int DL = D / 8;
+
+    int lane, g, t;
+    int lim[2];                            // last visible position of rows g, g + 8 (-1: no row)
+    uint32_t qa[2 * KK][4];                // f16 A fragments, d permuted as in WarpAttnF8
+    // acc[h][mt]: as WarpAttnF8::acc for rows 8h + 2t and 8h + 2t + 1
+    float acc[2][MT][4];
+    float m_run[2], l_run[2], m_max[2];    // of rows g and g + 8
+
+    __device__ __forceinline__ void init(int lane_) {
+        lane = lane_;
+        g = lane >> 2;
+        t = lane & 3;
+        lim[0] = lim[1] = -1;
+        reset();
+    }
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            m_run[h] = m_max[h] = -INFINITY;
+            l_run[h] = 0.f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[h][j][e] = 0.f;
+        }
+    }
+
+    // query rows (nullptr: no such row) and their causal limits
+    __device__ __forceinline__ void load_q(const T *q_lo, const T *q_hi, int lo_lim, int hi_lim) {
+        lim[0] = q_lo ? lo_lim : -1;
+        lim[1] = q_hi ? hi_lim : -1;
+        const T *src[2] = {q_lo, q_hi};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint4 w = src[h] ? __ldg(reinterpret_cast<const uint4 *>(src[h] + 32 * kk + 8 * t))
+                                       : make_uint4(0, 0, 0, 0);
+                qa[2 * kk][h] = WarpAttnF8<T, D, 1>::to_f16x2(w.x);          // d 32kk+8t + {0,1}
+                qa[2 * kk][2 + h] = WarpAttnF8<T, D, 1>::to_f16x2(w.y);      //            {2,3}
+                qa[2 * kk + 1][h] = WarpAttnF8<T, D, 1>::to_f16x2(w.z);      //            {4,5}
+                qa[2 * kk + 1][2 + h] = WarpAttnF8<T, D, 1>::to_f16x2(w.w);  //            {6,7}
+            }
+        }
+    }
+
+    // a value of rows g / g + 8 for this lane's accumulator rows 8h + 2t and
+    // 8h + 2t + 1
+    template <typename V>
+    __device__ __forceinline__ void row_values(V v, V &a, V &b) const {
+        a = __shfl_sync(0xffffffffu, v, (8 * t) & 31);
+        b = __shfl_sync(0xffffffffu, v, (8 * t + 4) & 31);
+    }
+
+    __device__ __forceinline__ void rescale(int h, float f) {
+        float fa, fb;
+        row_values(f, fa, fb);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            acc[h][mt][0] *= fa;
+            acc[h][mt][1] *= fb;
+            acc[h][mt][2] *= fa;
+            acc[h][mt][3] *= fb;
+        }
+    }
+
+    // One block of E4M3 tiles whose row 0 is at sequence position pos0; V rows
+    // past the sequence's end are zero (zero_rows).  scale_log2 already
+    // carries K's scale.
+    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int pos0, float scale_log2) {
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        const int r0 = fp8_tile_token(g), r1 = 8 + r0;
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const uint2 k0 = lds64(kt + fp8_swz<D>(r0, 32 * kk + 8 * t));
+            const uint2 k1 = lds64(kt + fp8_swz<D>(r1, 32 * kk + 8 * t));
+            const uint32_t *a = qa[2 * kk], *b = qa[2 * kk + 1];
+            Mma<__half>::run4(s0, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k0.x),
+                              f16x2_from_e4m3x2(k0.x >> 16));
+            Mma<__half>::run4(s1, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k1.x),
+                              f16x2_from_e4m3x2(k1.x >> 16));
+            Mma<__half>::run4(s0, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k0.y),
+                              f16x2_from_e4m3x2(k0.y >> 16));
+            Mma<__half>::run4(s1, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k1.y),
+                              f16x2_from_e4m3x2(k1.y >> 16));
+        }
+        const int ta = fp8_tile_token(2 * t), tb = fp8_tile_token(2 * t + 1);
+        const int pos[4] = {pos0 + ta, pos0 + tb, pos0 + 8 + ta, pos0 + 8 + tb};
+        uint32_t pb[2][2];                 // B fragments of the two row tiles
+        float alpha[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float sc[4] = {s0[2 * h], s0[2 * h + 1], s1[2 * h], s1[2 * h + 1]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[e] = pos[e] <= lim[h] ? sc[e] * scale_log2 : -INFINITY;
+            float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            m_max[h] = fmaxf(m_max[h], mx);
+            const float m_new = mx > m_run[h] + RESCALE_LOG2 ? mx : m_run[h];   // lazy rescaling
+            const float ms = m_new == -INFINITY ? 0.f : m_new;
+            alpha[h] = ex2(m_run[h] - ms);
+            pb[h][0] = Mma<__half>::pack(ex2(sc[0] - ms), ex2(sc[1] - ms));
+            pb[h][1] = Mma<__half>::pack(ex2(sc[2] - ms), ex2(sc[3] - ms));
+            float p0, p1, p2, p3;
+            Mma<__half>::unpack(pb[h][0], p0, p1);
+            Mma<__half>::unpack(pb[h][1], p2, p3);
+            l_run[h] = l_run[h] * alpha[h] + ((p0 + p1) + (p2 + p3));
+            m_run[h] = m_new;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+            rescale(0, alpha[0]);
+            rescale(1, alpha[1]);
+        }
+        // A fragments of V^T: d rows 2mt (a0, a2) and 2mt + 1 (a1, a3) of this
+        // lane's run of DL bytes, tokens ta, tb (a0, a1) and 8 + ta, 8 + tb
+        uint32_t wa[DL / 4], wb[DL / 4], wc[DL / 4], wd[DL / 4];
+        load_run(vt, ta, wa);
+        load_run(vt, tb, wb);
+        load_run(vt, 8 + ta, wc);
+        load_run(vt, 8 + tb, wd);
+#pragma unroll
+        for (int w = 0; w < DL / 4; ++w) {
+            const uint32_t lo01 = prmt(wa[w], wb[w], 0x5140), lo23 = prmt(wa[w], wb[w], 0x7362);
+            const uint32_t hi01 = prmt(wc[w], wd[w], 0x5140), hi23 = prmt(wc[w], wd[w], 0x7362);
+            const uint32_t a0 = f16x2_from_e4m3x2(lo01), a1 = f16x2_from_e4m3x2(lo01 >> 16);
+            const uint32_t a2 = f16x2_from_e4m3x2(hi01), a3 = f16x2_from_e4m3x2(hi01 >> 16);
+            Mma<__half>::run4(acc[0][2 * w], a0, a1, a2, a3, pb[0][0], pb[0][1]);
+            Mma<__half>::run4(acc[1][2 * w], a0, a1, a2, a3, pb[1][0], pb[1][1]);
+            const uint32_t c0 = f16x2_from_e4m3x2(lo23), c1 = f16x2_from_e4m3x2(lo23 >> 16);
+            const uint32_t c2 = f16x2_from_e4m3x2(hi23), c3 = f16x2_from_e4m3x2(hi23 >> 16);
+            Mma<__half>::run4(acc[0][2 * w + 1], c0, c1, c2, c3, pb[0][0], pb[0][1]);
+            Mma<__half>::run4(acc[1][2 * w + 1], c0, c1, c2, c3, pb[1][0], pb[1][1]);
+        }
+    }
+
+    // bytes DL*g .. DL*g + DL-1 of V row `row`
+    __device__ __forceinline__ void load_run(uint32_t vt, int row, uint32_t (&w)[DL / 4]) const {
+        if constexpr (D == 128) {
+            const uint4 v = lds128(vt + fp8_swz<D>(row, 16 * g));
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+            const uint2 v = lds64(vt + fp8_swz<D>(row, 8 * g));
+            w[0] = v.x; w[1] = v.y;
+        }
+    }
+
+    __device__ __forceinline__ static void zero_rows(unsigned char *vt, int rows, int lane) {
+        WarpAttnF8<T, D, 1>::zero_rows(vt, rows, lane);
+    }
+
+    // Bring the state to the true maximum, then sum the lanes of each row.
+    __device__ __forceinline__ void finish() {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            f[h] = m_max[h] == -INFINITY ? 1.f
+                                         : ex2((m_run[h] == -INFINITY ? m_max[h] : m_run[h]) - m_max[h]);
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+            rescale(0, f[0]);
+            rescale(1, f[1]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l_run[h] *= f[h];
+            m_run[h] = m_max[h];
+            l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
+            l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
+        }
+    }
+
+    // merge slot: Mw[16], Lw[16], Aw[16][D] in natural d order
+    __device__ __forceinline__ void store_partial(float *Mw, float *Lw, float *Aw) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (t == 0) {
+                Mw[8 * h + g] = m_run[h];
+                Lw[8 * h + g] = l_run[h];
+            }
+            const int ra = 8 * h + 2 * t, rb = ra + 1;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int d = DL * g + 2 * mt;
+                *reinterpret_cast<float2 *>(Aw + ra * D + d) = make_float2(acc[h][mt][0], acc[h][mt][2]);
+                *reinterpret_cast<float2 *>(Aw + rb * D + d) = make_float2(acc[h][mt][1], acc[h][mt][3]);
+            }
+        }
+    }
+
+    // f(row, d, v0, v1, first, m, l) for the rows that exist
+    template <typename Fn>
+    __device__ __forceinline__ void for_each_result(Fn &&f) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float ma, mb, la, lb;
+            int xa, xb;
+            row_values(m_run[h], ma, mb);
+            row_values(l_run[h], la, lb);
+            row_values(lim[h], xa, xb);
+            const int ra = 8 * h + 2 * t, rb = ra + 1;
+            const float ia = la > 0.f ? 1.f / la : 0.f, ib = lb > 0.f ? 1.f / lb : 0.f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int d = DL * g + 2 * mt;
+                if (xa >= 0) f(ra, d, acc[h][mt][0] * ia, acc[h][mt][2] * ia, g == 0 && mt == 0, ma, la);
+                if (xb >= 0) f(rb, d, acc[h][mt][1] * ib, acc[h][mt][3] * ib, g == 0 && mt == 0, mb, lb);
+            }
+        }
+    }
+};
+
 }  // namespace pa

@@ -77,6 +77,44 @@ cudaError_t reshape_and_cache_fp8(const void *k, const void *v, void *k_cache, v
                                   const float *k_scale, const float *v_scale,
                                   cudaStream_t st);
 
+// the cache write with per-head norms and the rotation by position in front
+// (pa_rope.cu); k_scale set: E4M3 caches.  Strides in elements.
+struct RopeParams {
+    void *q_out;
+    const void *q, *k, *v;
+    void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;           // [num_kv_heads], or nullptr
+    const void *q_weight, *k_weight;          // [head_dim], or nullptr: no norm
+    const float *rope_table;                  // [num_positions][rot_dim]: cos, then sin
+    const int64_t *positions, *slot_mapping;  // [num_tokens]
+    int64_t num_tokens, num_positions, num_slots;
+    int64_t q_stride, q_out_stride, k_stride, v_stride;
+    float eps;
+    int num_heads, num_kv_heads, head_dim, rot_dim, interleaved;
+    int parts, part_heads;                    // warps per token, heads of each
+    unsigned int *err;
+};
+cudaError_t rope_and_cache(const RopeParams &p, int dtype, cudaStream_t st);
+
+// verification of drafted tokens (pa_verify.cu); strides in elements
+struct VerifyParams {
+    int32_t *out_tokens, *num_accepted;       // [num_seqs][max_query_len], [num_seqs]
+    const void *target, *draft;               // rows of the vocabulary; draft may be nullptr
+    const int32_t *tokens;                    // [num_rows]
+    const float *accept_u, *sample_u;         // [num_rows], [num_seqs]
+    const int32_t *query_start;               // [num_seqs + 1]
+    int64_t target_stride, draft_stride;
+    int num_seqs, num_rows, max_query_len, vocab;
+    unsigned int *err;
+};
+cudaError_t verify_drafts(const VerifyParams &p, int dtype, cudaStream_t st);
+
+// multi-token queries over E4M3 caches (q and out bf16 / f16)
+cudaError_t decode_multi_fp8_bf16(const DecodeParams &p, int D, int G, long long unit_bound,
+                                  int cluster, cudaStream_t st);
+cudaError_t decode_multi_fp8_f16(const DecodeParams &p, int D, int G, long long unit_bound,
+                                 int cluster, cudaStream_t st);
+
 // persistent decode over E4M3 caches (q and out bf16 / f16); partial as above
 cudaError_t decode_fp8_bf16(const DecodeParams &p, int D, int G, bool partial,
                             long long unit_bound, int cluster, cudaStream_t st);

@@ -301,14 +301,15 @@ __host__ __device__ constexpr int persistent_warps() {
 
 // Blocks per SM the kernel is built for: eight warps of 16-bit tiles per SM
 // (one block of eight or two of four); E4M3 tiles are half the bytes, so
-// three blocks of four fit and hide more latency.
-template <typename KV, int NW>
+// three blocks of four fit and hide more latency (two for multi-token queries,
+// whose partials of 16 rows take the room of the third).
+template <typename KV, int NW, int MODE>
 __host__ __device__ constexpr int persistent_blocks_per_sm() {
-    return sizeof(KV) == 1 ? PA_F8_BLOCKS_PER_SM : (NW >= 8 ? 1 : 2);
+    return sizeof(KV) == 1 ? (MODE == MODE_MULTI ? 2 : PA_F8_BLOCKS_PER_SM) : (NW >= 8 ? 1 : 2);
 }
 
 template <typename T, typename KV, int D, int G, int NW, int S, int MODE>
-__global__ void __launch_bounds__(NW * 32, (persistent_blocks_per_sm<KV, NW>()))
+__global__ void __launch_bounds__(NW * 32, (persistent_blocks_per_sm<KV, NW, MODE>()))
 decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     constexpr bool TC = use_tc<T>();
     constexpr bool F8 = std::is_same<KV, e4m3>::value;
@@ -317,9 +318,9 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int ROWS = rows_of_mode(MODE, G);
     static_assert(!MQ || TC, "multi-token queries use the tensor-core path");
     static_assert(F8 || std::is_same<KV, T>::value, "cache type");
-    static_assert(!F8 || (TC && !MQ), "E4M3 caches: 16-bit q, one query token per sequence");
+    static_assert(!F8 || TC, "E4M3 caches: 16-bit q");
     using W = std::conditional_t<
-        F8, WarpAttnF8<T, D, G>,
+        F8, std::conditional_t<MQ, WarpAttnF8x16<T, D>, WarpAttnF8<T, D, G>>,
         std::conditional_t<MQ, WarpAttnTC16<T, D>,
                            std::conditional_t<TC, WarpAttnTC<T, D, G>, WarpAttn<T, D, G>>>>;
     using Lay = PersistentLayout<T, KV, D, G, NW, S, MODE>;
@@ -923,6 +924,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                            (long long)(u.j * G + r % G) * D;
                 };
                 wa.load_q(qrow(r_lo), qrow(r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
+                if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
             } else {
                 auto qptr = [&](int q) {
                     const UnitRec &u = units[q];
@@ -961,7 +963,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                         __syncwarp();
                     }
                 }
-                if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), p.scale_log2);
+                if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
                 else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
             } else {
                 wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
@@ -1003,7 +1005,7 @@ template <typename T, typename KV, int D, int G, int MODE, int NW>
 __host__ __device__ constexpr int persistent_stages() {
     int s = PA_STAGE_KB * 1024 / (int)(2 * 16 * D * sizeof(KV));
     s = s < 2 ? 2 : (s > 6 ? 6 : s);
-    const size_t cap = (size_t)(227 / persistent_blocks_per_sm<KV, NW>()) * 1024;
+    const size_t cap = (size_t)(227 / persistent_blocks_per_sm<KV, NW, MODE>()) * 1024;
     while (s > 2 && PersistentLayout<T, KV, D, G, NW, 0, MODE>::BYTES +
                             (size_t)NW * s * (2 * 16 * D * sizeof(KV) + 8) > cap)
         --s;

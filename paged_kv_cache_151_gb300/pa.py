@@ -27,6 +27,8 @@ PA_DEVERR_BLOCK_ID = 0x1
 PA_DEVERR_SEQ_LEN = 0x2
 PA_DEVERR_SLOT = 0x4
 PA_DEVERR_TIMEOUT = 0x8
+PA_DEVERR_POSITION = 0x10
+PA_DEVERR_TOKEN = 0x20
 
 
 class PAError(RuntimeError):
@@ -87,6 +89,18 @@ def load():
         lib.pa_decode_fp8.argtypes = dec8 + [P]
         lib.pa_decode_partitioned_fp8.restype = ctypes.c_int
         lib.pa_decode_partitioned_fp8.argtypes = dec8 + [i32, i32, P, sz, P]
+        lib.pa_decode_multi_fp8.restype = ctypes.c_int
+        lib.pa_decode_multi_fp8.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
+                                            i32, i64, i32, i32, i64, f32, i32, P]
+        rope = [P, P, f32, P, i64, i32, i32, P, P, i64, i32, i32, i32, i64, i64, i64, i64, i64,
+                i32, i32, P]
+        lib.pa_rope_and_cache.restype = ctypes.c_int
+        lib.pa_rope_and_cache.argtypes = [P, P, P, P, P, P] + rope
+        lib.pa_rope_and_cache_fp8.restype = ctypes.c_int
+        lib.pa_rope_and_cache_fp8.argtypes = [P, P, P, P, P, P, P, P] + rope
+        lib.pa_verify_drafts.restype = ctypes.c_int
+        lib.pa_verify_drafts.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i64, i64,
+                                         i32, P]
         lib.pa_copy_blocks.restype = ctypes.c_int
         lib.pa_copy_blocks.argtypes = [ctypes.POINTER(ctypes.c_void_p), i32, P, i64, i64, i64,
                                        P]
@@ -153,6 +167,83 @@ def pa_reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, stream=None):
         slot_mapping.data_ptr(), k.shape[0], Hkv, D, k.stride(0), v.stride(0), N, bs,
         _DTYPE[k.dtype], _stream(stream))
     _check("pa_reshape_and_cache", rc)
+
+
+def _rope_args(q_out, q, k, v, Hkv, D, rope_table, positions, slot_mapping, q_weight, k_weight,
+               eps, interleaved):
+    """Checks shared by the rotating cache writes; the arguments after the caches."""
+    tensors = [("k", k), ("v", v), ("slot_mapping", slot_mapping)]
+    tensors += [(n, t) for n, t in (("q", q), ("q_out", q_out), ("rope_table", rope_table),
+                                    ("positions", positions), ("q_weight", q_weight),
+                                    ("k_weight", k_weight)) if t is not None]
+    for n, t in tensors:
+        _dev(t, n)
+    if k.dim() != 3 or k.shape != v.shape or tuple(k.shape[1:]) != (Hkv, D):
+        raise ValueError("k and v must be [num_tokens, num_kv_heads, head_dim]")
+    if k.dtype not in _DTYPE or v.dtype != k.dtype:
+        raise ValueError("k and v must share a dtype in {float32, bfloat16, float16}")
+    T = k.shape[0]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    heads = [("k", k), ("v", v)]
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [num_tokens, num_heads, head_dim]")
+        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError("q, q_out and k must share a dtype")
+        heads += [("q", q), ("q_out", q_out)]
+    for n, t in heads:
+        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+            raise ValueError(f"{n} must have contiguous heads")
+    for n, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None and (t.dtype != k.dtype or t.shape != (D,) or not t.is_contiguous()):
+            raise ValueError(f"{n} must be a contiguous [head_dim] of k's dtype")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or \
+            not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 [num_tokens]")
+    R = npos = 0
+    if rope_table is not None:
+        if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or \
+                not rope_table.is_contiguous():
+            raise ValueError("rope_table must be a contiguous float32 [num_positions, rot_dim]")
+        npos, R = rope_table.shape
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        if positions.dtype != torch.int64 or positions.shape != (T,) or \
+                not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int64 [num_tokens]")
+    H = 0 if q is None else q.shape[1]
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    def stride(t, n):          # a single token's stride is never used
+        return n * D if t is None or T <= 1 else t.stride(0)
+    front = [ptr(q_out), ptr(q), k.data_ptr(), v.data_ptr()]
+    rest = [ptr(q_weight), ptr(k_weight), float(eps), ptr(rope_table), npos, R,
+            int(bool(interleaved)), ptr(positions), slot_mapping.data_ptr(), T, H, Hkv, D,
+            stride(q, H), stride(q_out, H), stride(k, Hkv), stride(v, Hkv)]
+    return front, rest
+
+
+def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, rope_table, positions, slot_mapping,
+                      q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None):
+    """The cache write with per-head norms and the rotation in front: q ([T,
+    H_q, D]) into ``q_out`` (which may be q), k and v ([T, H_kv, D]) into their
+    slots.  ``rope_table`` is float32 [num_positions, rot_dim], cos of the
+    rot_dim / 2 pairs and then their sin, ``positions`` int64 [T]; None for both:
+    no rotation.  ``q_weight`` and ``k_weight`` ([D]; None: no norm) are the
+    norms' weights.  q and q_out may be None: keys and values only."""
+    _dev(k_cache, "k_cache")
+    _dev(v_cache, "v_cache")
+    N, Hkv, bs, D = _cache_dims(k_cache, v_cache)
+    front, rest = _rope_args(q_out, q, k, v, Hkv, D, rope_table, positions, slot_mapping,
+                             q_weight, k_weight, eps, interleaved)
+    if k.dtype != k_cache.dtype:
+        raise ValueError("k, v and the caches must share a dtype")
+    rc = load().pa_rope_and_cache(*front, k_cache.data_ptr(), v_cache.data_ptr(), *rest, N, bs,
+                                  _DTYPE[k.dtype], _stream(stream))
+    _check("pa_rope_and_cache", rc)
 
 
 def _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens):
@@ -309,6 +400,55 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, seq_lens, query_star
     _check("pa_decode_multi", rc)
 
 
+def pa_verify_drafts(out_tokens, num_accepted, target_probs, draft_probs, tokens,
+                     accept_uniform, sample_uniform, query_start, max_query_len, stream=None):
+    """Accept or reject drafted tokens: sequence s owns rows query_start[s] ..
+    query_start[s+1]-1 of ``target_probs`` ([T, V]), ``draft_probs`` ([T, V], or
+    None), ``tokens`` (int32 [T]) and ``accept_uniform`` (float32 [T]); its
+    first row is the token accepted last, the others its drafts.
+    ``out_tokens`` (int32 [B, max_query_len]) receives the accepted drafts, the
+    token drawn with ``sample_uniform`` (float32 [B]) and then -1,
+    ``num_accepted`` (int32 [B]) the number accepted."""
+    for n, t in (("out_tokens", out_tokens), ("num_accepted", num_accepted),
+                 ("target_probs", target_probs), ("tokens", tokens),
+                 ("accept_uniform", accept_uniform), ("sample_uniform", sample_uniform),
+                 ("query_start", query_start)):
+        _dev(t, n)
+    if target_probs.dim() != 2 or target_probs.dtype not in _DTYPE:
+        raise ValueError("target_probs must be [num_rows, vocab] in {float32, bfloat16, float16}")
+    T, V = target_probs.shape
+    probs = [("target_probs", target_probs)]
+    if draft_probs is not None:
+        _dev(draft_probs, "draft_probs")
+        if draft_probs.shape != target_probs.shape or draft_probs.dtype != target_probs.dtype:
+            raise ValueError("draft_probs must be shaped and typed like target_probs")
+        probs.append(("draft_probs", draft_probs))
+    for n, t in probs:
+        if t.numel() and V > 1 and t.stride(1) != 1:
+            raise ValueError(f"{n} must have contiguous rows")
+    if num_accepted.dtype != torch.int32 or num_accepted.dim() != 1 or \
+            not num_accepted.is_contiguous():
+        raise ValueError("num_accepted must be a contiguous int32 [num_seqs]")
+    B, mq = num_accepted.shape[0], int(max_query_len)
+    for n, t, dt, shape in (("out_tokens", out_tokens, torch.int32, (B, mq)),
+                            ("tokens", tokens, torch.int32, (T,)),
+                            ("accept_uniform", accept_uniform, torch.float32, (T,)),
+                            ("sample_uniform", sample_uniform, torch.float32, (B,)),
+                            ("query_start", query_start, torch.int32, (B + 1,))):
+        if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous {dt} {list(shape)}")
+
+    def stride(t):             # a single row's stride is never used
+        return V if t is None or T <= 1 else t.stride(0)
+    rc = load().pa_verify_drafts(
+        out_tokens.data_ptr(), num_accepted.data_ptr(), target_probs.data_ptr(),
+        None if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
+        accept_uniform.data_ptr(), sample_uniform.data_ptr(), query_start.data_ptr(), B, T, mq,
+        V, stride(target_probs), stride(draft_probs), _DTYPE[target_probs.dtype],
+        _stream(stream))
+    _check("pa_verify_drafts", rc)
+
+
 def pa_copy_blocks(caches, block_mapping, stream=None):
     """Copy-on-write block copies: for every (src, dst) row of ``block_mapping``
     (CUDA int64 [P, 2]) copy block src to block dst in every tensor of
@@ -382,6 +522,20 @@ def pa_reshape_and_cache_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapp
     _check("pa_reshape_and_cache_fp8", rc)
 
 
+def pa_rope_and_cache_fp8(q_out, q, k, v, k_cache, v_cache, k_scale, v_scale, rope_table,
+                          positions, slot_mapping, q_weight=None, k_weight=None, eps=1e-6,
+                          interleaved=False, stream=None):
+    """pa_rope_and_cache into E4M3 caches, as E4M3(x / scale[j]); q_out keeps q's
+    dtype."""
+    N, Hkv, bs, D = _fp8_cache_dims(k_cache, v_cache, k_scale, v_scale)
+    front, rest = _rope_args(q_out, q, k, v, Hkv, D, rope_table, positions, slot_mapping,
+                             q_weight, k_weight, eps, interleaved)
+    rc = load().pa_rope_and_cache_fp8(*front, k_cache.data_ptr(), v_cache.data_ptr(),
+                                      k_scale.data_ptr(), v_scale.data_ptr(), *rest, N, bs,
+                                      _DTYPE[k.dtype], _stream(stream))
+    _check("pa_rope_and_cache_fp8", rc)
+
+
 def _decode_fp8_args(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens):
     for n, t in (("out", out), ("q", q), ("block_tables", block_tables),
                  ("seq_lens", seq_lens)):
@@ -431,6 +585,39 @@ def pa_decode_partitioned_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_
     _check("pa_decode_partitioned_fp8", rc)
 
 
+def pa_decode_multi_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                        query_start, max_query_len, scale, num_kv_heads, stream=None):
+    """pa_decode_multi over E4M3 caches: several new tokens per sequence, causal
+    among themselves."""
+    for n, t in (("out", out), ("q", q), ("block_tables", block_tables),
+                 ("seq_lens", seq_lens), ("query_start", query_start)):
+        _dev(t, n)
+    N, Hkv, bs, D = _fp8_cache_dims(k_cache, v_cache, k_scale, v_scale)
+    if num_kv_heads != Hkv:
+        raise ValueError("num_kv_heads does not match the cache")
+    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or q.stride(1) != D:
+        raise ValueError("q must be [num_rows, num_heads, head_dim] with contiguous heads")
+    if out.shape != q.shape or not out.is_contiguous() or out.dtype != q.dtype:
+        raise ValueError("out must be a contiguous tensor shaped and typed like q")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16")
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 [num_seqs]")
+    B = seq_lens.shape[0]
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks]")
+    if query_start.dtype != torch.int32 or query_start.shape != (B + 1,) or \
+            not query_start.is_contiguous():
+        raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
+    rc = load().pa_decode_multi_fp8(
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        query_start.data_ptr(), B, q.shape[0], int(max_query_len), q.shape[1], Hkv, D, N, bs,
+        block_tables.shape[1], q.stride(0), float(scale), _DTYPE[q.dtype], _stream(stream))
+    _check("pa_decode_multi_fp8", rc)
+
+
 def workspace_views(workspace, num_seqs, num_heads, head_dim, max_seq_len, partition_size):
     """(o_part, m_part, l_part) fp32 views of a partitioned-decode workspace,
     following the layout documented in include/pa.h."""
@@ -469,7 +656,9 @@ __all__ = [
     "pa_decode_partitioned_noalloc", "PA_NOALLOC_SCRATCH_BYTES",
     "pa_decode_cascade", "pa_decode_cascade_workspace_size",
     "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_partitioned_fp8",
+    "pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_decode_multi_fp8", "pa_verify_drafts",
     "pa_copy_blocks",
     "pa_device_error", "workspace_views",
     "PA_DEVERR_BLOCK_ID", "PA_DEVERR_SEQ_LEN", "PA_DEVERR_SLOT", "PA_DEVERR_TIMEOUT",
+    "PA_DEVERR_POSITION", "PA_DEVERR_TOKEN",
 ]
