@@ -137,6 +137,42 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The checks of a call of a dozen tensors cost more than a small kernel runs, so
+# the calls below ask each tensor for its device with one method call, and take
+# the current stream's handle without building a stream object where torch
+# offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(names, tensors):
+    """The current device, on which every tensor has to be."""
+    try:
+        devs = {t.get_device() for t in tensors}
+    except AttributeError:
+        devs = ()
+    if len(devs) == 1:
+        dev = devs.pop()
+        if dev >= 0 and dev == torch.cuda.current_device():
+            return dev
+    for n, t in zip(names.split(), tensors):
+        _dev(t, n)
+    raise ValueError("tensors are not on the current device")
+
+
+def _stream_of(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _heads(t, n, D):
+    """The token stride of t [T, heads, D], whose heads have to be contiguous."""
+    st = t.stride()
+    if (st[2] != 1 or (st[1] != D and t.shape[1] > 1)) and t.numel():
+        raise ValueError(f"{n} must have contiguous heads")
+    return st[0]
+
+
 def _cache_dims(k_cache: torch.Tensor, v_cache: torch.Tensor):
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
         raise ValueError("caches must both be [num_blocks, num_kv_heads, block_size, head_dim]")
@@ -169,61 +205,77 @@ def pa_reshape_and_cache(k, v, k_cache, v_cache, slot_mapping, stream=None):
     _check("pa_reshape_and_cache", rc)
 
 
-def _rope_args(q_out, q, k, v, Hkv, D, rope_table, positions, slot_mapping, q_weight, k_weight,
-               eps, interleaved):
-    """Checks shared by the rotating cache writes; the arguments after the caches."""
-    tensors = [("k", k), ("v", v), ("slot_mapping", slot_mapping)]
-    tensors += [(n, t) for n, t in (("q", q), ("q_out", q_out), ("rope_table", rope_table),
-                                    ("positions", positions), ("q_weight", q_weight),
-                                    ("k_weight", k_weight)) if t is not None]
-    for n, t in tensors:
-        _dev(t, n)
-    if k.dim() != 3 or k.shape != v.shape or tuple(k.shape[1:]) != (Hkv, D):
-        raise ValueError("k and v must be [num_tokens, num_kv_heads, head_dim]")
-    if k.dtype not in _DTYPE or v.dtype != k.dtype:
+_ROPE_NAMES = ("k v k_cache v_cache slot_mapping q_out q rope_table positions q_weight k_weight "
+               "k_scale v_scale")
+
+
+def _rope(fn, q_out, q, k, v, k_cache, v_cache, scales, rope_table, positions, slot_mapping,
+          q_weight, k_weight, eps, interleaved, stream):
+    """The rotating cache writes: checks, and the call of ``fn``; ``scales`` are
+    the arguments of the E4M3 form."""
+    dev = _here(_ROPE_NAMES, (k, v, k_cache, v_cache, slot_mapping,
+                              *[k if t is None else t for t in
+                                (q_out, q, rope_table, positions, q_weight, k_weight)], *scales))
+    N, Hkv, bs, D = (_fp8_caches(k_cache, v_cache, *scales) if scales
+                     else _cache_dims(k_cache, v_cache))
+    dt = k.dtype
+    code = _DTYPE.get(dt)
+    if code is None or v.dtype is not dt:
         raise ValueError("k and v must share a dtype in {float32, bfloat16, float16}")
-    T = k.shape[0]
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
-    heads = [("k", k), ("v", v)]
-    if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape:
+    if not scales and k_cache.dtype is not dt:
+        raise ValueError("k, v and the caches must share a dtype")
+    shape = k.shape
+    if len(shape) != 3 or shape != v.shape or shape[1] != Hkv or shape[2] != D:
+        raise ValueError("k and v must be [num_tokens, num_kv_heads, head_dim]")
+    T = shape[0]
+    k_st, v_st = _heads(k, "k", D), _heads(v, "v", D)
+    if q is None and q_out is None:
+        H = q_st = o_st = 0
+        q_ptr = o_ptr = None
+    else:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out come together")
+        qs = q.shape
+        if len(qs) != 3 or qs[0] != T or qs[2] != D or q_out.shape != qs:
             raise ValueError("q and q_out must be [num_tokens, num_heads, head_dim]")
-        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+        if q.dtype is not dt or q_out.dtype is not dt:
             raise ValueError("q, q_out and k must share a dtype")
-        heads += [("q", q), ("q_out", q_out)]
-    for n, t in heads:
-        if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
-            raise ValueError(f"{n} must have contiguous heads")
-    for n, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and (t.dtype != k.dtype or t.shape != (D,) or not t.is_contiguous()):
-            raise ValueError(f"{n} must be a contiguous [head_dim] of k's dtype")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or \
+        H, q_st, o_st = qs[1], _heads(q, "q", D), _heads(q_out, "q_out", D)
+        q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
+    if T <= 1:                 # a single token's stride is never used
+        k_st = v_st = Hkv * D
+        q_st = o_st = H * D
+    qw = kw = None
+    if q_weight is not None:
+        if q_weight.dtype is not dt or q_weight.shape != (D,) or not q_weight.is_contiguous():
+            raise ValueError("q_weight must be a contiguous [head_dim] of k's dtype")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.dtype is not dt or k_weight.shape != (D,) or not k_weight.is_contiguous():
+            raise ValueError("k_weight must be a contiguous [head_dim] of k's dtype")
+        kw = k_weight.data_ptr()
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,) or \
             not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be a contiguous int64 [num_tokens]")
-    R = npos = 0
+    P = R = 0
+    tab = pos = None
     if rope_table is not None:
-        if rope_table.dtype != torch.float32 or rope_table.dim() != 2 or \
+        if rope_table.dtype is not torch.float32 or rope_table.dim() != 2 or \
                 not rope_table.is_contiguous():
             raise ValueError("rope_table must be a contiguous float32 [num_positions, rot_dim]")
-        npos, R = rope_table.shape
         if positions is None:
             raise ValueError("a rotation needs positions")
-        if positions.dtype != torch.int64 or positions.shape != (T,) or \
+        if positions.dtype is not torch.int64 or positions.shape != (T,) or \
                 not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int64 [num_tokens]")
-    H = 0 if q is None else q.shape[1]
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    def stride(t, n):          # a single token's stride is never used
-        return n * D if t is None or T <= 1 else t.stride(0)
-    front = [ptr(q_out), ptr(q), k.data_ptr(), v.data_ptr()]
-    rest = [ptr(q_weight), ptr(k_weight), float(eps), ptr(rope_table), npos, R,
-            int(bool(interleaved)), ptr(positions), slot_mapping.data_ptr(), T, H, Hkv, D,
-            stride(q, H), stride(q_out, H), stride(k, Hkv), stride(v, Hkv)]
-    return front, rest
+        P, R = rope_table.shape
+        tab, pos = rope_table.data_ptr(), positions.data_ptr()
+    rc = fn(o_ptr, q_ptr, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            *[t.data_ptr() for t in scales], qw, kw, eps, tab, P, R, 1 if interleaved else 0, pos,
+            slot_mapping.data_ptr(), T, H, Hkv, D, q_st, o_st, k_st, v_st, N, bs, code,
+            _stream_of(stream, dev))
+    if rc:
+        raise PAError(fn.__name__, rc)
 
 
 def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, rope_table, positions, slot_mapping,
@@ -234,16 +286,8 @@ def pa_rope_and_cache(q_out, q, k, v, k_cache, v_cache, rope_table, positions, s
     rot_dim / 2 pairs and then their sin, ``positions`` int64 [T]; None for both:
     no rotation.  ``q_weight`` and ``k_weight`` ([D]; None: no norm) are the
     norms' weights.  q and q_out may be None: keys and values only."""
-    _dev(k_cache, "k_cache")
-    _dev(v_cache, "v_cache")
-    N, Hkv, bs, D = _cache_dims(k_cache, v_cache)
-    front, rest = _rope_args(q_out, q, k, v, Hkv, D, rope_table, positions, slot_mapping,
-                             q_weight, k_weight, eps, interleaved)
-    if k.dtype != k_cache.dtype:
-        raise ValueError("k, v and the caches must share a dtype")
-    rc = load().pa_rope_and_cache(*front, k_cache.data_ptr(), v_cache.data_ptr(), *rest, N, bs,
-                                  _DTYPE[k.dtype], _stream(stream))
-    _check("pa_rope_and_cache", rc)
+    _rope((_lib or load()).pa_rope_and_cache, q_out, q, k, v, k_cache, v_cache, (), rope_table,
+          positions, slot_mapping, q_weight, k_weight, eps, interleaved, stream)
 
 
 def _decode_args(out, q, k_cache, v_cache, block_tables, seq_lens):
@@ -409,44 +453,55 @@ def pa_verify_drafts(out_tokens, num_accepted, target_probs, draft_probs, tokens
     ``out_tokens`` (int32 [B, max_query_len]) receives the accepted drafts, the
     token drawn with ``sample_uniform`` (float32 [B]) and then -1,
     ``num_accepted`` (int32 [B]) the number accepted."""
-    for n, t in (("out_tokens", out_tokens), ("num_accepted", num_accepted),
-                 ("target_probs", target_probs), ("tokens", tokens),
-                 ("accept_uniform", accept_uniform), ("sample_uniform", sample_uniform),
-                 ("query_start", query_start)):
-        _dev(t, n)
-    if target_probs.dim() != 2 or target_probs.dtype not in _DTYPE:
+    dev = _here("out_tokens num_accepted target_probs draft_probs tokens accept_uniform "
+                "sample_uniform query_start",
+                (out_tokens, num_accepted, target_probs,
+                 target_probs if draft_probs is None else draft_probs, tokens, accept_uniform,
+                 sample_uniform, query_start))
+    dt, shape = target_probs.dtype, target_probs.shape
+    code = _DTYPE.get(dt)
+    if code is None or len(shape) != 2:
         raise ValueError("target_probs must be [num_rows, vocab] in {float32, bfloat16, float16}")
-    T, V = target_probs.shape
-    probs = [("target_probs", target_probs)]
+    T, V = shape
+    t_st, one = target_probs.stride()
+    if one != 1 and V > 1 and T:
+        raise ValueError("target_probs must have contiguous rows")
+    d_ptr, d_st = None, V
     if draft_probs is not None:
-        _dev(draft_probs, "draft_probs")
-        if draft_probs.shape != target_probs.shape or draft_probs.dtype != target_probs.dtype:
+        if draft_probs.shape != shape or draft_probs.dtype is not dt:
             raise ValueError("draft_probs must be shaped and typed like target_probs")
-        probs.append(("draft_probs", draft_probs))
-    for n, t in probs:
-        if t.numel() and V > 1 and t.stride(1) != 1:
-            raise ValueError(f"{n} must have contiguous rows")
-    if num_accepted.dtype != torch.int32 or num_accepted.dim() != 1 or \
+        d_st, one = draft_probs.stride()
+        if one != 1 and V > 1 and T:
+            raise ValueError("draft_probs must have contiguous rows")
+        d_ptr = draft_probs.data_ptr()
+    if T <= 1:                 # a single row's stride is never used
+        t_st = d_st = V
+    i32, f32 = torch.int32, torch.float32
+    if num_accepted.dtype is not i32 or num_accepted.dim() != 1 or \
             not num_accepted.is_contiguous():
         raise ValueError("num_accepted must be a contiguous int32 [num_seqs]")
-    B, mq = num_accepted.shape[0], int(max_query_len)
-    for n, t, dt, shape in (("out_tokens", out_tokens, torch.int32, (B, mq)),
-                            ("tokens", tokens, torch.int32, (T,)),
-                            ("accept_uniform", accept_uniform, torch.float32, (T,)),
-                            ("sample_uniform", sample_uniform, torch.float32, (B,)),
-                            ("query_start", query_start, torch.int32, (B + 1,))):
-        if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous {dt} {list(shape)}")
-
-    def stride(t):             # a single row's stride is never used
-        return V if t is None or T <= 1 else t.stride(0)
-    rc = load().pa_verify_drafts(
-        out_tokens.data_ptr(), num_accepted.data_ptr(), target_probs.data_ptr(),
-        None if draft_probs is None else draft_probs.data_ptr(), tokens.data_ptr(),
-        accept_uniform.data_ptr(), sample_uniform.data_ptr(), query_start.data_ptr(), B, T, mq,
-        V, stride(target_probs), stride(draft_probs), _DTYPE[target_probs.dtype],
-        _stream(stream))
-    _check("pa_verify_drafts", rc)
+    B = num_accepted.shape[0]
+    if out_tokens.dtype is not i32 or out_tokens.shape != (B, max_query_len) or \
+            not out_tokens.is_contiguous():
+        raise ValueError("out_tokens must be a contiguous int32 [num_seqs, max_query_len]")
+    if tokens.dtype is not i32 or tokens.shape != (T,) or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 [num_rows]")
+    if accept_uniform.dtype is not f32 or accept_uniform.shape != (T,) or \
+            not accept_uniform.is_contiguous():
+        raise ValueError("accept_uniform must be a contiguous float32 [num_rows]")
+    if sample_uniform.dtype is not f32 or sample_uniform.shape != (B,) or \
+            not sample_uniform.is_contiguous():
+        raise ValueError("sample_uniform must be a contiguous float32 [num_seqs]")
+    if query_start.dtype is not i32 or query_start.shape != (B + 1,) or \
+            not query_start.is_contiguous():
+        raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
+    rc = (_lib or load()).pa_verify_drafts(
+        out_tokens.data_ptr(), num_accepted.data_ptr(), target_probs.data_ptr(), d_ptr,
+        tokens.data_ptr(), accept_uniform.data_ptr(), sample_uniform.data_ptr(),
+        query_start.data_ptr(), B, T, max_query_len, V, t_st, d_st, code,
+        _stream_of(stream, dev))
+    if rc:
+        raise PAError("pa_verify_drafts", rc)
 
 
 def pa_copy_blocks(caches, block_mapping, stream=None):
@@ -482,21 +537,31 @@ def pa_copy_blocks(caches, block_mapping, stream=None):
 _FP8_TYPES = tuple(t for t in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if t)
 
 
-def _fp8_cache_dims(k_cache, v_cache, k_scale, v_scale):
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
-                 ("v_scale", v_scale)):
-        _dev(t, n)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+def _fp8_caches(k_cache, v_cache, k_scale, v_scale):
+    """The shape of E4M3 caches, checked together with their scales (not their
+    device)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape:
         raise ValueError("caches must both be [num_blocks, num_kv_heads, block_size, head_dim]")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("caches must be contiguous")
     if k_cache.dtype not in _FP8_TYPES or v_cache.dtype not in _FP8_TYPES:
         raise ValueError("FP8 caches hold E4M3 codes (uint8 or float8_e4m3fn tensors)")
-    Hkv = k_cache.shape[1]
-    for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype != torch.float32 or t.shape != (Hkv,) or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous float32 [num_kv_heads]")
-    return k_cache.shape
+    Hkv = shape[1]
+    if k_scale.dtype is not torch.float32 or k_scale.shape != (Hkv,) or \
+            not k_scale.is_contiguous():
+        raise ValueError("k_scale must be a contiguous float32 [num_kv_heads]")
+    if v_scale.dtype is not torch.float32 or v_scale.shape != (Hkv,) or \
+            not v_scale.is_contiguous():
+        raise ValueError("v_scale must be a contiguous float32 [num_kv_heads]")
+    return shape
+
+
+def _fp8_cache_dims(k_cache, v_cache, k_scale, v_scale):
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
+                 ("v_scale", v_scale)):
+        _dev(t, n)
+    return _fp8_caches(k_cache, v_cache, k_scale, v_scale)
 
 
 def pa_reshape_and_cache_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping,
@@ -527,13 +592,9 @@ def pa_rope_and_cache_fp8(q_out, q, k, v, k_cache, v_cache, k_scale, v_scale, ro
                           interleaved=False, stream=None):
     """pa_rope_and_cache into E4M3 caches, as E4M3(x / scale[j]); q_out keeps q's
     dtype."""
-    N, Hkv, bs, D = _fp8_cache_dims(k_cache, v_cache, k_scale, v_scale)
-    front, rest = _rope_args(q_out, q, k, v, Hkv, D, rope_table, positions, slot_mapping,
-                             q_weight, k_weight, eps, interleaved)
-    rc = load().pa_rope_and_cache_fp8(*front, k_cache.data_ptr(), v_cache.data_ptr(),
-                                      k_scale.data_ptr(), v_scale.data_ptr(), *rest, N, bs,
-                                      _DTYPE[k.dtype], _stream(stream))
-    _check("pa_rope_and_cache_fp8", rc)
+    _rope((_lib or load()).pa_rope_and_cache_fp8, q_out, q, k, v, k_cache, v_cache,
+          (k_scale, v_scale), rope_table, positions, slot_mapping, q_weight, k_weight, eps,
+          interleaved, stream)
 
 
 def _decode_fp8_args(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens):
@@ -589,33 +650,37 @@ def pa_decode_multi_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables
                         query_start, max_query_len, scale, num_kv_heads, stream=None):
     """pa_decode_multi over E4M3 caches: several new tokens per sequence, causal
     among themselves."""
-    for n, t in (("out", out), ("q", q), ("block_tables", block_tables),
-                 ("seq_lens", seq_lens), ("query_start", query_start)):
-        _dev(t, n)
-    N, Hkv, bs, D = _fp8_cache_dims(k_cache, v_cache, k_scale, v_scale)
+    dev = _here("out q k_cache v_cache k_scale v_scale block_tables seq_lens query_start",
+                (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, query_start))
+    N, Hkv, bs, D = _fp8_caches(k_cache, v_cache, k_scale, v_scale)
     if num_kv_heads != Hkv:
         raise ValueError("num_kv_heads does not match the cache")
-    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or q.stride(1) != D:
+    shape, st = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != D or st[2] != 1 or st[1] != D:
         raise ValueError("q must be [num_rows, num_heads, head_dim] with contiguous heads")
-    if out.shape != q.shape or not out.is_contiguous() or out.dtype != q.dtype:
+    dt = q.dtype
+    if out.shape != shape or not out.is_contiguous() or out.dtype is not dt:
         raise ValueError("out must be a contiguous tensor shaped and typed like q")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError("q must be bfloat16 or float16")
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+    i32 = torch.int32
+    if seq_lens.dtype is not i32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 [num_seqs]")
     B = seq_lens.shape[0]
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or \
-            block_tables.shape[0] != B or not block_tables.is_contiguous():
+    tables = block_tables.shape
+    if block_tables.dtype is not i32 or len(tables) != 2 or tables[0] != B or \
+            not block_tables.is_contiguous():
         raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks]")
-    if query_start.dtype != torch.int32 or query_start.shape != (B + 1,) or \
+    if query_start.dtype is not i32 or query_start.shape != (B + 1,) or \
             not query_start.is_contiguous():
         raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
-    rc = load().pa_decode_multi_fp8(
+    rc = (_lib or load()).pa_decode_multi_fp8(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-        query_start.data_ptr(), B, q.shape[0], int(max_query_len), q.shape[1], Hkv, D, N, bs,
-        block_tables.shape[1], q.stride(0), float(scale), _DTYPE[q.dtype], _stream(stream))
-    _check("pa_decode_multi_fp8", rc)
+        query_start.data_ptr(), B, shape[0], max_query_len, shape[1], Hkv, D, N, bs, tables[1],
+        st[0], scale, _DTYPE[dt], _stream_of(stream, dev))
+    if rc:
+        raise PAError("pa_decode_multi_fp8", rc)
 
 
 def workspace_views(workspace, num_seqs, num_heads, head_dim, max_seq_len, partition_size):
