@@ -19,8 +19,9 @@
 // the second, or two neighbouring chunks when interleaved), so the rotation
 // needs no exchange between lanes and every access is 16 bytes; the D/16
 // lanes of a head add up its squares with shuffles.  The same lane keeps the
-// same pairs for every head of a token, so a warp loads its cos and sin once
-// and runs over several heads with them.
+// same pairs for every head of a token, so a warp folds weights, cos and sin
+// into four factors a pair once and runs over several heads with them, the
+// next heads' loads in flight.
 #include <type_traits>
 
 #include "pa_common.cuh"
@@ -71,13 +72,86 @@ __device__ __forceinline__ Raw8<T> narrow8(const float *x) {
     return r;
 }
 
-__device__ __forceinline__ uint2 e4m3_of8(const float *x, float scale) {
-    uint2 r;
-    r.x = e4m3x2_from_f32(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
-          (e4m3x2_from_f32(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)) << 16);
-    r.y = e4m3x2_from_f32(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale)) |
-          (e4m3x2_from_f32(__fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale)) << 16);
-    return r;
+// The codes of x[0..7] / scale as the plain cache write stores them.  x times
+// the reciprocal r is within 2^-22.4 of the quotient, so where it gives the
+// same code from 2^-21 below and above, that is the quotient's code (rounding
+// is monotonic); the rest -- about one element in 2^17 -- is divided.
+// r == 0: always divide.
+__device__ __forceinline__ uint2 e4m3_of8(const float *x, float scale, float r) {
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 a = mul2(make_float2(x[4 * h], x[4 * h + 1]), make_float2(r, r));
+        const float2 b = mul2(make_float2(x[4 * h + 2], x[4 * h + 3]), make_float2(r, r));
+        constexpr float DN = 1.f - 0x1p-21f, UP = 1.f + 0x1p-21f;
+        const float2 al = mul2(a, make_float2(DN, DN)), ah = mul2(a, make_float2(UP, UP));
+        const float2 bl = mul2(b, make_float2(DN, DN)), bh = mul2(b, make_float2(UP, UP));
+        lo[h] = e4m3x2_from_f32(al.x, al.y) | (e4m3x2_from_f32(bl.x, bl.y) << 16);
+        hi[h] = e4m3x2_from_f32(ah.x, ah.y) | (e4m3x2_from_f32(bh.x, bh.y) << 16);
+    }
+    if (lo[0] != hi[0] || lo[1] != hi[1] || r == 0.f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            lo[h] = e4m3x2_from_f32(__fdiv_rn(x[4 * h], scale), __fdiv_rn(x[4 * h + 1], scale)) |
+                    (e4m3x2_from_f32(__fdiv_rn(x[4 * h + 2], scale), __fdiv_rn(x[4 * h + 3], scale)) << 16);
+    }
+    return make_uint2(lo[0], lo[1]);
+}
+
+// A lane's two chunks of a head, and the factors of their pairs: with weights w
+// (1 without a norm) a' = f (a A1 - b A2), b' = f (b B1 + a B2), A1 = w_a cos,
+// A2 = w_b sin, B1 = w_b cos, B2 = w_a sin; a lane past the rotation only has
+// w_a = A1 and w_b = B1 (a product with 0 would spread infinities).  In the
+// interleaved layout the pairs are neighbours and factor e belongs to element
+// e: the partner of x[2i] is x[2i + 1].
+struct Factors {
+    float A1[8], A2[8], B1[8], B2[8];
+};
+
+template <typename T>
+__device__ __forceinline__ void load_factors(Factors &f, const void *weight, const float *tr,
+                                             int half, bool rot, bool live, bool interleaved, int ea,
+                                             int eb) {
+    float wa[8], wb[8], cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.f;
+    if (weight && live) {
+        const T *w = reinterpret_cast<const T *>(weight);
+        widen8<T>(load_raw8<T>(w + ea), wa);
+        widen8<T>(load_raw8<T>(w + eb), wb);
+    }
+    if (!rot) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f.A1[e] = wa[e];
+            f.B1[e] = wb[e];
+            f.A2[e] = f.B2[e] = 0.f;
+        }
+        return;
+    }
+    Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr)), cs);
+    Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr) + 1), cs + 4);
+    Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr + half)), sn);
+    Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr + half) + 1), sn + 4);
+    if (interleaved) {
+        // pair i of this lane: elements 2i, 2i + 1 of (a, b) taken as one run of 16
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = e >> 1;
+            f.A1[e] = wa[e] * cs[i];
+            f.A2[e] = wa[e ^ 1] * sn[i];
+            f.B1[e] = wb[e] * cs[4 + i];
+            f.B2[e] = wb[e ^ 1] * sn[4 + i];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f.A1[e] = wa[e] * cs[e];
+            f.A2[e] = wb[e] * sn[e];
+            f.B1[e] = wb[e] * cs[e];
+            f.B2[e] = wa[e] * sn[e];
+        }
+    }
 }
 
 // One warp per (token, part of its heads); L lanes per head, 32 / L heads at
@@ -92,8 +166,7 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_consta
     const unsigned t = item / (unsigned)p.parts, part = item - t * (unsigned)p.parts;
     if (t >= (unsigned)p.num_tokens) return;
     const int D = p.head_dim, R = p.rot_dim, H = p.num_heads, Hkv = p.num_kv_heads;
-    const int rows = H + 2 * Hkv;
-    const int h0 = (int)part * p.part_heads, h1 = min(rows, h0 + p.part_heads);
+    const int h0 = (int)part * p.part_heads, h1 = min(H + 2 * Hkv, h0 + p.part_heads);
     const bool lane_ok = l < D / 16;
 
     const int64_t slot = p.slot_mapping[t];
@@ -106,7 +179,7 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_consta
         return;
     }
 
-    // this lane's two chunks, and the cos and sin of their pairs
+    // this lane's two chunks
     const int RL = R / 16;                          // lanes that rotate
     const bool rot = l < RL;
     int ea, eb;
@@ -120,91 +193,110 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_consta
         ea = R + 8 * (l - RL);
         eb = ea + (D - R) / 2;
     }
-    float cs[8], sn[8];
-    if (rot) {
-        const float *tr = p.rope_table + pos * R + 8 * l;
-        Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr)), cs);
-        Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr) + 1), cs + 4);
-        tr += R / 2;
-        Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr)), sn);
-        Elem<float>::to_f32(__ldg(reinterpret_cast<const uint4 *>(tr) + 1), sn + 4);
-    }
-    const T *q = reinterpret_cast<const T *>(p.q) + (int64_t)t * p.q_stride;
-    const T *k = reinterpret_cast<const T *>(p.k) + (int64_t)t * p.k_stride;
-    const T *v = reinterpret_cast<const T *>(p.v) + (int64_t)t * p.v_stride;
-    T *qo = reinterpret_cast<T *>(p.q_out) + (int64_t)t * p.q_out_stride;
-    const int64_t crow = ((slot >> 4) * Hkv * 16 + (slot & 15)) * D;   // row of KV head 0 (block_size 16)
+    const float *tr = p.rope_table + pos * R + 8 * l;
+    const float inv_d = 1.f / (float)D;
 
-    for (int hb = h0; hb < h1; hb += HW) {
-        const int h = hb + sub;
-        const bool is_q = h < H, is_k = !is_q && h < H + Hkv;
-        const int j = is_q ? h : (is_k ? h - H : h - H - Hkv);
-        const bool live = lane_ok && h < h1 && (is_q || write);
-        const T *src = (is_q ? q : is_k ? k : v) + (int64_t)j * D;
-        Raw8<T> ra = {}, rb = {};
-        if (live) {
-            ra = load_raw8<T>(src + ea);
-            rb = load_raw8<T>(src + eb);
-        }
-        float a[8], b[8];
-        widen8<T>(ra, a);
-        widen8<T>(rb, b);
-        const T *w = reinterpret_cast<const T *>(is_q ? p.q_weight : is_k ? p.k_weight : nullptr);
-        if (p.q_weight || p.k_weight) {             // the sum needs every lane of the warp
-            float ss = 0.f;
+    // heads [lo, hi) of q (or of k): from src on, the result to put(head, a, b)
+    auto turn = [&](const T *src, int lo, int hi, const void *weight, auto &&put) {
+        if (lo >= hi) return;
+        Raw8<T> na = {}, nb = {};
+        auto fetch = [&](int h) {
+            if (lane_ok && h < hi) {
+                na = load_raw8<T>(src + (int64_t)h * D + ea);
+                nb = load_raw8<T>(src + (int64_t)h * D + eb);
+            }
+        };
+        fetch(lo + sub);
+        Factors f;
+        load_factors<T>(f, weight, tr, R / 2, rot, lane_ok, p.interleaved, ea, eb);
+        for (int hb = lo; hb < hi; hb += HW) {
+            const int h = hb + sub;
+            float a[8], b[8];
+            widen8<T>(na, a);
+            widen8<T>(nb, b);
+            fetch(h + HW);
+            float g = 1.f;
+            if (weight) {                           // the sum needs every lane of the warp
+                float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 x = make_float2(a[e], a[e + 1]), y = make_float2(b[e], b[e + 1]);
+                    ss = fma2(x, x, fma2(y, y, ss));
+                }
+                float sum = lane_ok ? ss.x + ss.y : 0.f;
 #pragma unroll
-            for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (w && live) {
-                const float f = 1.f / sqrtf(ss / (float)D + p.eps);
-                float wa[8], wb[8];
-                widen8<T>(load_raw8<T>(w + ea), wa);
-                widen8<T>(load_raw8<T>(w + eb), wb);
+                for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                g = rsqrtf(sum * inv_d + p.eps);
+            }
+            float ra[8], rb[8];
+            if (!rot) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    a[e] *= f * wa[e];
-                    b[e] *= f * wb[e];
+                    ra[e] = a[e] * f.A1[e] * g;
+                    rb[e] = b[e] * f.B1[e] * g;
                 }
-            }
-        }
-        if (rot && (is_q || is_k)) {
-            if (p.interleaved) {
+            } else if (p.interleaved) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], u = b[2 * i + 1];
-                    a[2 * i] = x * cs[i] - y * sn[i];
-                    a[2 * i + 1] = y * cs[i] + x * sn[i];
-                    b[2 * i] = z * cs[4 + i] - u * sn[4 + i];
-                    b[2 * i + 1] = u * cs[4 + i] + z * sn[4 + i];
+                for (int e = 0; e < 8; e += 2) {
+                    ra[e] = (a[e] * f.A1[e] - a[e + 1] * f.A2[e]) * g;
+                    ra[e + 1] = (a[e + 1] * f.A1[e + 1] + a[e] * f.A2[e + 1]) * g;
+                    rb[e] = (b[e] * f.B1[e] - b[e + 1] * f.B2[e]) * g;
+                    rb[e + 1] = (b[e + 1] * f.B1[e + 1] + b[e] * f.B2[e + 1]) * g;
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float x = a[e], y = b[e];
-                    a[e] = x * cs[e] - y * sn[e];
-                    b[e] = y * cs[e] + x * sn[e];
+                    ra[e] = (a[e] * f.A1[e] - b[e] * f.A2[e]) * g;
+                    rb[e] = (b[e] * f.B1[e] + a[e] * f.B2[e]) * g;
                 }
             }
+            if (lane_ok && h < hi) put(h, ra, rb);
         }
-        if (!live) continue;
-        if (is_q) {
-            T *dst = qo + (int64_t)j * D;
-            store_raw8<T>(dst + ea, narrow8<T>(a));
-            store_raw8<T>(dst + eb, narrow8<T>(b));
+    };
+
+    T *qo = reinterpret_cast<T *>(p.q_out) + (int64_t)t * p.q_out_stride;
+    turn(reinterpret_cast<const T *>(p.q) + (int64_t)t * p.q_stride, h0, min(h1, H), p.q_weight,
+         [&](int h, const float *a, const float *b) {
+             store_raw8<T>(qo + (int64_t)h * D + ea, narrow8<T>(a));
+             store_raw8<T>(qo + (int64_t)h * D + eb, narrow8<T>(b));
+         });
+    if (!write) return;
+
+    // a row of KV head j of this token (block_size 16); chunk ea of it
+    auto cache_at = [&](int j) { return (((slot >> 4) * Hkv + j) * 16 + (slot & 15)) * D; };
+    auto recip = [&](float sc) { return sc > 0x1p-100f && sc < 0x1p100f ? 1.f / sc : 0.f; };
+    turn(reinterpret_cast<const T *>(p.k) + (int64_t)t * p.k_stride, max(h0 - H, 0),
+         min(h1 - H, Hkv), p.k_weight, [&](int j, const float *a, const float *b) {
+             if constexpr (F8) {
+                 const float sc = __ldg(p.k_scale + j), r = recip(sc);
+                 unsigned char *dst = static_cast<unsigned char *>(p.k_cache) + cache_at(j);
+                 *reinterpret_cast<uint2 *>(dst + ea) = e4m3_of8(a, sc, r);
+                 *reinterpret_cast<uint2 *>(dst + eb) = e4m3_of8(b, sc, r);
+             } else {
+                 T *dst = static_cast<T *>(p.k_cache) + cache_at(j);
+                 store_raw8<T>(dst + ea, narrow8<T>(a));
+                 store_raw8<T>(dst + eb, narrow8<T>(b));
+             }
+         });
+    // v: as it is (16-byte chunks l and D/16 + l of the head's 8-element ones)
+    const T *v = reinterpret_cast<const T *>(p.v) + (int64_t)t * p.v_stride;
+    const int va = 8 * l, vb = D / 2 + 8 * l;
+    for (int j = max(h0 - H - Hkv, 0) + sub; j < h1 - H - Hkv; j += HW) {
+        if (!lane_ok) continue;
+        const Raw8<T> ra = load_raw8<T>(v + (int64_t)j * D + va);
+        const Raw8<T> rb = load_raw8<T>(v + (int64_t)j * D + vb);
+        if constexpr (F8) {
+            const float sc = __ldg(p.v_scale + j), r = recip(sc);
+            unsigned char *dst = static_cast<unsigned char *>(p.v_cache) + cache_at(j);
+            float a[8], b[8];
+            widen8<T>(ra, a);
+            widen8<T>(rb, b);
+            *reinterpret_cast<uint2 *>(dst + va) = e4m3_of8(a, sc, r);
+            *reinterpret_cast<uint2 *>(dst + vb) = e4m3_of8(b, sc, r);
         } else {
-            const int64_t at = crow + (int64_t)j * 16 * D;
-            void *cache = is_k ? p.k_cache : p.v_cache;
-            if constexpr (F8) {
-                const float sc = __ldg((is_k ? p.k_scale : p.v_scale) + j);
-                unsigned char *dst = static_cast<unsigned char *>(cache) + at;
-                *reinterpret_cast<uint2 *>(dst + ea) = e4m3_of8(a, sc);
-                *reinterpret_cast<uint2 *>(dst + eb) = e4m3_of8(b, sc);
-            } else {
-                T *dst = static_cast<T *>(cache) + at;
-                store_raw8<T>(dst + ea, is_k ? narrow8<T>(a) : ra);   // v bit for bit
-                store_raw8<T>(dst + eb, is_k ? narrow8<T>(b) : rb);
-            }
+            T *dst = static_cast<T *>(p.v_cache) + cache_at(j);
+            store_raw8<T>(dst + va, ra);
+            store_raw8<T>(dst + vb, rb);
         }
     }
 }

@@ -37,11 +37,11 @@ def rotated(x, table, positions, interleaved):
 def stored_error_bound(y, size, dtype):
     """How far a stored result may be from y.  The rounding is off by HALF |y|.
     Before it, in fp32 (u = 2^-24): the norm's sum of squares has at most 20
-    roundings in a row (16 elements of a lane and 4 exchanges), halved by the
-    root; division, root, reciprocal and two products add 5; so a normalised
-    element is off by at most 15 u of itself, and the rotation's two products
-    and one sum by 3 u of the pair's size.  32 u of the pair's size covers both
-    and the rounding of a value that is off by that much."""
+    roundings in a row (16 elements of a lane and 4 exchanges), the mean and eps
+    2 more, halved by the root, which is off by 4 u itself: 15 u.  Weight times
+    cos or sin, that times the element, the sum of a pair's two and the norm's
+    product: 4 u of the pair's size.  32 u of it covers both, the reciprocal of
+    head_dim, and the rounding of a value that is off by that much."""
     return HALF[dtype] * np.abs(y) + 32 * 2.0 ** -24 * size + TINY[dtype]
 
 
