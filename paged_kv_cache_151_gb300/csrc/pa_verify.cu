@@ -7,9 +7,10 @@
 // accepted from w = p of the row behind the last one: the first v whose
 // cumulative weight C_v exceeds u W (W the row's sum).  The vocabulary's
 // cumulative sums decide a whole number, and a row has 10^4 to 10^5 borders that
-// u W can fall next to, so sums carry about 48 bits or more: a lane adds its
-// elements in pairs of floats (the rounding error of every addition is kept
-// and added up beside it), and everything above a lane is binary64.
+// u W can fall next to, so a sum is a pair of floats (the rounding error of
+// every addition is kept and added up beside it: about 46 bits) up to a warp's
+// run of the row, and binary64 above.  Binary64 throughout costs more than the
+// row's traffic: the GPU adds about two a clock and SM.
 //
 // Bound by HBM for batches (one or two rows of the vocabulary per sequence),
 // by latency for one sequence.  A cluster of C blocks takes one sequence: the
@@ -26,6 +27,7 @@ namespace {
 
 constexpr int VF_THREADS = 512;
 constexpr int VF_WARPS = VF_THREADS / 32;
+constexpr int VF_MAX_CLUSTER = 8;
 
 // Negative entries and NaN count as 0; the comparison also drops +inf.
 __device__ __forceinline__ float weight_of(float p, float q) {
@@ -43,32 +45,71 @@ struct Row {
     }
 };
 
-// hi + lo += x with the rounding error of hi + x kept in lo
-__device__ __forceinline__ void add_pair(float &hi, float &lo, float x) {
-    const float s = hi + x, z = s - hi;
-    lo += (hi - (s - z)) + (x - z);
-    hi = s;
+// A sum as hi + lo: the rounding error of every addition to hi goes to lo.
+struct Pair {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, z = s - hi;
+        lo += (hi - (s - z)) + (x - z);
+        hi = s;
+    }
+    __device__ __forceinline__ void add(const Pair &o) {
+        add(o.hi);
+        lo += o.lo;
+    }
+    // *this > o, by the difference (its first part is exact where it matters)
+    __device__ __forceinline__ bool above(const Pair &o) const { return (hi - o.hi) + (lo - o.lo) > 0.f; }
+};
+
+__device__ __forceinline__ Pair shfl_xor(const Pair &a, int o) {
+    return Pair{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
+}
+__device__ __forceinline__ Pair shfl_up(const Pair &a, int o) {
+    return Pair{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+}
+__device__ __forceinline__ Pair pair_of(double x) {
+    const float hi = (float)x;
+    return Pair{hi, (float)(x - (double)hi)};
 }
 
-__device__ __forceinline__ double warp_sum(double x) {
+// This lane's part of the weights of [lo, hi): elements lane, lane + 32, ...,
+// U of them in flight.
+template <typename T, bool TWO, int U>
+__device__ __forceinline__ Pair sum_run(const Row<T> &row, int64_t lo, int64_t hi, int lane) {
+    Pair acc{0.f, 0.f};
+    const T *p = row.p + lo + lane, *q = TWO ? row.q + lo + lane : nullptr;
+    const int64_t hole = row.hole - lo - lane;
+    const int n = (int)(hi - lo) - lane;            // elements from this lane on
+    for (int i = 0; i < n; i += 32 * U) {
+        float x[U], y[U];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+        for (int e = 0; e < U; ++e) {
+            const bool in = i + 32 * e < n;
+            x[e] = in ? Elem<T>::load1(p + i + 32 * e) : 0.f;
+            y[e] = TWO && in ? Elem<T>::load1(q + i + 32 * e) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+            const float w = weight_of(x[e], y[e]);
+            acc.add(i + 32 * e == hole ? 0.f : w);
+        }
+    }
+    return acc;
 }
 
-__device__ __forceinline__ double ld_dsmem_f64(uint32_t addr) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(addr), "d"(v) : "memory");
 }
 
 template <typename T>
 __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
-    __shared__ int sh_acc;                          // accepted drafts
-    __shared__ int sh_reject;                       // a draft was rejected
-    __shared__ double sh_warp[VF_WARPS];            // sums of the warps' runs
-    __shared__ double sh_block;                     // and of the block's
-    __shared__ double sh_scan[VF_WARPS];
+    __shared__ int sh_acc, sh_reject;               // accepted drafts; whether one was rejected
+    __shared__ Pair sh_warp[VF_WARPS];              // sums of the warps' runs
+    __shared__ double sh_blocks[2][VF_MAX_CLUSTER]; // of the cluster's blocks, a pass each
+    __shared__ int sh_own;                          // run that holds the border, -1: another block's,
+                                                    // -2: nothing to draw from
+    __shared__ Pair sh_goal;                        // the border from the run's start
+    __shared__ Pair sh_scan[VF_WARPS];
     __shared__ unsigned sh_first, sh_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
@@ -86,6 +127,7 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
         }
         return;
     }
+    const float us = p.sample_u[s];
     const T *target = static_cast<const T *>(p.target);
     const T *draft = static_cast<const T *>(p.draft);
 
@@ -99,12 +141,13 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
             if (i < n) {
                 const int64_t r = (int64_t)q0 + i;
                 const int32_t x = p.tokens[r];
+                const float u = p.accept_u[r];
                 ok = false;
                 if (x >= 0 && x < V) {
                     const float pt = weight_of(Elem<T>::load1(target + (r - 1) * p.target_stride + x), 0.f);
                     const float qt = draft ? fmaxf(Elem<T>::load1(draft + r * p.draft_stride + x), 0.f) : 1.f;
                     // the product of two floats is exact in binary64
-                    ok = (double)p.accept_u[r] * (double)qt < (double)pt;
+                    ok = (double)u * (double)qt < (double)pt;
                 } else {
                     outside = true;
                 }
@@ -121,6 +164,8 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
         if (lane == 0) {
             sh_acc = acc;
             sh_reject = reject;
+            sh_first = 0xffffffffu;
+            sh_last = 0;
         }
     }
     __syncthreads();
@@ -139,114 +184,114 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
         const int64_t x = ((int64_t)rank * VF_WARPS + w) * chunk;
         return x < V ? x : V;
     };
+    if (rank == 0) {
+        for (int j = tid; j < p.max_query_len; j += VF_THREADS)
+            if (j != a) out[j] = j < a ? p.tokens[q0 + 1 + j] : -1;
+        if (tid == 0) p.num_accepted[s] = a;
+    }
 
-    double W = 0., before = 0., mine = 0.;
+    int own = -2;
     for (int pass = 0; pass < 2; ++pass) {
-        // ---- sums of the runs
+        // ---- sums of the runs, and of the blocks
         const int64_t lo = run_lo(warp), hi = run_lo(warp + 1);
-        float sh = 0.f, sl = 0.f;
-        constexpr int U = 8;
-        for (int64_t v0 = lo + lane; v0 < hi; v0 += 32 * U) {
-            float x[U];
+        constexpr int U = sizeof(T) == 4 ? 8 : 16;
+        Pair sum = row.q ? sum_run<T, true, 8>(row, lo, hi, lane) : sum_run<T, false, U>(row, lo, hi, lane);
 #pragma unroll
-            for (int e = 0; e < U; ++e) x[e] = v0 + 32 * e < hi ? row.at(v0 + 32 * e) : 0.f;
-#pragma unroll
-            for (int e = 0; e < U; ++e) add_pair(sh, sl, x[e]);
-        }
-        const double sum = warp_sum((double)sh + (double)sl);
+        for (int o = 16; o > 0; o >>= 1) sum.add(shfl_xor(sum, o));
         if (lane == 0) sh_warp[warp] = sum;
         __syncthreads();
-        if (tid == 0) {
-            double b = 0.;
-            for (int w = 0; w < VF_WARPS; ++w) b += sh_warp[w];
-            sh_block = b;
+        double mine = 0., inc = 0.;                 // lane w of warp 0: run w's sum, and up to it
+        if (warp == 0) {
+            if (lane < VF_WARPS) mine = (double)sh_warp[lane].hi + (double)sh_warp[lane].lo;
+            inc = mine;
+#pragma unroll
+            for (int o = 1; o < VF_WARPS; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const double block = __shfl_sync(0xffffffffu, inc, VF_WARPS - 1);
+            if (lane < C) st_dsmem_f64(map_to_rank(&sh_blocks[pass][rank], (uint32_t)lane), block);
         }
         cluster_sync();
-        W = before = mine = 0.;
-        for (int c = 0; c < C; ++c) {
-            const double b = ld_dsmem_f64(map_to_rank(&sh_block, (uint32_t)c));
-            if (c == rank) {
-                before = W;
-                mine = b;
+        // ---- the border u W: the block whose sums reach past it, and the run
+        if (warp == 0) {
+            const double b = lane < C ? sh_blocks[pass][lane] : 0.;
+            double upto = b;                        // blocks 0 .. lane
+#pragma unroll
+            for (int o = 1; o < VF_MAX_CLUSTER; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
             }
-            W += b;
+            const double W = __shfl_sync(0xffffffffu, upto, VF_MAX_CLUSTER - 1);
+            const double u = us > 0.f ? (us < 1.f ? (double)us : 1.) : 0.;
+            const double x = u * W;
+            // the first block with sums past x, or the last with any weight
+            const unsigned past = __ballot_sync(0xffffffffu, lane < C && b > 0. && x < upto);
+            const unsigned any = __ballot_sync(0xffffffffu, lane < C && b > 0.);
+            int o = -2;
+            if (W > 0. && W < INFINITY) {
+                const int blk = past ? __ffs(past) - 1 : 31 - __clz(any);
+                o = -1;
+                if (blk == rank) {
+                    double before = __shfl_sync(0xffffffffu, upto, blk) - __shfl_sync(0xffffffffu, b, blk);
+                    const unsigned rp = __ballot_sync(0xffffffffu, mine > 0. && x < before + inc);
+                    const unsigned ra = __ballot_sync(0xffffffffu, mine > 0.);
+                    o = rp ? __ffs(rp) - 1 : 31 - __clz(ra);
+                    before += __shfl_sync(0xffffffffu, inc - mine, o);
+                    if (lane == 0) sh_goal = pair_of(x - before);
+                }
+            }
+            if (lane == 0) sh_own = o;
         }
-        cluster_sync();                             // peers have read sh_block
+        __syncthreads();
+        own = sh_own;
         // nothing left of max(p - q, 0): the target's own row; every block
-        // sees the same W
-        if (W > 0. || (!row.q && row.hole < 0)) break;
+        // sees the same sums
+        if (own != -2 || (!row.q && row.hole < 0)) break;
         row.q = nullptr;
         row.hole = -1;
     }
+    if (own == -2 && rank == 0 && tid == 0) out[a] = -1;
+    if (own < 0) return;
 
-    // ---- the border u W, in the block whose sums reach past it (the last
-    // block with any weight if rounding leaves none)
-    const float us = p.sample_u[s];
-    const double u = us > 0.f ? (us < 1.f ? (double)us : 1.) : 0.;
-    const double x = u * W;
-    const bool drawn = W > 0. && W < INFINITY;
-    if (rank == 0) {
-        for (int j = tid; j < p.max_query_len; j += VF_THREADS) {
-            if (j < a) out[j] = p.tokens[q0 + 1 + j];
-            else if (j > a || !drawn) out[j] = -1;
-        }
-        if (tid == 0) p.num_accepted[s] = a;
-    }
-    if (!drawn) return;
-    const bool here = mine > 0. && x >= before && (x < before + mine || before + mine >= W);
-    if (!here) return;
-    // the run of this block
-    double base = before;
-    int own = -1, lastw = 0;
-    double ob = base;
-    for (int w = 0; w < VF_WARPS; ++w) {
-        const double b = sh_warp[w];
-        if (b > 0.) {
-            lastw = w;
-            ob = base;
-            if (x < base + b) {
-                own = w;
-                break;
-            }
-        }
-        base += b;
-    }
-    if (own < 0) own = lastw;
-    base = ob;
-    // its elements, dealt to the threads in order; a scan finds the thread
+    // ---- the run's elements, dealt to the threads in order; a scan finds the
+    // thread, and it the element
+    const Pair goal = sh_goal;
     const int64_t lo = run_lo(own), len = run_lo(own + 1) - lo;
     const int64_t per = (len + VF_THREADS - 1) / VF_THREADS;
     const int64_t e0 = lo + min(len, per * tid), e1 = lo + min(len, per * (tid + 1));
-    double sum = 0.;
-    for (int64_t v = e0; v < e1; ++v) sum += (double)row.at(v);
-    double inc = sum;
+    Pair sum{0.f, 0.f};
+    for (int64_t v = e0; v < e1; ++v) sum.add(row.at(v));
+    Pair inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const Pair y = shfl_up(inc, o);
+        if (lane >= o) inc.add(y);
     }
+    Pair before = shfl_up(inc, 1);                  // the warp's lanes before this one
+    if (lane == 0) before = Pair{0.f, 0.f};
     if (lane == 31) sh_scan[warp] = inc;
-    if (tid == 0) {
-        sh_first = 0xffffffffu;
-        sh_last = 0;
-    }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) base += sh_scan[w];
-    if (sum > 0.) {
-        if (x < base + inc) atomicMin(&sh_first, (unsigned)tid);
+    Pair base{0.f, 0.f};
+    for (int w = 0; w < warp; ++w) base.add(sh_scan[w]);
+    Pair end = base;
+    end.add(inc);
+    if (sum.hi > 0.f) {
+        if (end.above(goal)) atomicMin(&sh_first, (unsigned)tid);
         atomicMax(&sh_last, (unsigned)tid);
     }
     __syncthreads();
     const unsigned chosen = sh_first != 0xffffffffu ? sh_first : sh_last;
     if ((unsigned)tid != chosen) return;
-    double run = base + (inc - sum);
+    Pair run = base;                                // up to this thread's elements
+    run.add(before);
     int64_t token = -1;
     for (int64_t v = e0; v < e1; ++v) {
         const float w = row.at(v);
         if (w > 0.f) {
             token = v;
-            run += (double)w;
-            if (x < run) break;
+            run.add(w);
+            if (run.above(goal)) break;
         }
     }
     out[a] = (int32_t)token;
@@ -254,10 +299,13 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
 
 template <typename T>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
+#ifndef PA_VERIFY_BLOCKS
+#define PA_VERIFY_BLOCKS 2
+#endif
     const int sms = sm_count_of_current_device();
-    const int64_t slots = (int64_t)(sms > 0 ? sms : 152) * 2;
+    const int64_t slots = (int64_t)(sms > 0 ? sms : 152) * PA_VERIFY_BLOCKS;
     int C = 1;
-    while (C < 8 && (int64_t)p.num_seqs * C * 2 <= slots) C *= 2;
+    while (C < VF_MAX_CLUSTER && (int64_t)p.num_seqs * C * 2 <= slots) C *= 2;
     if ((int64_t)p.num_seqs * C > (int64_t)INT32_MAX) return cudaErrorNotSupported;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.num_seqs * C), 1, 1);
