@@ -693,11 +693,23 @@ extern "C" int pa_decode_multi_fp8(
     p.num_seqs = num_seqs; p.num_heads = num_heads; p.num_kv_heads = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
     p.scale_log2 = scale * pa::LOG2E;
+    // as for 16-bit caches: runs of at least PREFILL_GROUP_ROWS (token, head) rows
+    // go to the tcgen05 kernel, the others to the persistent kernel
+    const bool split = rows >= pa::PREFILL_GROUP_ROWS;
+    const int64_t small_rows = split ? pa::PREFILL_GROUP_ROWS - 1 : rows;
+    p.mq_split_rows = split ? pa::PREFILL_GROUP_ROWS : 0;
     if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
     if (!prepare_maps(p, PA_E4M3, head_dim)) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long unit_bound = (long long)num_seqs * num_kv_heads * ((rows + 15) / 16);
-    cudaError_t e = dtype == PA_BF16
+    if (split) {
+        const int groups = (int)((rows + pa::PREFILL_F8_ROWS - 1) / pa::PREFILL_F8_ROWS);
+        const cudaError_t e = dtype == PA_BF16 ? pa::prefill_f8_bf16(p, head_dim, G, groups, st)
+                                               : pa::prefill_f8_f16(p, head_dim, G, groups, st);
+        if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
+        if (e != cudaSuccess) return PA_ERR_CUDA;
+    }
+    const long long unit_bound = (long long)num_seqs * num_kv_heads * ((small_rows + 15) / 16);
+    const cudaError_t e = dtype == PA_BF16
                         ? pa::decode_multi_fp8_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
                         : pa::decode_multi_fp8_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st);
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;

@@ -109,6 +109,11 @@ struct VerifyParams {
 };
 cudaError_t verify_drafts(const VerifyParams &p, int dtype, cudaStream_t st);
 
+// the rows of long multi-token runs over E4M3 caches (pa_prefill_f8.cuh)
+constexpr int PREFILL_F8_ROWS = 256;       // rows of one item
+cudaError_t prefill_f8_bf16(const DecodeParams &p, int D, int G, int groups, cudaStream_t st);
+cudaError_t prefill_f8_f16(const DecodeParams &p, int D, int G, int groups, cudaStream_t st);
+
 // multi-token queries over E4M3 caches (q and out bf16 / f16)
 cudaError_t decode_multi_fp8_bf16(const DecodeParams &p, int D, int G, long long unit_bound,
                                   int cluster, cudaStream_t st);

@@ -1,0 +1,490 @@
+// pa_prefill_f8.cuh -- multi-token queries with many rows per sequence (a chunk
+// of a prompt) over E4M3 caches, on the fifth-generation tensor cores.
+//
+// "vLLM: Architecture, PagedAttention & Internals", *Prefill, decode, and
+// chunked prefill*.  Row r of sequence s's run (token i = r / G, head r % G of
+// the KV head's group) attends over positions 0 .. L - n + i.  As in the
+// decode path every code is exactly an f16 value, so q is rounded to f16, the
+// codes are converted on the way into shared memory and both products run as
+// kind::f16 with fp32 accumulation; K's scale folds into the score scale and
+// V's into the final normalisation.
+//
+// A work item is 256 rows of one (sequence, KV head), as two tiles of 128 rows
+// (the M side of an MMA), so that every key is loaded and converted once for
+// 256 rows; one block per SM works through its items, 64 keys a step:
+//   S = Q K^T   M = 128, N = 64, K = head_dim: Q from TMEM (written there once
+//               per item by the threads that own its rows), K from shared
+//               memory.  With Q in shared memory too the product would read
+//               192 bytes a clock, more than the 128 that there are.
+//   softmax     one thread per row (four warps a tile): 64 scores from TMEM,
+//               causal mask, online softmax in fp32 with lazy rescaling, P as
+//               f16 pairs over the scores' own columns
+//   O += P V    M = 128, N = head_dim, K = 64: P from TMEM, V from shared memory
+//               MN-major; O stays in TMEM over the item
+// TMEM columns (512): S/P of tile 0 and 1 (64 each), O (head_dim each), Q
+// (head_dim / 2 each).  P takes the place of S, so a tile's next S waits for its
+// P V; the tensor pipe works on one tile while the other's softmax runs.
+//
+// Roles of the 14 warps: 0-3 and 4-7 softmax of tile 0 and 1; 8, 9 convert K and
+// 10, 11 V (32 rows of a step each: 16-byte loads of codes two steps ahead in
+// registers, f16 to the 128-byte swizzled stages, four stages each of K and V);
+// lane 0 of warps 12 and 13 issues the MMAs of tile 0 and 1.  MMAs with different
+// accumulators may complete out of order, so an issuer waits for a step's P V
+// before the S that overwrites its P.  Completion comes back through
+// tcgen05.commit on mbarriers.  Every wait is bounded; on a timeout the block
+// stops and the error word says so.
+#pragma once
+
+#include <atomic>
+
+#include "pa_common.cuh"
+#include "pa_decode.cuh"
+#include "pa_fp8.cuh"
+#include "pa_internal.h"
+#include "pa_mma.cuh"
+#include "pa_prefill.cuh"
+#include "pa_tc5.cuh"
+
+namespace pa {
+
+constexpr int PF8_ROWS = PREFILL_F8_ROWS;      // rows of one item: two tiles of 128
+constexpr int PF8_KEYS = 64;                   // keys of a step: four cache blocks
+constexpr int PF8_STAGES = 4;                  // of K, and of V
+constexpr int PF8_THREADS = 14 * 32;
+constexpr int PF8_K_WARP = 8;                  // and 9; V: 10, 11
+constexpr int PF8_MMA_WARP = 12;               // and 13
+
+template <int D>
+struct PrefillF8Layout {
+    static constexpr int NH = D / 64;                                // 128-byte groups of an f16 row
+    static constexpr uint32_t KV_BYTES = PF8_KEYS * D * 2;           // [NH][64 keys][128 B]
+    static constexpr size_t OFF_K = 0;
+    static constexpr size_t OFF_V = (size_t)PF8_STAGES * KV_BYTES;
+    static constexpr size_t OFF_BARS = 2 * (size_t)PF8_STAGES * KV_BYTES;
+    static constexpr int NBARS = 4 * PF8_STAGES + 8 + 1;
+    static constexpr size_t OFF_TMEM = OFF_BARS + (size_t)NBARS * 8;
+    static constexpr size_t BYTES = OFF_TMEM + 16 + 1024;            // + alignment of the base
+    // TMEM columns of tile t: S and P, O, Q
+    static constexpr uint32_t TMEM_S = 0, TMEM_O = 128, TMEM_Q = 128 + 2 * D;
+    static_assert(TMEM_Q + D <= 512 && KV_BYTES % 1024 == 0, "TMEM columns; swizzle atoms");
+};
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(PF8_THREADS, 1)
+prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
+    static_assert(sizeof(T) == 2 && (D == 64 || D == 128), "16-bit q and out, head_dim 64 or 128");
+    static_assert(128 % G == 0, "a tile holds whole tokens");
+    using Lay = PrefillF8Layout<D>;
+    constexpr uint32_t KVB = Lay::KV_BYTES;
+    constexpr int NS = PF8_STAGES;
+    constexpr uint32_t ID_S = tc5_idesc<__half>(128, PF8_KEYS, 0);   // Q K^T: K K-major
+    constexpr uint32_t ID_O = tc5_idesc<__half>(128, D, 1);          // P V: V MN-major
+
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::OFF_BARS);
+    uint64_t *kfull = bars;                // [NS] K of a step converted (two warps)
+    uint64_t *vfull = bars + NS;           // [NS] V of a step converted
+    uint64_t *kfree = bars + 2 * NS;       // [NS] both tiles' S of a step done
+    uint64_t *vfree = bars + 3 * NS;       // [NS] both tiles' P V of a step done
+    uint64_t *q_full = bars + 4 * NS;      // [2] a tile's Q in TMEM (four warps)
+    uint64_t *s_full = q_full + 2;         // [2] a tile's S of a step in TMEM
+    uint64_t *p_full = q_full + 4;         // [2] a tile's P of a step in TMEM (four warps)
+    uint64_t *pv_done = q_full + 6;        // [2] a tile's P V of a step done
+    uint64_t *mma_idle = q_full + 8;       // the block's MMAs are all done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
+    __shared__ PrefillSched sched;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hkv = p.num_kv_heads, H = p.num_heads;
+
+    // the kernel launched next (the rows of the short runs) may set up; it waits
+    // for this grid before it touches the caches or out
+    launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < 4 * NS; ++i) mbar_init(&bars[i], 2);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 4);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&pv_done[t], 1);
+        }
+        mbar_init(mma_idle, 2);
+        fence_mbar_init();
+    }
+    if (warp == 0) tc5_alloc(tmem_slot, 512);
+    tc5_fence_before_sync();
+    __syncthreads();
+    tc5_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    const int total = prefill_schedule<G, PF8_ROWS>(p, groups, sched);
+    grid_dependency_wait();                // q, the caches and out from here on
+
+    const int R = (int)gridDim.x, me = (int)blockIdx.x;
+    // The geometry of an item; every role computes it alike.
+    struct Item {
+        int s, j, row0, q0, nq, L, nrows, nsteps;
+    };
+    auto item_at = [&](int k, Item &it) -> bool {  // all lanes of a warp
+        const long long x = (long long)k * R + ((k & 1) ? (R - 1 - me) : me);   // snake
+        if (x >= total) return false;
+        int grp;
+        prefill_item<G, PF8_ROWS>(p, groups, sched, (int)x, it.s, it.j, grp);
+        it.q0 = p.query_start[it.s];
+        it.nq = p.query_start[it.s + 1] - it.q0;
+        it.L = p.seq_lens[it.s];
+        it.row0 = grp * PF8_ROWS;
+        it.nrows = min(PF8_ROWS, it.nq * G - it.row0);           // >= 1
+        const int n_keys = it.L - it.nq + (it.row0 + it.nrows - 1) / G + 1;   // keys any row sees
+        it.nsteps = (n_keys + PF8_KEYS - 1) / PF8_KEYS;
+        return true;
+    };
+
+    if (warp >= PF8_K_WARP && warp < PF8_MMA_WARP) {
+        // ---- convert K (warps 8, 9) or V (10, 11): rows 32 * half .. + 31 of each
+        // step.  D / 16 lanes hold a row's codes, 16 each.
+        const bool kside = warp < PF8_K_WARP + 2;
+        const int half = warp & 1;
+        constexpr int LPR = D / 16, RPI = 32 / LPR, NI = 32 / RPI;
+        const int r0 = lane / LPR, jl = lane % LPR;
+        const unsigned char *cache = static_cast<const unsigned char *>(kside ? p.k_cache : p.v_cache);
+        unsigned char *const stage0 = smem + (kside ? Lay::OFF_K : Lay::OFF_V);
+        uint64_t *const full = kside ? kfull : vfull;
+        uint64_t *const empty = kside ? kfree : vfree;
+
+        // the load cursor: step c of item k, and the physical blocks of this
+        // warp's two cache blocks of it
+        Item it;
+        int k = 0, c = 0, pb[2] = {-1, -1};
+        bool more = item_at(0, it);
+        auto blocks_of = [&]() {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int lb = 4 * c + 2 * half + b;
+                pb[b] = more && 16 * lb < it.L
+                            ? __ldg(p.block_tables + (long long)it.s * p.max_blocks + lb) : -1;
+            }
+        };
+        blocks_of();
+        auto load = [&](uint4 (&buf)[NI]) -> bool {        // the cursor's step; moves on
+            if (!more) return false;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int key0 = 16 * (4 * c + 2 * half + b);
+                bool ok = key0 < it.L;
+                if (ok && (pb[b] < 0 || (long long)pb[b] >= p.num_blocks)) {
+                    if (kside && lane == 0) set_error(p.err, ERR_BLOCK_ID);
+                    ok = false;
+                }
+                const unsigned char *src = cache + ((long long)(ok ? pb[b] : 0) * Hkv + it.j) * (16 * D) + 16 * jl;
+#pragma unroll
+                for (int i = 0; i < NI / 2; ++i) {
+                    const int r = i * RPI + r0;            // rows past the sequence: zeros
+                    buf[b * (NI / 2) + i] = ok && key0 + r < it.L
+                        ? __ldg(reinterpret_cast<const uint4 *>(src + r * D)) : make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (++c == it.nsteps) {
+                c = 0;
+                more = item_at(++k, it);
+            }
+            blocks_of();
+            return true;
+        };
+        // chunk cc of 8 f16 of row r lies at cc ^ (r & 7) of its 128-byte group;
+        // lanes of the second group store their odd chunk first, so that the
+        // eight lanes of a row touch all banks
+        const int hgrp = jl / 4, cc = 2 * (jl % 4);
+        auto store = [&](unsigned char *st, const uint4 (&buf)[NI]) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = 32 * half + i * RPI + r0;
+                const uint4 w = buf[i];
+                const uint4 lo = make_uint4(f16x2_from_e4m3x2(w.x), f16x2_from_e4m3x2(w.x >> 16),
+                                            f16x2_from_e4m3x2(w.y), f16x2_from_e4m3x2(w.y >> 16));
+                const uint4 hi = make_uint4(f16x2_from_e4m3x2(w.z), f16x2_from_e4m3x2(w.z >> 16),
+                                            f16x2_from_e4m3x2(w.w), f16x2_from_e4m3x2(w.w >> 16));
+                unsigned char *row = st + hgrp * (PF8_KEYS * 128) + r * 128;
+                const int first = cc + (hgrp & 1), second = cc + 1 - (hgrp & 1);
+                *reinterpret_cast<uint4 *>(row + ((first ^ (r & 7)) << 4)) = hgrp & 1 ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + ((second ^ (r & 7)) << 4)) = hgrp & 1 ? lo : hi;
+            }
+        };
+        long long g = 0;
+        auto put = [&](const uint4 (&buf)[NI]) -> bool {
+            const int st = (int)(g % NS);
+            bool w = true;
+            if (lane == 0 && g >= NS) w = mbar_wait_bounded(&empty[st], (uint32_t)((g / NS - 1) & 1), p.err);
+            if (!__shfl_sync(0xffffffffu, w, 0)) return false;
+            store(stage0 + (size_t)st * KVB, buf);
+            fence_proxy_async_smem();              // the rows before the MMAs
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
+            ++g;
+            return true;
+        };
+        uint4 b0[NI], b1[NI];
+        bool h0 = load(b0), h1 = load(b1);
+        while (h0) {
+            if (!put(b0)) break;
+            h0 = load(b0);
+            if (!h1) break;
+            if (!put(b1)) break;
+            h1 = load(b1);
+        }
+    } else if (warp >= PF8_MMA_WARP) {
+        // ---- the MMAs of tile t
+        const int t = warp - PF8_MMA_WARP;
+        bool ok = true;
+        long long g0 = 0, gt = 0;                  // steps so far; of this tile
+        int kt = 0;                                // items with this tile
+        Item it;
+        const uint64_t dk = tc5_desc_sw128(smem_u32(smem + Lay::OFF_K), 16, 1024);
+        const uint64_t dv = tc5_desc_sw128(smem_u32(smem + Lay::OFF_V), PF8_KEYS * 128, 1024);
+        const uint32_t tS = tmem + Lay::TMEM_S + 64 * t, tO = tmem + Lay::TMEM_O + D * t;
+        const uint32_t tQ = tmem + Lay::TMEM_Q + (D / 2) * t;
+        for (int k = 0; ok && item_at(k, it); ++k) {
+            const int n = it.nsteps;
+            const bool rows = it.nrows > 128 * t;
+            if (lane == 0) {
+                auto wait = [&](uint64_t *bar, long long phase) -> bool {
+                    const bool w = mbar_wait_bounded(bar, (uint32_t)(phase & 1), p.err);
+                    tc5_fence_after_sync();
+                    return w;
+                };
+                ok = !rows || wait(&q_full[t], kt);
+                for (int c = 0; ok && c < n; ++c) {
+                    const long long g = g0 + c;
+                    const int st = (int)(g % NS);
+                    ok = wait(&kfull[st], g / NS);
+                    if (!ok) break;
+                    if (!rows) {                   // an idle tile gives the stages back
+                        mbar_arrive(&kfree[st]);
+                        ok = wait(&vfull[st], g / NS);
+                        mbar_arrive(&vfree[st]);
+                        continue;
+                    }
+                    // P of the step before lies in these columns
+                    if (c > 0) ok = wait(&pv_done[t], gt + c - 1);
+                    if (!ok) break;
+                    const uint64_t kb = dk + (uint64_t)((uint32_t)st * KVB >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)            // 16 elements = 32 bytes
+                        tc5_mma_ta(tS, tQ + 8 * ks, kb + (uint32_t)(((ks >> 2) * (PF8_KEYS * 128) + (ks & 3) * 32) >> 4),
+                                   ID_S, ks > 0);
+                    tc5_commit(&s_full[t]);
+                    tc5_commit(&kfree[st]);
+                    ok = wait(&p_full[t], gt + c) && wait(&vfull[st], g / NS);
+                    if (!ok) break;
+                    const uint64_t vb = dv + (uint64_t)((uint32_t)st * KVB >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < PF8_KEYS / 16; ++ks)     // 16 keys = 2048 bytes
+                        tc5_mma_ta(tO, tS + 8 * ks, vb + (uint32_t)(ks * 2048 >> 4), ID_O, c > 0 || ks > 0);
+                    tc5_commit(&pv_done[t]);
+                    tc5_commit(&vfree[st]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            g0 += n;
+            if (rows) {
+                gt += n;
+                ++kt;
+            }
+        }
+        // MMAs may still be running (after a timeout): wait for them
+        if (lane == 0) {
+            tc5_commit(mma_idle);
+            mbar_wait_bounded(mma_idle, 0, p.err);
+        }
+    } else if (warp < PF8_K_WARP) {
+        // ---- softmax: thread r of tile t owns row 128 t + r of every item
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;   // this warp's TMEM lanes
+        const uint32_t tS = tmem + Lay::TMEM_S + 64 * t + lane_base, tO = tmem + Lay::TMEM_O + D * t + lane_base;
+        const uint32_t tQ = tmem + Lay::TMEM_Q + (D / 2) * t + lane_base;
+        long long g = 0;                           // steps of this tile
+        bool ok = true;
+        Item it;
+        for (int k = 0; ok && item_at(k, it); ++k) {
+            if (it.nrows <= 128 * t) continue;     // no rows of this tile
+            const int rr = it.row0 + 128 * t + r;
+            const int tok = rr / G, head = rr % G;
+            const bool row_ok = 128 * t + r < it.nrows;
+            // last visible position; rows past the run see what its last row sees
+            const int lim = it.L - it.nq + min(tok, it.nq - 1);
+            // the score scale; a negative one moves its sign to q, and one of 0 is
+            // a tiny one, so that masked scores stay -inf
+            float sl2 = p.scale_log2 * __ldg(p.k_scale + it.j);
+            const uint32_t sign = sl2 < 0.f ? 0x80008000u : 0u;
+            sl2 = fmaxf(fabsf(sl2), 1e-30f);
+
+            // -- Q of this row to TMEM as f16 pairs
+            {
+                const T *q = static_cast<const T *>(p.q) + (long long)(it.q0 + tok) * p.q_seq_stride +
+                             (long long)(it.j * G + head) * D;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 x = row_ok ? __ldg(reinterpret_cast<const uint4 *>(q + c0) + i)
+                                               : make_uint4(0, 0, 0, 0);
+                        w[4 * i] = WarpAttnF8<T, D, 1>::to_f16x2(x.x) ^ sign;
+                        w[4 * i + 1] = WarpAttnF8<T, D, 1>::to_f16x2(x.y) ^ sign;
+                        w[4 * i + 2] = WarpAttnF8<T, D, 1>::to_f16x2(x.z) ^ sign;
+                        w[4 * i + 3] = WarpAttnF8<T, D, 1>::to_f16x2(x.w) ^ sign;
+                    }
+                    tc5_st32u(tQ + c0 / 2, w);     // waits for the store
+                }
+                tc5_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[t]);
+            }
+
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int c = 0; c < it.nsteps; ++c, ++g) {
+                const bool got = mbar_wait_bounded(&s_full[t], (uint32_t)(g & 1), p.err);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                tc5_fence_after_sync();
+                float sv[PF8_KEYS];
+                tc5_ld64u(tS, *reinterpret_cast<uint32_t(*)[PF8_KEYS]>(&sv[0]));
+                const int nvis = lim - c * PF8_KEYS + 1;     // positions of this step the row sees
+                if (__any_sync(0xffffffffu, nvis < PF8_KEYS)) {
+#pragma unroll
+                    for (int e = 0; e < PF8_KEYS; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
+                }
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < PF8_KEYS; e += 8) {
+                    m4[0] = max3f(m4[0], sv[e], sv[e + 1]);
+                    m4[1] = max3f(m4[1], sv[e + 2], sv[e + 3]);
+                    m4[2] = max3f(m4[2], sv[e + 4], sv[e + 5]);
+                    m4[3] = max3f(m4[3], sv[e + 6], sv[e + 7]);
+                }
+                const float mxs = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+                // lazy rescaling: the reference level moves only by more than 2^RESCALE_LOG2
+                const float m_new = mxs > m_run + RESCALE_LOG2 ? mxs : m_run;
+                const float ms = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = m_new == m_run ? 1.f : ex2(m_run - ms);
+                uint32_t pw[PF8_KEYS / 2];
+                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                 make_float2(0.f, 0.f)};
+                const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-ms, -ms);
+#pragma unroll
+                for (int e = 0; e < PF8_KEYS / 2; ++e) {
+                    const float2 x = fma2(make_float2(sv[2 * e], sv[2 * e + 1]), sc2, nm2);
+                    const float2 pe = make_float2(ex2(x.x), ex2(x.y));
+                    pw[e] = Mma<__half>::pack(pe.x, pe.y);
+                    acc[e & 3] = add2(acc[e & 3], pe);
+                }
+                // P over the scores of this row
+                tc5_st32u(tS, pw);
+                const float2 a2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                l_run = l_run * alpha + (a2.x + a2.y);
+                m_run = m_new;
+                // this row of O to the new level, once P V of the step before is done
+                // (O holds nothing before the item's first)
+                if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    const bool done = mbar_wait_bounded(&pv_done[t], (uint32_t)((g - 1) & 1), p.err);
+                    if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
+                    tc5_fence_after_sync();
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        float o[32];
+                        tc5_ld32(tO + c0, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tc5_st32(tO + c0, o);
+                    }
+                }
+                tc5_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+
+            // -- O / l, in V's scale, into out (this thread's row)
+            const bool done = mbar_wait_bounded(&pv_done[t], (uint32_t)((g - 1) & 1), p.err);
+            if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
+            tc5_fence_after_sync();
+            const float inv = l_run > 0.f ? __ldg(p.v_scale + it.j) / l_run : 0.f;
+            T *o = static_cast<T *>(p.out) + ((long long)(it.q0 + tok) * H + it.j * G + head) * D;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float v[32];
+                tc5_ld32(tO + c0, v);
+                if (row_ok) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w;
+                        w.x = Mma<T>::pack(v[e] * inv, v[e + 1] * inv);
+                        w.y = Mma<T>::pack(v[e + 2] * inv, v[e + 3] * inv);
+                        w.z = Mma<T>::pack(v[e + 4] * inv, v[e + 5] * inv);
+                        w.w = Mma<T>::pack(v[e + 6] * inv, v[e + 7] * inv);
+                        *reinterpret_cast<uint4 *>(o + c0 + e) = w;
+                    }
+                }
+            }
+            // O and S read before the next item's MMAs overwrite them (they wait for
+            // this warp's next arrivals)
+            tc5_fence_before_sync();
+        }
+    }
+
+    tc5_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tc5_dealloc(tmem, 512);
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, cudaStream_t st) {
+    constexpr size_t smem = PrefillF8Layout<D>::BYTES;
+    static_assert(smem + sizeof(PrefillSched) + 1024 <= 227 * 1024, "shared memory");
+    auto kern = prefill_f8_kernel<T, D, G>;
+    static std::atomic<bool> attr_set[64];    // per device, read by any host thread
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
+    }
+    // one block per SM, but no more than the items can be: the worst case, and
+    // one more than the full items of each run (a run has at least
+    // PREFILL_GROUP_ROWS rows)
+    const long long worst = (long long)groups * p.num_seqs * p.num_kv_heads;
+    const long long rows_all = (long long)p.num_q_rows * G;
+    const long long bound = p.num_kv_heads * (rows_all / PF8_ROWS + rows_all / PREFILL_GROUP_ROWS + 1);
+    const int sms = sm_count_of_current_device();
+    long long blocks = sms > 0 ? sms : 152;
+    if (blocks > worst) blocks = worst;
+    if (blocks > bound) blocks = bound;
+    if (blocks <= 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(PF8_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p, groups);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch_prefill_f8(const DecodeParams &p, int D, int G, int groups, cudaStream_t st) {
+#define PA_CASE(DD, GG) \
+    if (D == DD && G == GG) return launch_prefill_f8<T, DD, GG>(p, groups, st);
+    PA_CASE(64, 1) PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
+    PA_CASE(128, 1) PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
+#undef PA_CASE
+    return cudaErrorNotSupported;
+}
+
+}  // namespace pa
