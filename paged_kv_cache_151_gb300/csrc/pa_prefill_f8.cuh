@@ -12,27 +12,30 @@
 // A work item is 256 rows of one (sequence, KV head), as two tiles of 128 rows
 // (the M side of an MMA), so that every key is loaded and converted once for
 // 256 rows; one block per SM works through its items, 64 keys a step:
-//   S = Q K^T   M = 128, N = 64, K = head_dim: Q from TMEM (written there once
-//               per item by the threads that own its rows), K from shared
-//               memory.  With Q in shared memory too the product would read
-//               192 bytes a clock, more than the 128 that there are.
-//   softmax     one thread per row (four warps a tile): 64 scores from TMEM,
-//               causal mask, online softmax in fp32 with lazy rescaling, P as
-//               f16 pairs over the scores' own columns
+//   S = Q K^T   M = 128, N = 64, K = head_dim: the first 64 elements of Q from
+//               TMEM (written there once per item by the threads that own its
+//               rows), the rest and K from shared memory.  With all of Q in
+//               shared memory the product would read 192 bytes a clock, more
+//               than the 128 that there are.
+//   softmax     one thread per row (four warps a tile): 64 scores from TMEM --
+//               after which the next step's S may overwrite them -- causal
+//               mask, online softmax in fp32 with lazy rescaling, P as f16
+//               pairs to TMEM once P V of the step before is done
 //   O += P V    M = 128, N = head_dim, K = 64: P from TMEM, V from shared memory
 //               MN-major; O stays in TMEM over the item
-// TMEM columns (512): S/P of tile 0 and 1 (64 each), O (head_dim each), Q
-// (head_dim / 2 each).  P takes the place of S, so a tile's next S waits for its
-// P V; the tensor pipe works on one tile while the other's softmax runs.
+// TMEM columns: S of tile 0 and 1 (64 each), P (32 each), O (head_dim each),
+// Q (32 each): 512 at head_dim 128.  S of the next step is in place when a
+// softmax warp comes back for it, so neither the tensor pipe nor the softmax
+// warps wait for a whole chain of S, softmax and P V.  (P over the scores' own
+// columns, with all of Q in TMEM, ties the three into one chain: a step of
+// both tiles took 3160 clocks, the two tiles in step with each other.)
 //
 // Roles of the 14 warps: 0-3 and 4-7 softmax of tile 0 and 1; 8, 9 convert K and
 // 10, 11 V (32 rows of a step each: 16-byte loads of codes two steps ahead in
-// registers, f16 to the 128-byte swizzled stages, four stages each of K and V);
-// lane 0 of warps 12 and 13 issues the MMAs of tile 0 and 1.  MMAs with different
-// accumulators may complete out of order, so an issuer waits for a step's P V
-// before the S that overwrites its P.  Completion comes back through
-// tcgen05.commit on mbarriers.  Every wait is bounded; on a timeout the block
-// stops and the error word says so.
+// registers, f16 to the 128-byte swizzled stages, PF8_STAGES stages each of K
+// and V); lane 0 of warps 12 and 13 issues the MMAs of tile 0 and 1.  Completion
+// comes back through tcgen05.commit on mbarriers.  Every wait is bounded; on a
+// timeout the block stops and the error word says so.
 #pragma once
 
 #include <atomic>
@@ -58,15 +61,18 @@ template <int D>
 struct PrefillF8Layout {
     static constexpr int NH = D / 64;                                // 128-byte groups of an f16 row
     static constexpr uint32_t KV_BYTES = PF8_KEYS * D * 2;           // [NH][64 keys][128 B]
+    static constexpr uint32_t Q_BYTES = (NH - 1) * 128 * 128;        // a tile's [NH - 1][128 rows][128 B]
     static constexpr size_t OFF_K = 0;
     static constexpr size_t OFF_V = (size_t)PF8_STAGES * KV_BYTES;
-    static constexpr size_t OFF_BARS = 2 * (size_t)PF8_STAGES * KV_BYTES;
-    static constexpr int NBARS = 4 * PF8_STAGES + 8 + 1;
+    static constexpr size_t OFF_Q = 2 * (size_t)PF8_STAGES * KV_BYTES;
+    static constexpr size_t OFF_BARS = OFF_Q + 2 * (size_t)Q_BYTES;
+    static constexpr int NBARS = 4 * PF8_STAGES + 10 + 1;
     static constexpr size_t OFF_TMEM = OFF_BARS + (size_t)NBARS * 8;
     static constexpr size_t BYTES = OFF_TMEM + 16 + 1024;            // + alignment of the base
-    // TMEM columns of tile t: S and P, O, Q
-    static constexpr uint32_t TMEM_S = 0, TMEM_O = 128, TMEM_Q = 128 + 2 * D;
-    static_assert(TMEM_Q + D <= 512 && KV_BYTES % 1024 == 0, "TMEM columns; swizzle atoms");
+    // first TMEM columns of tile 0's S, P, O and Q; tile 1's come 64, 32, D and
+    // 32 later
+    static constexpr uint32_t TMEM_S = 0, TMEM_P = 128, TMEM_O = 192, TMEM_Q = 192 + 2 * D;
+    static_assert(TMEM_Q + 64 <= 512 && KV_BYTES % 1024 == 0, "TMEM columns; swizzle atoms");
 };
 
 template <typename T, int D, int G>
@@ -90,8 +96,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     uint64_t *q_full = bars + 4 * NS;      // [2] a tile's Q in TMEM (four warps)
     uint64_t *s_full = q_full + 2;         // [2] a tile's S of a step in TMEM
     uint64_t *p_full = q_full + 4;         // [2] a tile's P of a step in TMEM (four warps)
-    uint64_t *pv_done = q_full + 6;        // [2] a tile's P V of a step done
-    uint64_t *mma_idle = q_full + 8;       // the block's MMAs are all done
+    uint64_t *pv_done = q_full + 6;        // [2] a tile's P V of a step done: P free, O whole
+    uint64_t *s_free = q_full + 8;         // [2] a tile's S of a step read (four warps)
+    uint64_t *mma_idle = q_full + 10;      // the block's MMAs are all done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
     __shared__ PrefillSched sched;
 
@@ -108,6 +115,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&pv_done[t], 1);
+            mbar_init(&s_free[t], 4);
         }
         mbar_init(mma_idle, 2);
         fence_mbar_init();
@@ -211,11 +219,11 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                 *reinterpret_cast<uint4 *>(row + ((second ^ (r & 7)) << 4)) = hgrp & 1 ? lo : hi;
             }
         };
-        long long g = 0;
+        unsigned g = 0;
         auto put = [&](const uint4 (&buf)[NI]) -> bool {
             const int st = (int)(g % NS);
             bool w = true;
-            if (lane == 0 && g >= NS) w = mbar_wait_bounded(&empty[st], (uint32_t)((g / NS - 1) & 1), p.err);
+            if (lane == 0 && g >= NS) w = mbar_wait_bounded(&empty[st], (g / NS - 1) & 1, p.err);
             if (!__shfl_sync(0xffffffffu, w, 0)) return false;
             store(stage0 + (size_t)st * KVB, buf);
             fence_proxy_async_smem();              // the rows before the MMAs
@@ -234,55 +242,66 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             h1 = load(b1);
         }
     } else if (warp >= PF8_MMA_WARP) {
-        // ---- the MMAs of tile t
+        // ---- the MMAs of tile t: S of step c + 1, then P V of step c
         const int t = warp - PF8_MMA_WARP;
         bool ok = true;
-        long long g0 = 0, gt = 0;                  // steps so far; of this tile
-        int kt = 0;                                // items with this tile
+        unsigned g0 = 0, gt = 0;                   // steps so far; of this tile
+        unsigned kt = 0;                           // items with this tile
         Item it;
         const uint64_t dk = tc5_desc_sw128(smem_u32(smem + Lay::OFF_K), 16, 1024);
         const uint64_t dv = tc5_desc_sw128(smem_u32(smem + Lay::OFF_V), PF8_KEYS * 128, 1024);
-        const uint32_t tS = tmem + Lay::TMEM_S + 64 * t, tO = tmem + Lay::TMEM_O + D * t;
-        const uint32_t tQ = tmem + Lay::TMEM_Q + (D / 2) * t;
+        const uint64_t dq = tc5_desc_sw128(smem_u32(smem + Lay::OFF_Q + t * Lay::Q_BYTES), 16, 1024);
+        const uint32_t tS = tmem + Lay::TMEM_S + 64 * t, tP = tmem + Lay::TMEM_P + 32 * t;
+        const uint32_t tO = tmem + Lay::TMEM_O + D * t, tQ = tmem + Lay::TMEM_Q + 32 * t;
         for (int k = 0; ok && item_at(k, it); ++k) {
-            const int n = it.nsteps;
+            const unsigned n = (unsigned)it.nsteps;
             const bool rows = it.nrows > 128 * t;
             if (lane == 0) {
-                auto wait = [&](uint64_t *bar, long long phase) -> bool {
-                    const bool w = mbar_wait_bounded(bar, (uint32_t)(phase & 1), p.err);
-                    tc5_fence_after_sync();
-                    return w;
+                auto wait = [&](uint64_t *bar, unsigned phase) -> bool {
+                    return mbar_wait_bounded(bar, phase & 1, p.err);
                 };
                 ok = !rows || wait(&q_full[t], kt);
-                for (int c = 0; ok && c < n; ++c) {
-                    const long long g = g0 + c;
-                    const int st = (int)(g % NS);
-                    ok = wait(&kfull[st], g / NS);
-                    if (!ok) break;
-                    if (!rows) {                   // an idle tile gives the stages back
-                        mbar_arrive(&kfree[st]);
-                        ok = wait(&vfull[st], g / NS);
-                        mbar_arrive(&vfree[st]);
-                        continue;
+                for (unsigned c = 0; ok && c <= n; ++c) {
+                    if (c < n) {
+                        const unsigned g = g0 + c, st = g % NS;
+                        ok = wait(&kfull[st], g / NS);
+                        if (ok && rows) {
+                            // S of the step before has been read (by the item
+                            // before, if this is an item's first)
+                            ok = gt + c == 0 || wait(&s_free[t], gt + c - 1);
+                            if (!ok) break;
+                            tc5_fence_after_sync();
+                            const uint64_t kb = dk + (uint64_t)(st * KVB >> 4);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)             // 16 elements = 32 bytes
+                                tc5_mma_ta(tS, tQ + 8 * ks, kb + (uint32_t)(ks * 32 >> 4), ID_S, ks > 0);
+#pragma unroll
+                            for (int ks = 4; ks < D / 16; ++ks)
+                                tc5_mma(tS, dq + (uint32_t)(((ks >> 2) - 1) * (128 * 128) + (ks & 3) * 32 >> 4),
+                                        kb + (uint32_t)(((ks >> 2) * (PF8_KEYS * 128) + (ks & 3) * 32) >> 4), ID_S, 1);
+                            tc5_commit(&s_full[t]);
+                            tc5_commit(&kfree[st]);
+                        } else if (ok) {           // an idle tile gives the stage back
+                            mbar_arrive(&kfree[st]);
+                        }
                     }
-                    // P of the step before lies in these columns
-                    if (c > 0) ok = wait(&pv_done[t], gt + c - 1);
-                    if (!ok) break;
-                    const uint64_t kb = dk + (uint64_t)((uint32_t)st * KVB >> 4);
+                    if (ok && c > 0) {
+                        const unsigned g = g0 + c - 1, st = g % NS;
+                        ok = wait(&vfull[st], g / NS);
+                        if (ok && rows) {
+                            ok = wait(&p_full[t], gt + c - 1);
+                            if (!ok) break;
+                            tc5_fence_after_sync();
+                            const uint64_t vb = dv + (uint64_t)(st * KVB >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)            // 16 elements = 32 bytes
-                        tc5_mma_ta(tS, tQ + 8 * ks, kb + (uint32_t)(((ks >> 2) * (PF8_KEYS * 128) + (ks & 3) * 32) >> 4),
-                                   ID_S, ks > 0);
-                    tc5_commit(&s_full[t]);
-                    tc5_commit(&kfree[st]);
-                    ok = wait(&p_full[t], gt + c) && wait(&vfull[st], g / NS);
-                    if (!ok) break;
-                    const uint64_t vb = dv + (uint64_t)((uint32_t)st * KVB >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < PF8_KEYS / 16; ++ks)     // 16 keys = 2048 bytes
-                        tc5_mma_ta(tO, tS + 8 * ks, vb + (uint32_t)(ks * 2048 >> 4), ID_O, c > 0 || ks > 0);
-                    tc5_commit(&pv_done[t]);
-                    tc5_commit(&vfree[st]);
+                            for (int ks = 0; ks < PF8_KEYS / 16; ++ks) // 16 keys = 2048 bytes
+                                tc5_mma_ta(tO, tP + 8 * ks, vb + (uint32_t)(ks * 2048 >> 4), ID_O, c > 1 || ks > 0);
+                            tc5_commit(&pv_done[t]);
+                            tc5_commit(&vfree[st]);
+                        } else if (ok) {
+                            mbar_arrive(&vfree[st]);
+                        }
+                    }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -301,9 +320,10 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         // ---- softmax: thread r of tile t owns row 128 t + r of every item
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;   // this warp's TMEM lanes
-        const uint32_t tS = tmem + Lay::TMEM_S + 64 * t + lane_base, tO = tmem + Lay::TMEM_O + D * t + lane_base;
-        const uint32_t tQ = tmem + Lay::TMEM_Q + (D / 2) * t + lane_base;
-        long long g = 0;                           // steps of this tile
+        const uint32_t tS = tmem + Lay::TMEM_S + 64 * t + lane_base, tP = tmem + Lay::TMEM_P + 32 * t + lane_base;
+        const uint32_t tO = tmem + Lay::TMEM_O + D * t + lane_base, tQ = tmem + Lay::TMEM_Q + 32 * t + lane_base;
+        unsigned char *const qrow = smem + Lay::OFF_Q + t * Lay::Q_BYTES + r * 128;
+        unsigned g = 0;                            // steps of this tile
         bool ok = true;
         Item it;
         for (int k = 0; ok && item_at(k, it); ++k) {
@@ -313,30 +333,41 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             const bool row_ok = 128 * t + r < it.nrows;
             // last visible position; rows past the run see what its last row sees
             const int lim = it.L - it.nq + min(tok, it.nq - 1);
+            const int cmask = (__reduce_min_sync(0xffffffffu, lim) + 1) / PF8_KEYS;   // steps before: no mask
             // the score scale; a negative one moves its sign to q, and one of 0 is
             // a tiny one, so that masked scores stay -inf
             float sl2 = p.scale_log2 * __ldg(p.k_scale + it.j);
             const uint32_t sign = sl2 < 0.f ? 0x80008000u : 0u;
             sl2 = fmaxf(fabsf(sl2), 1e-30f);
 
-            // -- Q of this row to TMEM as f16 pairs
+            // -- Q of this row as f16: the first 64 elements to TMEM as pairs, the
+            // rest to shared memory (128-byte swizzle); the item before is done
+            // with both
             {
                 const T *q = static_cast<const T *>(p.q) + (long long)(it.q0 + tok) * p.q_seq_stride +
                              (long long)(it.j * G + head) * D;
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 64) {
+                for (int h = 0; h < D / 64; ++h) {
                     uint32_t w[32];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 x = row_ok ? __ldg(reinterpret_cast<const uint4 *>(q + c0) + i)
+                        const uint4 x = row_ok ? __ldg(reinterpret_cast<const uint4 *>(q + 64 * h) + i)
                                                : make_uint4(0, 0, 0, 0);
                         w[4 * i] = WarpAttnF8<T, D, 1>::to_f16x2(x.x) ^ sign;
                         w[4 * i + 1] = WarpAttnF8<T, D, 1>::to_f16x2(x.y) ^ sign;
                         w[4 * i + 2] = WarpAttnF8<T, D, 1>::to_f16x2(x.z) ^ sign;
                         w[4 * i + 3] = WarpAttnF8<T, D, 1>::to_f16x2(x.w) ^ sign;
                     }
-                    tc5_st32u(tQ + c0 / 2, w);     // waits for the store
+                    if (h == 0) {
+                        tc5_st32u(tQ, w);          // waits for the store
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(qrow + (h - 1) * (128 * 128) + ((i ^ (r & 7)) << 4)) =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    }
                 }
+                if (D > 64) fence_proxy_async_smem();
                 tc5_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[t]);
@@ -344,13 +375,16 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 
             float m_run = -INFINITY, l_run = 0.f;
             for (int c = 0; c < it.nsteps; ++c, ++g) {
-                const bool got = mbar_wait_bounded(&s_full[t], (uint32_t)(g & 1), p.err);
+                const bool got = mbar_wait_bounded(&s_full[t], g & 1, p.err);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc5_fence_after_sync();
                 float sv[PF8_KEYS];
                 tc5_ld64u(tS, *reinterpret_cast<uint32_t(*)[PF8_KEYS]>(&sv[0]));
-                const int nvis = lim - c * PF8_KEYS + 1;     // positions of this step the row sees
-                if (__any_sync(0xffffffffu, nvis < PF8_KEYS)) {
+                tc5_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[t]);
+                if (c >= cmask) {
+                    const int nvis = lim - c * PF8_KEYS + 1;     // positions of this step the row sees
 #pragma unroll
                     for (int e = 0; e < PF8_KEYS; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
                 }
@@ -378,17 +412,19 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     pw[e] = Mma<__half>::pack(pe.x, pe.y);
                     acc[e & 3] = add2(acc[e & 3], pe);
                 }
-                // P over the scores of this row
-                tc5_st32u(tS, pw);
                 const float2 a2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
                 l_run = l_run * alpha + (a2.x + a2.y);
                 m_run = m_new;
-                // this row of O to the new level, once P V of the step before is done
-                // (O holds nothing before the item's first)
-                if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    const bool done = mbar_wait_bounded(&pv_done[t], (uint32_t)((g - 1) & 1), p.err);
+                // P V of the step before is done: its P may be overwritten, and this
+                // row of O taken to the new level (O holds nothing before the
+                // item's first)
+                if (g > 0) {
+                    const bool done = mbar_wait_bounded(&pv_done[t], (g - 1) & 1, p.err);
                     if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
                     tc5_fence_after_sync();
+                }
+                tc5_st32u(tP, pw);
+                if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         float o[32];
@@ -405,7 +441,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             if (!ok) break;
 
             // -- O / l, in V's scale, into out (this thread's row)
-            const bool done = mbar_wait_bounded(&pv_done[t], (uint32_t)((g - 1) & 1), p.err);
+            const bool done = mbar_wait_bounded(&pv_done[t], (g - 1) & 1, p.err);
             if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
             tc5_fence_after_sync();
             const float inv = l_run > 0.f ? __ldg(p.v_scale + it.j) / l_run : 0.f;
