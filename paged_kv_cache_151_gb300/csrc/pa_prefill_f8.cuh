@@ -30,12 +30,14 @@
 // columns, with all of Q in TMEM, ties the three into one chain: a step of
 // both tiles took 3160 clocks, the two tiles in step with each other.)
 //
-// Roles of the 14 warps: 0-3 and 4-7 softmax of tile 0 and 1; 8, 9 convert K and
+// Roles of the 16 warps: 0-3 and 4-7 softmax of tile 0 and 1; 8, 9 convert K and
 // 10, 11 V (32 rows of a step each: 16-byte loads of codes two steps ahead in
 // registers, f16 to the 128-byte swizzled stages, PF8_STAGES stages each of K
-// and V); lane 0 of warps 12 and 13 issues the MMAs of tile 0 and 1.  Completion
-// comes back through tcgen05.commit on mbarriers.  Every wait is bounded; on a
-// timeout the block stops and the error word says so.
+// and V); lane 0 of warps 12 and 13 issues S of tile 0 and 1, of warps 14 and 15
+// P V (an issue blocks while the pipe is busy, so one warp for both would hold
+// the next S back behind a P V, or the reverse).  Completion comes back through
+// tcgen05.commit on mbarriers; one lane of a warp polls.  Every wait is bounded;
+// on a timeout the block stops and the error word says so.
 #pragma once
 
 #include <atomic>
@@ -53,9 +55,9 @@ namespace pa {
 constexpr int PF8_ROWS = PREFILL_F8_ROWS;      // rows of one item: two tiles of 128
 constexpr int PF8_KEYS = 64;                   // keys of a step: four cache blocks
 constexpr int PF8_STAGES = 4;                  // of K, and of V
-constexpr int PF8_THREADS = 14 * 32;
+constexpr int PF8_THREADS = 16 * 32;
 constexpr int PF8_K_WARP = 8;                  // and 9; V: 10, 11
-constexpr int PF8_MMA_WARP = 12;               // and 13
+constexpr int PF8_MMA_WARP = 12;               // and 13: S; 14, 15: P V
 
 template <int D>
 struct PrefillF8Layout {
@@ -117,7 +119,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             mbar_init(&pv_done[t], 1);
             mbar_init(&s_free[t], 4);
         }
-        mbar_init(mma_idle, 2);
+        mbar_init(mma_idle, 4);
         fence_mbar_init();
     }
     if (warp == 0) tc5_alloc(tmem_slot, 512);
@@ -151,13 +153,21 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 
     if (warp >= PF8_K_WARP && warp < PF8_MMA_WARP) {
         // ---- convert K (warps 8, 9) or V (10, 11): rows 32 * half .. + 31 of each
-        // step.  D / 16 lanes hold a row's codes, 16 each.
+        // step.  A lane holds 16 codes of a row: the pieces 0-3 of two
+        // neighbouring rows lie in eight neighbouring lanes, whose f16 chunks 2 jl
+        // (and 2 jl + 1) then fall on all banks under the swizzle.
         const bool kside = warp < PF8_K_WARP + 2;
         const int half = warp & 1;
-        constexpr int LPR = D / 16, RPI = 32 / LPR, NI = 32 / RPI;
-        const int r0 = lane / LPR, jl = lane % LPR;
-        const unsigned char *cache = static_cast<const unsigned char *>(kside ? p.k_cache : p.v_cache);
-        unsigned char *const stage0 = smem + (kside ? Lay::OFF_K : Lay::OFF_V);
+        constexpr int RPI = 512 / D, NI = 32 / RPI;       // rows of an instruction; instructions
+        const int jl = (lane & 3) | (D == 128 ? (lane >> 1) & 4 : 0);
+        const int r0 = D == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
+        const unsigned char *cache = static_cast<const unsigned char *>(kside ? p.k_cache : p.v_cache) +
+                                     r0 * D + 16 * jl;
+        // f16 chunk cc of row r lies at cc ^ (r & 7) of its 128-byte group; with
+        // four rows an instruction, every second one flips bit 2 of that
+        unsigned char *const stage0 = smem + (kside ? Lay::OFF_K : Lay::OFF_V) +
+                                      (jl >> 2) * (PF8_KEYS * 128) + (32 * half + r0) * 128;
+        const int lo0 = ((2 * (jl & 3)) ^ r0) << 4, hi0 = ((2 * (jl & 3) + 1) ^ r0) << 4;
         uint64_t *const full = kside ? kfull : vfull;
         uint64_t *const empty = kside ? kfree : vfree;
 
@@ -165,58 +175,61 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         // warp's two cache blocks of it
         Item it;
         int k = 0, c = 0, pb[2] = {-1, -1};
+        const int32_t *tab = nullptr;
+        long long joff = 0;
+        const long long bstride = (long long)Hkv * (16 * D);
         bool more = item_at(0, it);
-        auto blocks_of = [&]() {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int lb = 4 * c + 2 * half + b;
-                pb[b] = more && 16 * lb < it.L
-                            ? __ldg(p.block_tables + (long long)it.s * p.max_blocks + lb) : -1;
-            }
+        auto item_set = [&]() {
+            if (!more) return;
+            tab = p.block_tables + (long long)it.s * p.max_blocks + 2 * half;
+            joff = (long long)it.j * (16 * D);
         };
+        auto blocks_of = [&]() {
+            if (!more) return;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                if (64 * c + 32 * half + 16 * b < it.L) pb[b] = __ldg(tab + 4 * c + b);
+        };
+        item_set();
         blocks_of();
         auto load = [&](uint4 (&buf)[NI]) -> bool {        // the cursor's step; moves on
             if (!more) return false;
+            const int key0 = 64 * c + 32 * half;
+            const bool whole = key0 + 32 <= it.L;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int key0 = 16 * (4 * c + 2 * half + b);
-                bool ok = key0 < it.L;
-                if (ok && (pb[b] < 0 || (long long)pb[b] >= p.num_blocks)) {
+                // rows past the sequence and bad blocks: zeros
+                int rows = whole ? 16 : min(16, it.L - key0 - 16 * b);
+                if (rows > 0 && (pb[b] < 0 || (long long)pb[b] >= p.num_blocks)) {
                     if (kside && lane == 0) set_error(p.err, ERR_BLOCK_ID);
-                    ok = false;
+                    rows = 0;
                 }
-                const unsigned char *src = cache + ((long long)(ok ? pb[b] : 0) * Hkv + it.j) * (16 * D) + 16 * jl;
+                const unsigned char *src = cache + (rows > 0 ? pb[b] : 0) * bstride + joff;
 #pragma unroll
-                for (int i = 0; i < NI / 2; ++i) {
-                    const int r = i * RPI + r0;            // rows past the sequence: zeros
-                    buf[b * (NI / 2) + i] = ok && key0 + r < it.L
-                        ? __ldg(reinterpret_cast<const uint4 *>(src + r * D)) : make_uint4(0, 0, 0, 0);
-                }
+                for (int i = 0; i < NI / 2; ++i)
+                    buf[b * (NI / 2) + i] = i * RPI + r0 < rows
+                        ? __ldg(reinterpret_cast<const uint4 *>(src + i * RPI * D)) : make_uint4(0, 0, 0, 0);
             }
             if (++c == it.nsteps) {
                 c = 0;
                 more = item_at(++k, it);
+                item_set();
             }
             blocks_of();
             return true;
         };
-        // chunk cc of 8 f16 of row r lies at cc ^ (r & 7) of its 128-byte group;
-        // lanes of the second group store their odd chunk first, so that the
-        // eight lanes of a row touch all banks
-        const int hgrp = jl / 4, cc = 2 * (jl % 4);
         auto store = [&](unsigned char *st, const uint4 (&buf)[NI]) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int r = 32 * half + i * RPI + r0;
                 const uint4 w = buf[i];
-                const uint4 lo = make_uint4(f16x2_from_e4m3x2(w.x), f16x2_from_e4m3x2(w.x >> 16),
-                                            f16x2_from_e4m3x2(w.y), f16x2_from_e4m3x2(w.y >> 16));
-                const uint4 hi = make_uint4(f16x2_from_e4m3x2(w.z), f16x2_from_e4m3x2(w.z >> 16),
-                                            f16x2_from_e4m3x2(w.w), f16x2_from_e4m3x2(w.w >> 16));
-                unsigned char *row = st + hgrp * (PF8_KEYS * 128) + r * 128;
-                const int first = cc + (hgrp & 1), second = cc + 1 - (hgrp & 1);
-                *reinterpret_cast<uint4 *>(row + ((first ^ (r & 7)) << 4)) = hgrp & 1 ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + ((second ^ (r & 7)) << 4)) = hgrp & 1 ? lo : hi;
+                const int flip = RPI == 4 && (i & 1) ? 64 : 0;
+                unsigned char *row = st + i * RPI * 128;
+                *reinterpret_cast<uint4 *>(row + (lo0 ^ flip)) =
+                    make_uint4(f16x2_from_e4m3x2(w.x), f16x2_from_e4m3x2(w.x >> 16),
+                               f16x2_from_e4m3x2(w.y), f16x2_from_e4m3x2(w.y >> 16));
+                *reinterpret_cast<uint4 *>(row + (hi0 ^ flip)) =
+                    make_uint4(f16x2_from_e4m3x2(w.z), f16x2_from_e4m3x2(w.z >> 16),
+                               f16x2_from_e4m3x2(w.w), f16x2_from_e4m3x2(w.w >> 16));
             }
         };
         unsigned g = 0;
@@ -242,10 +255,11 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             h1 = load(b1);
         }
     } else if (warp >= PF8_MMA_WARP) {
-        // ---- the MMAs of tile t: S of step c + 1, then P V of step c
-        const int t = warp - PF8_MMA_WARP;
+        // ---- the MMAs of tile t: S (warps 12, 13) or P V (14, 15)
+        const int t = warp & 1;
+        const bool sside = warp < PF8_MMA_WARP + 2;
         bool ok = true;
-        unsigned g0 = 0, gt = 0;                   // steps so far; of this tile
+        unsigned g = 0, gt = 0;                    // steps so far; of this tile
         unsigned kt = 0;                           // items with this tile
         Item it;
         const uint64_t dk = tc5_desc_sw128(smem_u32(smem + Lay::OFF_K), 16, 1024);
@@ -253,63 +267,53 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         const uint64_t dq = tc5_desc_sw128(smem_u32(smem + Lay::OFF_Q + t * Lay::Q_BYTES), 16, 1024);
         const uint32_t tS = tmem + Lay::TMEM_S + 64 * t, tP = tmem + Lay::TMEM_P + 32 * t;
         const uint32_t tO = tmem + Lay::TMEM_O + D * t, tQ = tmem + Lay::TMEM_Q + 32 * t;
+        auto wait = [&](uint64_t *bar, unsigned phase) -> bool {
+            return mbar_wait_bounded(bar, phase & 1, p.err);
+        };
         for (int k = 0; ok && item_at(k, it); ++k) {
-            const unsigned n = (unsigned)it.nsteps;
-            const bool rows = it.nrows > 128 * t;
-            if (lane == 0) {
-                auto wait = [&](uint64_t *bar, unsigned phase) -> bool {
-                    return mbar_wait_bounded(bar, phase & 1, p.err);
-                };
-                ok = !rows || wait(&q_full[t], kt);
-                for (unsigned c = 0; ok && c <= n; ++c) {
-                    if (c < n) {
-                        const unsigned g = g0 + c, st = g % NS;
-                        ok = wait(&kfull[st], g / NS);
-                        if (ok && rows) {
-                            // S of the step before has been read (by the item
-                            // before, if this is an item's first)
-                            ok = gt + c == 0 || wait(&s_free[t], gt + c - 1);
-                            if (!ok) break;
-                            tc5_fence_after_sync();
-                            const uint64_t kb = dk + (uint64_t)(st * KVB >> 4);
+            const int n = it.nsteps;
+            if (lane == 0 && it.nrows <= 128 * t) {
+                // an idle tile gives the stages back
+                uint64_t *const full = sside ? kfull : vfull, *const empty = sside ? kfree : vfree;
+                for (int c = 0; ok && c < n; ++c, ++g) {
+                    ok = wait(&full[g % NS], g / NS);
+                    if (ok) mbar_arrive(&empty[g % NS]);
+                }
+            } else if (lane == 0 && sside) {
+                ok = wait(&q_full[t], kt++);
+                for (int c = 0; ok && c < n; ++c, ++g, ++gt) {
+                    const unsigned st = g % NS;
+                    // K has landed, and S of the step before has been read (by the
+                    // item before, if this is an item's first)
+                    ok = wait(&kfull[st], g / NS) && (gt == 0 || wait(&s_free[t], gt - 1));
+                    if (!ok) break;
+                    tc5_fence_after_sync();
+                    const uint64_t kb = dk + (uint64_t)(st * KVB >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)             // 16 elements = 32 bytes
-                                tc5_mma_ta(tS, tQ + 8 * ks, kb + (uint32_t)(ks * 32 >> 4), ID_S, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)             // 16 elements = 32 bytes
+                        tc5_mma_ta(tS, tQ + 8 * ks, kb + (uint32_t)(ks * 32 >> 4), ID_S, ks > 0);
 #pragma unroll
-                            for (int ks = 4; ks < D / 16; ++ks)
-                                tc5_mma(tS, dq + (uint32_t)(((ks >> 2) - 1) * (128 * 128) + (ks & 3) * 32 >> 4),
-                                        kb + (uint32_t)(((ks >> 2) * (PF8_KEYS * 128) + (ks & 3) * 32) >> 4), ID_S, 1);
-                            tc5_commit(&s_full[t]);
-                            tc5_commit(&kfree[st]);
-                        } else if (ok) {           // an idle tile gives the stage back
-                            mbar_arrive(&kfree[st]);
-                        }
-                    }
-                    if (ok && c > 0) {
-                        const unsigned g = g0 + c - 1, st = g % NS;
-                        ok = wait(&vfull[st], g / NS);
-                        if (ok && rows) {
-                            ok = wait(&p_full[t], gt + c - 1);
-                            if (!ok) break;
-                            tc5_fence_after_sync();
-                            const uint64_t vb = dv + (uint64_t)(st * KVB >> 4);
+                    for (int ks = 4; ks < D / 16; ++ks)
+                        tc5_mma(tS, dq + (uint32_t)(((ks >> 2) - 1) * (128 * 128) + (ks & 3) * 32 >> 4),
+                                kb + (uint32_t)(((ks >> 2) * (PF8_KEYS * 128) + (ks & 3) * 32) >> 4), ID_S, 1);
+                    tc5_commit(&s_full[t]);
+                    tc5_commit(&kfree[st]);
+                }
+            } else if (lane == 0) {
+                for (int c = 0; ok && c < n; ++c, ++g, ++gt) {
+                    const unsigned st = g % NS;
+                    ok = wait(&vfull[st], g / NS) && wait(&p_full[t], gt);
+                    if (!ok) break;
+                    tc5_fence_after_sync();
+                    const uint64_t vb = dv + (uint64_t)(st * KVB >> 4);
 #pragma unroll
-                            for (int ks = 0; ks < PF8_KEYS / 16; ++ks) // 16 keys = 2048 bytes
-                                tc5_mma_ta(tO, tP + 8 * ks, vb + (uint32_t)(ks * 2048 >> 4), ID_O, c > 1 || ks > 0);
-                            tc5_commit(&pv_done[t]);
-                            tc5_commit(&vfree[st]);
-                        } else if (ok) {
-                            mbar_arrive(&vfree[st]);
-                        }
-                    }
+                    for (int ks = 0; ks < PF8_KEYS / 16; ++ks) // 16 keys = 2048 bytes
+                        tc5_mma_ta(tO, tP + 8 * ks, vb + (uint32_t)(ks * 2048 >> 4), ID_O, c > 0 || ks > 0);
+                    tc5_commit(&pv_done[t]);
+                    tc5_commit(&vfree[st]);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            g0 += n;
-            if (rows) {
-                gt += n;
-                ++kt;
-            }
         }
         // MMAs may still be running (after a timeout): wait for them
         if (lane == 0) {
@@ -325,6 +329,13 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         unsigned char *const qrow = smem + Lay::OFF_Q + t * Lay::Q_BYTES + r * 128;
         unsigned g = 0;                            // steps of this tile
         bool ok = true;
+        auto wait = [&](uint64_t *bar, unsigned phase) -> bool {       // the whole warp
+            bool w = true;
+            if (lane == 0) w = mbar_wait_bounded(bar, phase & 1, p.err);
+            w = __shfl_sync(0xffffffffu, w, 0);
+            tc5_fence_after_sync();
+            return w;
+        };
         Item it;
         for (int k = 0; ok && item_at(k, it); ++k) {
             if (it.nrows <= 128 * t) continue;     // no rows of this tile
@@ -375,9 +386,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 
             float m_run = -INFINITY, l_run = 0.f;
             for (int c = 0; c < it.nsteps; ++c, ++g) {
-                const bool got = mbar_wait_bounded(&s_full[t], g & 1, p.err);
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                tc5_fence_after_sync();
+                if (!wait(&s_full[t], g)) { ok = false; break; }
                 float sv[PF8_KEYS];
                 tc5_ld64u(tS, *reinterpret_cast<uint32_t(*)[PF8_KEYS]>(&sv[0]));
                 tc5_fence_before_sync();
@@ -418,11 +427,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                 // P V of the step before is done: its P may be overwritten, and this
                 // row of O taken to the new level (O holds nothing before the
                 // item's first)
-                if (g > 0) {
-                    const bool done = mbar_wait_bounded(&pv_done[t], (g - 1) & 1, p.err);
-                    if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
-                    tc5_fence_after_sync();
-                }
+                if (g > 0 && !wait(&pv_done[t], g - 1)) { ok = false; break; }
                 tc5_st32u(tP, pw);
                 if (c > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
@@ -441,9 +446,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             if (!ok) break;
 
             // -- O / l, in V's scale, into out (this thread's row)
-            const bool done = mbar_wait_bounded(&pv_done[t], (g - 1) & 1, p.err);
-            if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
-            tc5_fence_after_sync();
+            if (!wait(&pv_done[t], g - 1)) { ok = false; break; }
             const float inv = l_run > 0.f ? __ldg(p.v_scale + it.j) / l_run : 0.f;
             T *o = static_cast<T *>(p.out) + ((long long)(it.q0 + tok) * H + it.j * G + head) * D;
 #pragma unroll
