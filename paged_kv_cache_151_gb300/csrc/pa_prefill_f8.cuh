@@ -30,10 +30,16 @@
 // columns, with all of Q in TMEM, ties the three into one chain: a step of
 // both tiles took 3160 clocks, the two tiles in step with each other.)
 //
+// A cluster of C blocks (1, 2 or 4) shares an item by its keys where the items
+// alone would leave SMs idle: each block takes n / C consecutive steps, and at
+// the end block r owns head_dim / C columns of O: every softmax thread writes
+// the other blocks' columns of its row, and its (m, l), into their shared memory,
+// and merges its own columns in the order of the ranks (so the result is a
+// function of the sizes and of C only).
+//
 // Roles of the 16 warps: 0-3 and 4-7 softmax of tile 0 and 1; 8, 9 convert K and
 // 10, 11 V (32 rows of a step each: 16-byte loads of codes two steps ahead in
-// registers, f16 to the 128-byte swizzled stages, PF8_STAGES stages each of K
-// and V); lane 0 of warps 12 and 13 issues S of tile 0 and 1, of warps 14 and 15
+// registers, f16 to the 128-byte swizzled stages of K and V); lane 0 of warps 12 and 13 issues S of tile 0 and 1, of warps 14 and 15
 // P V (an issue blocks while the pipe is busy, so one warp for both would hold
 // the next S back behind a P V, or the reverse).  Completion comes back through
 // tcgen05.commit on mbarriers; one lane of a warp polls.  Every wait is bounded;
@@ -54,21 +60,29 @@ namespace pa {
 
 constexpr int PF8_ROWS = PREFILL_F8_ROWS;      // rows of one item: two tiles of 128
 constexpr int PF8_KEYS = 64;                   // keys of a step: four cache blocks
-constexpr int PF8_STAGES = 4;                  // of K, and of V
+// stages of K, and of V: what the exchange buffers of a cluster leave room for
+__host__ __device__ constexpr int pf8_stages(int C) { return C == 1 ? 4 : C == 2 ? 3 : 2; }
 constexpr int PF8_THREADS = 16 * 32;
 constexpr int PF8_K_WARP = 8;                  // and 9; V: 10, 11
 constexpr int PF8_MMA_WARP = 12;               // and 13: S; 14, 15: P V
 
-template <int D>
+template <int D, int C>
 struct PrefillF8Layout {
+    static constexpr int STAGES = pf8_stages(C);
     static constexpr int NH = D / 64;                                // 128-byte groups of an f16 row
     static constexpr uint32_t KV_BYTES = PF8_KEYS * D * 2;           // [NH][64 keys][128 B]
     static constexpr uint32_t Q_BYTES = (NH - 1) * 128 * 128;        // a tile's [NH - 1][128 rows][128 B]
+    // from the other blocks of the cluster, a tile: columns of O [C][D / C / 4][128
+    // rows] float4 (the own rank's slot is not there), and (m, l) [C][128]
+    static constexpr uint32_t XO_BYTES = (C - 1) * (D / C) * 128 * 4;
+    static constexpr uint32_t XS_BYTES = C > 1 ? C * 128 * 8 : 0;
     static constexpr size_t OFF_K = 0;
-    static constexpr size_t OFF_V = (size_t)PF8_STAGES * KV_BYTES;
-    static constexpr size_t OFF_Q = 2 * (size_t)PF8_STAGES * KV_BYTES;
-    static constexpr size_t OFF_BARS = OFF_Q + 2 * (size_t)Q_BYTES;
-    static constexpr int NBARS = 4 * PF8_STAGES + 10 + 1;
+    static constexpr size_t OFF_V = (size_t)STAGES * KV_BYTES;
+    static constexpr size_t OFF_Q = 2 * (size_t)STAGES * KV_BYTES;
+    static constexpr size_t OFF_XO = OFF_Q + 2 * (size_t)Q_BYTES;
+    static constexpr size_t OFF_XS = OFF_XO + 2 * (size_t)XO_BYTES;
+    static constexpr size_t OFF_BARS = OFF_XS + 2 * (size_t)XS_BYTES;
+    static constexpr int NBARS = 4 * STAGES + 14 + 1;
     static constexpr size_t OFF_TMEM = OFF_BARS + (size_t)NBARS * 8;
     static constexpr size_t BYTES = OFF_TMEM + 16 + 1024;            // + alignment of the base
     // first TMEM columns of tile 0's S, P, O and Q; tile 1's come 64, 32, D and
@@ -77,14 +91,45 @@ struct PrefillF8Layout {
     static_assert(TMEM_Q + 64 <= 512 && KV_BYTES % 1024 == 0, "TMEM columns; swizzle atoms");
 };
 
-template <typename T, int D, int G>
+// A remote or local shared-memory float4 / float2, and an arrival at another
+// block's barrier that publishes what this warp wrote there.
+__device__ __forceinline__ void st_dsmem_f32x4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "f"(a), "f"(b),
+                 "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ void st_dsmem_f32x2(uint32_t addr, float a, float b) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" :: "r"(addr), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+// the address `addr` of this block's shared memory in block `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t out;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+    return out;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+
+template <typename T, int D, int G, int C>
 __global__ void __launch_bounds__(PF8_THREADS, 1)
 prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     static_assert(sizeof(T) == 2 && (D == 64 || D == 128), "16-bit q and out, head_dim 64 or 128");
     static_assert(128 % G == 0, "a tile holds whole tokens");
-    using Lay = PrefillF8Layout<D>;
+    static_assert(C == 1 || C == 2 || C == 4, "blocks that share an item");
+    using Lay = PrefillF8Layout<D, C>;
     constexpr uint32_t KVB = Lay::KV_BYTES;
-    constexpr int NS = PF8_STAGES;
+    constexpr int NS = Lay::STAGES;
     constexpr uint32_t ID_S = tc5_idesc<__half>(128, PF8_KEYS, 0);   // Q K^T: K K-major
     constexpr uint32_t ID_O = tc5_idesc<__half>(128, D, 1);          // P V: V MN-major
 
@@ -100,7 +145,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     uint64_t *p_full = q_full + 4;         // [2] a tile's P of a step in TMEM (four warps)
     uint64_t *pv_done = q_full + 6;        // [2] a tile's P V of a step done: P free, O whole
     uint64_t *s_free = q_full + 8;         // [2] a tile's S of a step read (four warps)
-    uint64_t *mma_idle = q_full + 10;      // the block's MMAs are all done
+    uint64_t *x_full = q_full + 10;        // [2] a tile's rows from the other blocks are here
+    uint64_t *x_free = q_full + 12;        // [2] the other blocks have read this one's rows
+    uint64_t *mma_idle = q_full + 14;      // the block's MMAs are all done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
     __shared__ PrefillSched sched;
 
@@ -118,6 +165,8 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             mbar_init(&p_full[t], 4);
             mbar_init(&pv_done[t], 1);
             mbar_init(&s_free[t], 4);
+            mbar_init(&x_full[t], C > 1 ? 4 * (C - 1) : 1);
+            mbar_init(&x_free[t], C > 1 ? 4 * (C - 1) : 1);
         }
         mbar_init(mma_idle, 4);
         fence_mbar_init();
@@ -127,14 +176,17 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     __syncthreads();
     tc5_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if constexpr (C > 1) cluster_sync();   // the peers' barriers are there
 
     const int total = prefill_schedule<G, PF8_ROWS>(p, groups, sched);
     grid_dependency_wait();                // q, the caches and out from here on
 
-    const int R = (int)gridDim.x, me = (int)blockIdx.x;
-    // The geometry of an item; every role computes it alike.
+    const int R = (int)gridDim.x / C, me = (int)blockIdx.x / C;    // clusters
+    const int rank = C > 1 ? (int)cluster_ctarank() : 0;
+    // The geometry of an item, and this block's steps of it; every role computes
+    // it alike.
     struct Item {
-        int s, j, row0, q0, nq, L, nrows, nsteps;
+        int s, j, row0, q0, nq, L, nrows, step0, nsteps;
     };
     auto item_at = [&](int k, Item &it) -> bool {  // all lanes of a warp
         const long long x = (long long)k * R + ((k & 1) ? (R - 1 - me) : me);   // snake
@@ -147,7 +199,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         it.row0 = grp * PF8_ROWS;
         it.nrows = min(PF8_ROWS, it.nq * G - it.row0);           // >= 1
         const int n_keys = it.L - it.nq + (it.row0 + it.nrows - 1) / G + 1;   // keys any row sees
-        it.nsteps = (n_keys + PF8_KEYS - 1) / PF8_KEYS;
+        const int n = (n_keys + PF8_KEYS - 1) / PF8_KEYS;
+        it.step0 = n * rank / C;
+        it.nsteps = n * (rank + 1) / C - it.step0;
         return true;
     };
 
@@ -174,27 +228,29 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         // the load cursor: step c of item k, and the physical blocks of this
         // warp's two cache blocks of it
         Item it;
-        int k = 0, c = 0, pb[2] = {-1, -1};
+        int k = -1, c = 0, pb[2] = {-1, -1};
         const int32_t *tab = nullptr;
         long long joff = 0;
         const long long bstride = (long long)Hkv * (16 * D);
-        bool more = item_at(0, it);
-        auto item_set = [&]() {
+        bool more = false;
+        auto item_next = [&]() {                   // the next item with steps of this block's
+            do more = item_at(++k, it); while (more && it.nsteps == 0);
             if (!more) return;
-            tab = p.block_tables + (long long)it.s * p.max_blocks + 2 * half;
+            c = 0;
+            tab = p.block_tables + (long long)it.s * p.max_blocks + 4 * it.step0 + 2 * half;
             joff = (long long)it.j * (16 * D);
         };
         auto blocks_of = [&]() {
             if (!more) return;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
-                if (64 * c + 32 * half + 16 * b < it.L) pb[b] = __ldg(tab + 4 * c + b);
+                if (64 * (it.step0 + c) + 32 * half + 16 * b < it.L) pb[b] = __ldg(tab + 4 * c + b);
         };
-        item_set();
+        item_next();
         blocks_of();
         auto load = [&](uint4 (&buf)[NI]) -> bool {        // the cursor's step; moves on
             if (!more) return false;
-            const int key0 = 64 * c + 32 * half;
+            const int key0 = 64 * (it.step0 + c) + 32 * half;
             const bool whole = key0 + 32 <= it.L;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -210,11 +266,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     buf[b * (NI / 2) + i] = i * RPI + r0 < rows
                         ? __ldg(reinterpret_cast<const uint4 *>(src + i * RPI * D)) : make_uint4(0, 0, 0, 0);
             }
-            if (++c == it.nsteps) {
-                c = 0;
-                more = item_at(++k, it);
-                item_set();
-            }
+            if (++c == it.nsteps) item_next();
             blocks_of();
             return true;
         };
@@ -328,12 +380,18 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         const uint32_t tO = tmem + Lay::TMEM_O + D * t + lane_base, tQ = tmem + Lay::TMEM_Q + 32 * t + lane_base;
         unsigned char *const qrow = smem + Lay::OFF_Q + t * Lay::Q_BYTES + r * 128;
         unsigned g = 0;                            // steps of this tile
+        unsigned kt = 0;                           // items of it
         bool ok = true;
         auto wait = [&](uint64_t *bar, unsigned phase) -> bool {       // the whole warp
             bool w = true;
             if (lane == 0) w = mbar_wait_bounded(bar, phase & 1, p.err);
             w = __shfl_sync(0xffffffffu, w, 0);
             tc5_fence_after_sync();
+            return w;
+        };
+        auto wait_cluster = [&](uint64_t *bar, unsigned phase) -> bool {
+            const bool w = wait(bar, phase);
+            fence_acq_rel_cluster();               // what the other blocks wrote before it
             return w;
         };
         Item it;
@@ -386,14 +444,15 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 
             float m_run = -INFINITY, l_run = 0.f;
             for (int c = 0; c < it.nsteps; ++c, ++g) {
+                const int step = it.step0 + c;
                 if (!wait(&s_full[t], g)) { ok = false; break; }
                 float sv[PF8_KEYS];
                 tc5_ld64u(tS, *reinterpret_cast<uint32_t(*)[PF8_KEYS]>(&sv[0]));
                 tc5_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free[t]);
-                if (c >= cmask) {
-                    const int nvis = lim - c * PF8_KEYS + 1;     // positions of this step the row sees
+                if (step >= cmask) {
+                    const int nvis = lim - step * PF8_KEYS + 1;     // positions of this step the row sees
 #pragma unroll
                     for (int e = 0; e < PF8_KEYS; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
                 }
@@ -446,24 +505,103 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             if (!ok) break;
 
             // -- O / l, in V's scale, into out (this thread's row)
-            if (!wait(&pv_done[t], g - 1)) { ok = false; break; }
-            const float inv = l_run > 0.f ? __ldg(p.v_scale + it.j) / l_run : 0.f;
+            if (g > 0 && !wait(&pv_done[t], g - 1)) { ok = false; break; }
             T *o = static_cast<T *>(p.out) + ((long long)(it.q0 + tok) * H + it.j * G + head) * D;
+            const float vsc = __ldg(p.v_scale + it.j);
+            auto write = [&](int c0, const float *v, float f) {    // 8 columns
+                uint4 w;
+                w.x = Mma<T>::pack(v[0] * f, v[1] * f);
+                w.y = Mma<T>::pack(v[2] * f, v[3] * f);
+                w.z = Mma<T>::pack(v[4] * f, v[5] * f);
+                w.w = Mma<T>::pack(v[6] * f, v[7] * f);
+                *reinterpret_cast<uint4 *>(o + c0) = w;
+            };
+            if constexpr (C == 1) {
+                const float inv = l_run > 0.f ? vsc / l_run : 0.f;
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                float v[32];
-                tc5_ld32(tO + c0, v);
-                if (row_ok) {
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float v[32];
+                    tc5_ld32(tO + c0, v);
+                    if (row_ok) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = Mma<T>::pack(v[e] * inv, v[e + 1] * inv);
-                        w.y = Mma<T>::pack(v[e + 2] * inv, v[e + 3] * inv);
-                        w.z = Mma<T>::pack(v[e + 4] * inv, v[e + 5] * inv);
-                        w.w = Mma<T>::pack(v[e + 6] * inv, v[e + 7] * inv);
-                        *reinterpret_cast<uint4 *>(o + c0 + e) = w;
+                        for (int e = 0; e < 32; e += 8) write(c0 + e, v + e, inv);
                     }
                 }
+            } else {
+                constexpr int DC = D / C;                          // columns of a block
+                constexpr int CH = DC < 32 ? DC : 32;              // of them at a time
+                const uint32_t xo = smem_u32(smem + Lay::OFF_XO + t * Lay::XO_BYTES) + 16 * r;
+                const uint32_t xs = smem_u32(smem + Lay::OFF_XS + t * Lay::XS_BYTES) + 8 * r;
+                // the other blocks have read the item before
+                if (kt > 0 && !wait_cluster(&x_free[t], kt - 1)) { ok = false; break; }
+#pragma unroll 1
+                for (int i = 1; i < C; ++i) {
+                    const int to = (rank + i) % C;                 // its columns of this row
+                    const uint32_t xoff = map_rank(xo, to) + (rank < to ? rank : rank - 1) * (DC * 512);
+                    if (it.nsteps > 0) {
+#pragma unroll
+                        for (int c0 = 0; c0 < DC; c0 += CH) {
+                            float v[32];
+                            tc5_ld32(tO + to * DC + c0, v);
+#pragma unroll
+                            for (int e = 0; e < CH; e += 4)
+                                st_dsmem_f32x4(xoff + (c0 + e) * 512, v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        }
+                    }
+                    st_dsmem_f32x2(map_rank(xs, to) + rank * 1024, m_run, l_run);
+                    fence_acq_rel_cluster();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&x_full[t]), to));
+                }
+                st_dsmem_f32x2(xs + rank * 1024, m_run, l_run);
+                if (!wait_cluster(&x_full[t], kt)) { ok = false; break; }
+                // the common level, each block's weight, and the sum
+                float w[C], M = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    const float2 ml = lds_f32x2(xs + i * 1024);
+                    w[i] = ml.y > 0.f ? ml.x : -INFINITY;
+                    M = fmaxf(M, w[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    w[i] = w[i] == -INFINITY ? 0.f : ex2(w[i] - M);
+                    sum = fmaf(w[i], lds_f32x2(xs + i * 1024).y, sum);
+                }
+                const float inv = sum > 0.f ? vsc / sum : 0.f;
+#pragma unroll
+                for (int c0 = 0; c0 < DC; c0 += CH) {
+                    float v[32], x[32];
+                    tc5_ld32(tO + rank * DC + c0, v);
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) x[e] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < C; ++i) {
+                        if (i == rank) {
+                            // nothing of this row here (or no step at all): O is not read
+#pragma unroll
+                            for (int e = 0; e < CH; ++e) x[e] = w[i] != 0.f ? fmaf(w[i], v[e], x[e]) : x[e];
+                        } else if (w[i] != 0.f) {
+                            const uint32_t from = xo + (i < rank ? i : i - 1) * (DC * 512) + c0 * 512;
+#pragma unroll
+                            for (int e = 0; e < CH; e += 4) {
+                                const float4 y = lds_f32x4(from + e * 512);
+                                x[e] = fmaf(w[i], y.x, x[e]);
+                                x[e + 1] = fmaf(w[i], y.y, x[e + 1]);
+                                x[e + 2] = fmaf(w[i], y.z, x[e + 2]);
+                                x[e + 3] = fmaf(w[i], y.w, x[e + 3]);
+                            }
+                        }
+                    }
+                    if (row_ok) {
+#pragma unroll
+                        for (int e = 0; e < CH; e += 8) write(rank * DC + c0 + e, x + e, inv);
+                    }
+                }
+                // the others may write the next item's rows
+                __syncwarp();
+                if (lane < C && lane != rank) mbar_arrive_cluster(map_rank(smem_u32(&x_free[t]), lane));
+                ++kt;
             }
             // O and S read before the next item's MMAs overwrite them (they wait for
             // this warp's next arrivals)
@@ -474,52 +612,93 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     tc5_fence_before_sync();
     __syncthreads();
     if (warp == 0) tc5_dealloc(tmem, 512);
+    if constexpr (C > 1) cluster_sync();   // no block leaves while a peer may write to it
 }
 
-template <typename T, int D, int G>
-cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, cudaStream_t st) {
-    constexpr size_t smem = PrefillF8Layout<D>::BYTES;
+template <typename T, int D, int G, int C>
+cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items, cudaStream_t st) {
+    constexpr size_t smem = PrefillF8Layout<D, C>::BYTES;
     static_assert(smem + sizeof(PrefillSched) + 1024 <= 227 * 1024, "shared memory");
-    auto kern = prefill_f8_kernel<T, D, G>;
-    static std::atomic<bool> attr_set[64];    // per device, read by any host thread
+    auto kern = prefill_f8_kernel<T, D, G, C>;
+    // clusters that fit on the device at once, found with the kernel's attributes set
+    static std::atomic<int> fitted[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
-    }
-    // one block per SM, but no more than the items can be: the worst case, and
-    // one more than the full items of each run (a run has at least
-    // PREFILL_GROUP_ROWS rows)
-    const long long worst = (long long)groups * p.num_seqs * p.num_kv_heads;
-    const long long rows_all = (long long)p.num_q_rows * G;
-    const long long bound = p.num_kv_heads * (rows_all / PF8_ROWS + rows_all / PREFILL_GROUP_ROWS + 1);
-    const int sms = sm_count_of_current_device();
-    long long blocks = sms > 0 ? sms : 152;
-    if (blocks > worst) blocks = worst;
-    if (blocks > bound) blocks = bound;
-    if (blocks <= 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
     cfg.blockDim = dim3(PF8_THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    int nc = dev >= 0 && dev < 64 ? fitted[dev].load(std::memory_order_acquire) : 0;
+    if (nc <= 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        nc = sm_count_of_current_device();
+        if (C > 1) {
+            cfg.gridDim = dim3(C * 64, 1, 1);
+            e = cudaOccupancyMaxActiveClusters(&nc, kern, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        if (nc < 1) nc = 1;
+        if (dev >= 0 && dev < 64) fitted[dev].store(nc, std::memory_order_release);
+    }
+    const long long blocks = (items < nc ? items : nc) * C;
+    if (blocks <= 0) return cudaSuccess;
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
     e = cudaLaunchKernelEx(&cfg, kern, p, groups);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
+// Blocks that share an item.  `items` bounds the items from above (their keys
+// are known on the device only).  A wave of the items takes as long as its
+// longest, so what counts is how full the last wave is: with few items, or few
+// waves, the split that fills the SMs best wins; sharing costs an exchange per
+// item, so the larger split has to be better by an eighth.
+#ifndef PA_PF8_CLUSTER
+#define PA_PF8_CLUSTER 0
+#endif
+inline int prefill_f8_split(long long items, int sms) {
+    if (PA_PF8_CLUSTER) return PA_PF8_CLUSTER;
+    int best = 1;
+    double best_t = 0.;
+    for (int c = 1; c <= 4; c *= 2) {
+        const long long slots = sms / c > 0 ? sms / c : 1;
+        const double t = (double)((items + slots - 1) / slots) / c;      // waves, in whole items
+        if (c == 1 || t * 1.125 < best_t) {
+            best = c;
+            best_t = t;
+        }
+    }
+    return best;
+}
+
 template <typename T>
 cudaError_t dispatch_prefill_f8(const DecodeParams &p, int D, int G, int groups, cudaStream_t st) {
-#define PA_CASE(DD, GG) \
-    if (D == DD && G == GG) return launch_prefill_f8<T, DD, GG>(p, groups, st);
+    // at most `groups` items a run, and one more than the full items of all rows
+    // for each run (a run has at least PREFILL_GROUP_ROWS rows)
+    const long long rows_all = (long long)p.num_q_rows * G;
+    long long runs = rows_all / PREFILL_GROUP_ROWS;
+    if (runs > p.num_seqs) runs = p.num_seqs;
+    long long items = rows_all / PF8_ROWS + runs;
+    if (items > groups * (long long)p.num_seqs) items = groups * (long long)p.num_seqs;
+    items *= p.num_kv_heads;
+    const int sms = sm_count_of_current_device();
+    const int split = prefill_f8_split(items, sms > 0 ? sms : 152);
+#define PA_CASE(DD, GG)                                                                        \
+    if (D == DD && G == GG)                                                                    \
+        return split == 1 ? launch_prefill_f8<T, DD, GG, 1>(p, groups, items, st)               \
+             : split == 2 ? launch_prefill_f8<T, DD, GG, 2>(p, groups, items, st)               \
+                          : launch_prefill_f8<T, DD, GG, 4>(p, groups, items, st);
     PA_CASE(64, 1) PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
     PA_CASE(128, 1) PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
 #undef PA_CASE
