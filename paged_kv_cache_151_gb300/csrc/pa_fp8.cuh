@@ -335,6 +335,12 @@ struct WarpAttnF8 {
 // layouts of WarpAttnF8.  Lane (g, t) scores rows g ("lo") and g + 8 ("hi");
 // the value product takes the rows as two tiles of eight columns, which share
 // the V fragments, so a block's codes are converted once for 16 rows.
+//
+// The scores of a block and its softmax and value product are two calls, so
+// that the scores of the next block run beside the softmax of this one.  A row's
+// reference level moves only when a score exceeds it by more than
+// 2^RESCALE_LOG2, and only then do its lanes exchange their maxima: (m, l, acc)
+// are to that level, not to the true maximum.
 template <typename T, int D>
 struct WarpAttnF8x16 {
     static_assert(sizeof(T) == 2, "q and out are 16-bit");
@@ -348,7 +354,7 @@ struct WarpAttnF8x16 {
     uint32_t qa[2 * KK][4];                // f16 A fragments, d permuted as in WarpAttnF8
     // acc[h][mt]: as WarpAttnF8::acc for rows 8h + 2t and 8h + 2t + 1
     float acc[2][MT][4];
-    float m_run[2], l_run[2], m_max[2];    // of rows g and g + 8
+    float m_run[2], l_run[2];              // level of rows g and g + 8; this lane's part of their sums
 
     __device__ __forceinline__ void init(int lane_) {
         lane = lane_;
@@ -361,7 +367,7 @@ struct WarpAttnF8x16 {
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            m_run[h] = m_max[h] = -INFINITY;
+            m_run[h] = -INFINITY;
             l_run[h] = 0.f;
 #pragma unroll
             for (int j = 0; j < MT; ++j)
@@ -370,10 +376,11 @@ struct WarpAttnF8x16 {
         }
     }
 
-    // query rows (nullptr: no such row) and their causal limits
-    __device__ __forceinline__ void load_q(const T *q_lo, const T *q_hi, int lo_lim, int hi_lim) {
-        lim[0] = q_lo ? lo_lim : -1;
-        lim[1] = q_hi ? hi_lim : -1;
+    // query rows (nullptr: no such row); their causal limits go to `lims`
+    __device__ __forceinline__ void load_q(const T *q_lo, const T *q_hi, int lo_lim, int hi_lim,
+                                           int (&lims)[2]) {
+        lims[0] = q_lo ? lo_lim : -1;
+        lims[1] = q_hi ? hi_lim : -1;
         const T *src[2] = {q_lo, q_hi};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -409,11 +416,15 @@ struct WarpAttnF8x16 {
         }
     }
 
-    // One block of E4M3 tiles whose row 0 is at sequence position pos0; V rows
-    // past the sequence's end are zero (zero_rows).  scale_log2 already
-    // carries K's scale.
-    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int pos0, float scale_log2) {
+    // Scores of a block: rows g and g + 8 against this lane's four tokens, in the
+    // order tokens PERM[2t], PERM[2t+1], 8 + those; four MMA chains of half the
+    // k-steps each.
+    struct Scores {
+        float v[2][4];
+    };
+    __device__ __forceinline__ Scores scores(uint32_t kt) const {
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        float s2[4] = {0.f, 0.f, 0.f, 0.f}, s3[4] = {0.f, 0.f, 0.f, 0.f};
         const int r0 = fp8_tile_token(g), r1 = 8 + r0;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
@@ -424,38 +435,57 @@ struct WarpAttnF8x16 {
                               f16x2_from_e4m3x2(k0.x >> 16));
             Mma<__half>::run4(s1, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k1.x),
                               f16x2_from_e4m3x2(k1.x >> 16));
-            Mma<__half>::run4(s0, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k0.y),
+            Mma<__half>::run4(s2, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k0.y),
                               f16x2_from_e4m3x2(k0.y >> 16));
-            Mma<__half>::run4(s1, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k1.y),
+            Mma<__half>::run4(s3, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k1.y),
                               f16x2_from_e4m3x2(k1.y >> 16));
         }
+        return Scores{{{s0[0] + s2[0], s0[1] + s2[1], s1[0] + s3[0], s1[1] + s3[1]},
+                       {s0[2] + s2[2], s0[3] + s2[3], s1[2] + s3[2], s1[3] + s3[3]}}};
+    }
+
+    // Softmax and value product of a block whose row 0 is at sequence position
+    // pos0; V rows past the sequence's end are zero (zero_rows).  scale_log2
+    // already carries K's scale.
+    __device__ __forceinline__ void values(const Scores &sv, uint32_t vt, int pos0, float scale_log2) {
         const int ta = fp8_tile_token(2 * t), tb = fp8_tile_token(2 * t + 1);
-        const int pos[4] = {pos0 + ta, pos0 + tb, pos0 + 8 + ta, pos0 + 8 + tb};
+        float sc[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[h][e] = sv.v[h][e] * scale_log2;
+        if (__any_sync(0xffffffffu, pos0 + 15 > min(lim[0], lim[1]))) {
+            const int pos[4] = {pos0 + ta, pos0 + tb, pos0 + 8 + ta, pos0 + 8 + tb};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[h][e] = pos[e] <= lim[h] ? sc[h][e] : -INFINITY;
+        }
+        float mx[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mx[h] = fmaxf(max3f(sc[h][0], sc[h][1], sc[h][2]), sc[h][3]);
+        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + RESCALE_LOG2 || mx[1] > m_run[1] + RESCALE_LOG2)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                const float m_new = mx[h] > m_run[h] + RESCALE_LOG2 ? mx[h] : m_run[h];
+                const float alpha = m_new == m_run[h] ? 1.f : ex2(m_run[h] - m_new);
+                m_run[h] = m_new;
+                l_run[h] *= alpha;
+                rescale(h, alpha);
+            }
+        }
         uint32_t pb[2][2];                 // B fragments of the two row tiles
-        float alpha[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float sc[4] = {s0[2 * h], s0[2 * h + 1], s1[2 * h], s1[2 * h + 1]};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[e] = pos[e] <= lim[h] ? sc[e] * scale_log2 : -INFINITY;
-            float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            m_max[h] = fmaxf(m_max[h], mx);
-            const float m_new = mx > m_run[h] + RESCALE_LOG2 ? mx : m_run[h];   // lazy rescaling
-            const float ms = m_new == -INFINITY ? 0.f : m_new;
-            alpha[h] = ex2(m_run[h] - ms);
-            pb[h][0] = Mma<__half>::pack(ex2(sc[0] - ms), ex2(sc[1] - ms));
-            pb[h][1] = Mma<__half>::pack(ex2(sc[2] - ms), ex2(sc[3] - ms));
+            const float ms = m_run[h] == -INFINITY ? 0.f : m_run[h];   // a row that sees nothing yet
+            pb[h][0] = Mma<__half>::pack(ex2(sc[h][0] - ms), ex2(sc[h][1] - ms));
+            pb[h][1] = Mma<__half>::pack(ex2(sc[h][2] - ms), ex2(sc[h][3] - ms));
             float p0, p1, p2, p3;
             Mma<__half>::unpack(pb[h][0], p0, p1);
             Mma<__half>::unpack(pb[h][1], p2, p3);
-            l_run[h] = l_run[h] * alpha[h] + ((p0 + p1) + (p2 + p3));
-            m_run[h] = m_new;
-        }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-            rescale(0, alpha[0]);
-            rescale(1, alpha[1]);
+            l_run[h] += (p0 + p1) + (p2 + p3);
         }
         // A fragments of V^T: d rows 2mt (a0, a2) and 2mt + 1 (a1, a3) of this
         // lane's run of DL bytes, tokens ta, tb (a0, a1) and 8 + ta, 8 + tb
@@ -494,21 +524,10 @@ struct WarpAttnF8x16 {
         WarpAttnF8<T, D, 1>::zero_rows(vt, rows, lane);
     }
 
-    // Bring the state to the true maximum, then sum the lanes of each row.
+    // Sum the lanes of each row.
     __device__ __forceinline__ void finish() {
-        float f[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            f[h] = m_max[h] == -INFINITY ? 1.f
-                                         : ex2((m_run[h] == -INFINITY ? m_max[h] : m_run[h]) - m_max[h]);
-        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-            rescale(0, f[0]);
-            rescale(1, f[1]);
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            l_run[h] *= f[h];
-            m_run[h] = m_max[h];
             l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 1);
             l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 2);
         }

@@ -316,6 +316,13 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     constexpr bool PARTIAL = MODE == MODE_PARTITIONED;
     constexpr bool MQ = MODE == MODE_MULTI;
     constexpr int ROWS = rows_of_mode(MODE, G);
+    // A unit that several warps share is merged by the last of them to arrive.
+    // With 16 rows of E4M3 queries in more than SPREAD_PARTS partials the warps
+    // of the cluster merge it together instead, a row each, once all are done: one
+    // warp would read 16 partials of 16 rows through distributed shared memory,
+    // some 25 us of a batch of one.
+    constexpr bool SPREAD = F8 && MQ;
+    constexpr int SPREAD_PARTS = 4;
     static_assert(!MQ || TC, "multi-token queries use the tensor-core path");
     static_assert(F8 || std::is_same<KV, T>::value, "cache type");
     static_assert(!F8 || TC, "E4M3 caches: 16-bit q");
@@ -874,6 +881,8 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         }
         __syncwarp();
         wa.reset();
+        if (SPREAD && shared_unit >= 0 && parts_of(shared_unit) > SPREAD_PARTS)
+            shared_unit = -1;                      // merged at the end, by all warps
         if (!at_end) {
             // only the range's first unit can be shared and end inside it
             if (shared_unit >= 0) pending = shared_unit;
@@ -896,85 +905,173 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         pending = -1;
     };
 
+    // Row r of unit u's sequence: its (token r / G, head r % G), token i seeing
+    // positions up to L - nq + i; this lane holds rows g and g + 8 of the
+    // unit's 16-row tile.
+    auto q_row = [&](const UnitRec &u, int r) -> const T * {
+        if (r >= u.nq * G) return nullptr;
+        return reinterpret_cast<const T *>(p.q) + (long long)(u.q0 + r / G) * p.q_seq_stride +
+               (long long)(u.j * G + r % G) * D;
+    };
+
     int cur = -1, qnext = -1;                      // unit whose query is loaded ahead
     float unit_scale = p.scale_log2;               // score scale (x K's scale for E4M3)
     int k_done = 0;
     bool ok = true;
-    for (int k = 0; k < n_mine; ++k) {
-        if (k - c0 == 32) {
-            c0 += 32;
-            ui_cur = ui_nxt;
-            pb_cur = pb_nxt;
-            fetch(c0 + 32 + lane, ui_nxt, pb_nxt);
-        }
-        int ui, pbk;
-        of(k, ui, pbk);
-        if (ui != cur) {
-            if (cur >= 0) leave_unit(cur, false);
-            cur = ui;
-            if constexpr (MQ) {
-                // this lane's rows g and g + 8 of the unit's 16-row tile:
-                // (token i, head) pairs, token i seeing positions up to L - nq + i
-                const UnitRec &u = units[ui];
-                const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
-                auto qrow = [&](int r) -> const T * {
-                    if (r >= u.nq * G) return nullptr;
-                    return reinterpret_cast<const T *>(p.q) +
-                           (long long)(u.q0 + r / G) * p.q_seq_stride +
-                           (long long)(u.j * G + r % G) * D;
-                };
-                wa.load_q(qrow(r_lo), qrow(r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
-                if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
-            } else {
-                auto qptr = [&](int q) {
-                    const UnitRec &u = units[q];
-                    return reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
-                           (long long)u.j * G * D;
-                };
-                if (qnext != ui) wa.prefetch_q(qptr(ui));
-                if constexpr (TC) wa.take_q();
-                else wa.take_q(p.scale_log2);
-                if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + units[ui].j);
-                // load the next unit's query while this one streams
-                qnext = -1;
-                if (ui + 1 < nu && cum[ui + 1] < my_hi && units[ui + 1].nb > 0) {
-                    qnext = ui + 1;
-                    wa.prefetch_q(qptr(qnext));
-                }
+    if constexpr (SPREAD) {
+        // 16-row tiles over E4M3 caches: the scores of block k + 1 are issued before
+        // the softmax and value product of block k (92 -> see below us for 256
+        // sequences of four rows), so the matrix instructions of one run beside
+        // the exchanges and exponentials of the other
+        auto stage_of = [&](int k) { return my_stages + (size_t)(k % S) * 2 * TILE; };
+        auto wait_stage = [&](int k) -> bool {
+            const bool w = mbar_wait_bounded(&my_bars[k % S], (uint32_t)((k / S) & 1), p.err);
+            return __all_sync(0xffffffffu, w);
+        };
+        // block k: its unit, its position and whether it can be read
+        int ui = -1, pbk = 0, pos = 0;
+        bool good = false;
+        int lims[2] = {-1, -1};
+        float next_scale = 0.f;
+        typename W::Scores sv = {};
+        // move to block k (the one after the present one, or the first): returns
+        // false after a timeout
+        auto enter = [&](int k, int &ui_k, int &pos_k, bool &good_k, typename W::Scores &sv_k) -> bool {
+            if (k - c0 == 32) {
+                c0 += 32;
+                ui_cur = ui_nxt;
+                pb_cur = pb_nxt;
+                fetch(c0 + 32 + lane, ui_nxt, pb_nxt);
             }
+            of(k, ui_k, pbk);
+            if (ui_k != ui) {
+                const UnitRec &u = units[ui_k];
+                const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
+                wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G, lims);
+                next_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
+                pos_k = pos_of(k, ui_k);
+            } else {
+                pos_k = pos + 16;
+            }
+            if (!wait_stage(k)) return false;
+            k_done = k + 1;
+            good_k = pbk >= 0 && (long long)pbk < p.num_blocks;
+            if (good_k) sv_k = wa.scores(smem_u32(stage_of(k)));
+            return true;
+        };
+        if (n_mine > 0) {
+            int first = -1;
+            ok = enter(0, first, pos, good, sv);
+            cur = ui = first;
+            wa.lim[0] = lims[0];
+            wa.lim[1] = lims[1];
+            unit_scale = next_scale;
         }
-        const int st = k % S;
-        const bool waited = mbar_wait_bounded(&my_bars[st], (uint32_t)((k / S) & 1), p.err);
-        if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
-        k_done = k + 1;
-        if (pbk >= 0 && (long long)pbk < p.num_blocks) {
-            unsigned char *Kt = my_stages + (size_t)st * 2 * TILE;
-            const int rows = rows_of(k, ui);
-            if constexpr (TC) {
-                // tail rows hold other tokens' data: the one-token block math
-                // drops them in registers; the others clear them in the tile
-                if (F8 || MQ) {
-                    if (rows < 16) {
-                        if constexpr (F8) W::zero_rows(Kt + TILE, rows, lane);
-                        else WarpAttnTC<T, D, G>::zero_rows(Kt + TILE, rows, lane);
-                        // these generic writes must be ordered before the next
-                        // bulk copy into the stage
-                        fence_proxy_async_smem();
-                        __syncwarp();
+        for (int k = 0; ok && k < n_mine; ++k) {
+            int ui_n = ui, pos_n = 0;
+            bool good_n = false;
+            typename W::Scores sv_n = {};
+            if (k + 1 < n_mine && !enter(k + 1, ui_n, pos_n, good_n, sv_n)) {
+                ok = false;
+                break;
+            }
+            if (good) {
+                unsigned char *Vt = stage_of(k) + TILE;
+                const int rows = min(16, units[ui].L - pos);
+                if (rows < 16) {                   // other tokens' data behind the sequence
+                    W::zero_rows(Vt, rows, lane);
+                    fence_proxy_async_smem();      // before the next copy into the stage
+                    __syncwarp();
+                }
+                wa.values(sv, smem_u32(Vt), pos, unit_scale);
+            }
+            __syncwarp();                          // every lane is done with the stage
+            const int kn = k + S;
+            if (kn < n_mine) {
+                int uin, pbn;
+                of(kn, uin, pbn);
+                if (lane == 0) issue(kn, uin, pbn);
+            }
+            if (ui_n != ui) {
+                leave_unit(ui, false);
+                cur = ui_n;
+                wa.lim[0] = lims[0];
+                wa.lim[1] = lims[1];
+                unit_scale = next_scale;
+            }
+            ui = ui_n;
+            pos = pos_n;
+            good = good_n;
+            sv = sv_n;
+        }
+    } else {
+        for (int k = 0; k < n_mine; ++k) {
+            if (k - c0 == 32) {
+                c0 += 32;
+                ui_cur = ui_nxt;
+                pb_cur = pb_nxt;
+                fetch(c0 + 32 + lane, ui_nxt, pb_nxt);
+            }
+            int ui, pbk;
+            of(k, ui, pbk);
+            if (ui != cur) {
+                if (cur >= 0) leave_unit(cur, false);
+                cur = ui;
+                if constexpr (MQ) {
+                    const UnitRec &u = units[ui];
+                    const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
+                    wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
+                } else {
+                    auto qptr = [&](int q) {
+                        const UnitRec &u = units[q];
+                        return reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
+                               (long long)u.j * G * D;
+                    };
+                    if (qnext != ui) wa.prefetch_q(qptr(ui));
+                    if constexpr (TC) wa.take_q();
+                    else wa.take_q(p.scale_log2);
+                    if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + units[ui].j);
+                    // load the next unit's query while this one streams
+                    qnext = -1;
+                    if (ui + 1 < nu && cum[ui + 1] < my_hi && units[ui + 1].nb > 0) {
+                        qnext = ui + 1;
+                        wa.prefetch_q(qptr(qnext));
                     }
                 }
-                if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
-                else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
-            } else {
-                wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
             }
-        }
-        __syncwarp();                              // every lane is done with the stage
-        const int kn = k + S;
-        if (kn < n_mine) {
-            int uin, pbn;
-            of(kn, uin, pbn);
-            if (lane == 0) issue(kn, uin, pbn);
+            const int st = k % S;
+            const bool waited = mbar_wait_bounded(&my_bars[st], (uint32_t)((k / S) & 1), p.err);
+            if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
+            k_done = k + 1;
+            if (pbk >= 0 && (long long)pbk < p.num_blocks) {
+                unsigned char *Kt = my_stages + (size_t)st * 2 * TILE;
+                const int rows = rows_of(k, ui);
+                if constexpr (TC) {
+                    // tail rows hold other tokens' data: the one-token block math
+                    // drops them in registers; the others clear them in the tile
+                    if (F8 || MQ) {
+                        if (rows < 16) {
+                            if constexpr (F8) W::zero_rows(Kt + TILE, rows, lane);
+                            else WarpAttnTC<T, D, G>::zero_rows(Kt + TILE, rows, lane);
+                            // these generic writes must be ordered before the next
+                            // bulk copy into the stage
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), p.scale_log2);
+                    else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
+                } else {
+                    wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
+                }
+            }
+            __syncwarp();                              // every lane is done with the stage
+            const int kn = k + S;
+            if (kn < n_mine) {
+                int uin, pbn;
+                of(kn, uin, pbn);
+                if (lane == 0) issue(kn, uin, pbn);
+            }
         }
     }
     // a timeout leaves the unit unmerged (its output is not written; the
@@ -983,10 +1080,78 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     // accesses to peers' shared memory follow)
     if (C > 1) cluster_wait();
     if (ok && cur >= 0) leave_unit(cur, true);
+    if constexpr (SPREAD) {
+        // The units in more than SPREAD_PARTS partials, by the warp that they start
+        // in (the same list in every block of the cluster).
+        auto spread_at = [&](int w0) -> int {      // unit, or -1
+            const int lo = range_lo(w0), hi = range_lo(w0 + 1);
+            if (lo == hi) return -1;
+            const int ui = locate(hi - 1);
+            if (cum[ui] + units[ui].nb <= hi || cum[ui] < lo) return -1;   // ends here, or starts before
+            return parts_of(ui) > SPREAD_PARTS ? ui : -1;
+        };
+        bool any = false;
+        for (int w0 = lane; w0 < NWC; w0 += 32) any = any || spread_at(w0) >= 0;
+        if (__any_sync(0xffffffffu, any)) {
+            // arrive[w] < 0: warp w of this block did not finish its range
+            if (lane == 0 && !ok) atomicExch(&arrive[warp], -(1 << 30));
+            __syncthreads();
+            if (C > 1) cluster_sync();             // every partial of the cluster is parked
+            for (int w0 = 0; w0 < NWC; ++w0) {
+                const int ui = spread_at(w0);
+                if (ui < 0) continue;
+                const UnitRec u = units[ui];
+                const int w1 = owner(cum[ui] + u.nb - 1);
+                for (int r = gw; r < ROWS; r += NWC) {     // row r of the tile
+                    const long long row = out_row(u, r);
+                    if (row < 0) continue;
+                    constexpr int V = D / 32;      // outputs of a lane
+                    constexpr int AHEAD = 4;       // partials in flight
+                    float M = -INFINITY, Ls = 0.f, O[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) O[e] = 0.f;
+                    bool whole = true;
+                    for (int wb = w0; wb <= w1; wb += AHEAD) {
+                        float mw[AHEAD], lw[AHEAD], ow[AHEAD][V];
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i) {
+                            const int w = wb + i;
+                            mw[i] = -INFINITY;
+                            if (w > w1 || range_lo(w) == range_lo(w + 1)) continue;
+                            const float *pw = part_of(w, (w == w1 && w != w0) ? 0 : 1);
+                            const uint32_t rw = (uint32_t)(w / NW);
+                            whole = whole && ld_acquire_dsmem_s32(map_to_rank(&arrive[w % NW], rw)) >= 0;
+                            mw[i] = ld_dsmem_f32(map_to_rank(pw + ROWS * D + r, rw));
+                            lw[i] = ld_dsmem_f32(map_to_rank(pw + ROWS * D + ROWS + r, rw));
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                ow[i][e] = ld_dsmem_f32(map_to_rank(pw + r * D + lane + 32 * e, rw));
+                        }
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i) {
+                            if (mw[i] == -INFINITY) continue;      // no partial, or nothing seen
+                            const float Mn = fmaxf(M, mw[i]);
+                            const float a = M == -INFINITY ? 0.f : ex2(M - Mn), b = ex2(mw[i] - Mn);
+                            Ls = fmaf(b, lw[i], Ls * a);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) O[e] = fmaf(b, ow[i][e], O[e] * a);
+                            M = Mn;
+                        }
+                    }
+                    if (!whole) continue;          // one of its warps timed out
+                    const float inv = Ls > 0.f ? v_scale_of(u) / Ls : 0.f;
+                    T *o = reinterpret_cast<T *>(p.out) + row * D + lane;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) Elem<T>::store1(o + 32 * e, O[e] * inv);
+                }
+            }
+        }
+    }
 
     // after a timeout: wait (bounded) for this warp's copies still in flight
     if (!ok) {
-        const int issued = min(n_mine, k_done + S);
+        // (the E4M3 multi-token loop is one block ahead of its copies)
+        const int issued = min(n_mine, S + (SPREAD ? max(k_done - 1, 0) : k_done));
         for (int k = k_done; k < issued; ++k)
             mbar_wait_bounded(&my_bars[k % S], (uint32_t)((k / S) & 1), p.err);
     }

@@ -615,19 +615,51 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     if constexpr (C > 1) cluster_sync();   // no block leaves while a peer may write to it
 }
 
+// Clusters of C blocks that the device holds at once (blocks for C = 1), with the
+// kernel's attributes set; looked up once per device.
 template <typename T, int D, int G, int C>
-cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items, cudaStream_t st) {
+cudaError_t prefill_f8_fit(int *clusters) {
     constexpr size_t smem = PrefillF8Layout<D, C>::BYTES;
     static_assert(smem + sizeof(PrefillSched) + 1024 <= 227 * 1024, "shared memory");
     auto kern = prefill_f8_kernel<T, D, G, C>;
-    // clusters that fit on the device at once, found with the kernel's attributes set
     static std::atomic<int> fitted[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    int nc = dev >= 0 && dev < 64 ? fitted[dev].load(std::memory_order_acquire) : 0;
+    if (nc <= 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        nc = sm_count_of_current_device();
+        if (C > 1) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(C * 64, 1, 1);
+            cfg.blockDim = dim3(PF8_THREADS, 1, 1);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = C;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&nc, kern, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        if (nc < 1) nc = 1;
+        if (dev >= 0 && dev < 64) fitted[dev].store(nc, std::memory_order_release);
+    }
+    *clusters = nc;
+    return cudaSuccess;
+}
+
+template <typename T, int D, int G, int C>
+cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items, int clusters,
+                              cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((items < clusters ? items : clusters) * C), 1, 1);
     cfg.blockDim = dim3(PF8_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = PrefillF8Layout<D, C>::BYTES;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -638,48 +670,35 @@ cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    int nc = dev >= 0 && dev < 64 ? fitted[dev].load(std::memory_order_acquire) : 0;
-    if (nc <= 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        nc = sm_count_of_current_device();
-        if (C > 1) {
-            cfg.gridDim = dim3(C * 64, 1, 1);
-            e = cudaOccupancyMaxActiveClusters(&nc, kern, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-        if (nc < 1) nc = 1;
-        if (dev >= 0 && dev < 64) fitted[dev].store(nc, std::memory_order_release);
-    }
-    const long long blocks = (items < nc ? items : nc) * C;
-    if (blocks <= 0) return cudaSuccess;
-    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    e = cudaLaunchKernelEx(&cfg, kern, p, groups);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_f8_kernel<T, D, G, C>, p, groups);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 // Blocks that share an item.  `items` bounds the items from above (their keys
-// are known on the device only).  A wave of the items takes as long as its
-// longest, so what counts is how full the last wave is: with few items, or few
-// waves, the split that fills the SMs best wins; sharing costs an exchange per
-// item, so the larger split has to be better by an eighth.
-#ifndef PA_PF8_CLUSTER
-#define PA_PF8_CLUSTER 0
-#endif
-inline int prefill_f8_split(long long items, int sms) {
-    if (PA_PF8_CLUSTER) return PA_PF8_CLUSTER;
-    int best = 1;
+// are known on the device only).  A wave of items takes as long as its longest,
+// so what counts is how full the last wave is: with few items the split that
+// fills the SMs wins.  Sharing costs an exchange per item and stages, so the
+// larger split has to be better by an eighth.
+template <typename T, int D, int G>
+cudaError_t run_prefill_f8(const DecodeParams &p, int groups, long long items, cudaStream_t st) {
+    int fit[3];
+    cudaError_t e = prefill_f8_fit<T, D, G, 1>(&fit[0]);
+    if (e == cudaSuccess) e = prefill_f8_fit<T, D, G, 2>(&fit[1]);
+    if (e == cudaSuccess) e = prefill_f8_fit<T, D, G, 4>(&fit[2]);
+    if (e != cudaSuccess) return e;
+    int best = 0;
     double best_t = 0.;
-    for (int c = 1; c <= 4; c *= 2) {
-        const long long slots = sms / c > 0 ? sms / c : 1;
-        const double t = (double)((items + slots - 1) / slots) / c;      // waves, in whole items
-        if (c == 1 || t * 1.125 < best_t) {
-            best = c;
+    for (int i = 0; i < 3; ++i) {
+        const double t = (double)((items + fit[i] - 1) / fit[i]) / (1 << i);     // waves, in whole items
+        if (i == 0 || t * 1.125 < best_t) {
+            best = i;
             best_t = t;
         }
     }
-    return best;
+    if (best == 0) return launch_prefill_f8<T, D, G, 1>(p, groups, items, fit[0], st);
+    if (best == 1) return launch_prefill_f8<T, D, G, 2>(p, groups, items, fit[1], st);
+    return launch_prefill_f8<T, D, G, 4>(p, groups, items, fit[2], st);
 }
 
 template <typename T>
@@ -692,13 +711,9 @@ cudaError_t dispatch_prefill_f8(const DecodeParams &p, int D, int G, int groups,
     long long items = rows_all / PF8_ROWS + runs;
     if (items > groups * (long long)p.num_seqs) items = groups * (long long)p.num_seqs;
     items *= p.num_kv_heads;
-    const int sms = sm_count_of_current_device();
-    const int split = prefill_f8_split(items, sms > 0 ? sms : 152);
-#define PA_CASE(DD, GG)                                                                        \
-    if (D == DD && G == GG)                                                                    \
-        return split == 1 ? launch_prefill_f8<T, DD, GG, 1>(p, groups, items, st)               \
-             : split == 2 ? launch_prefill_f8<T, DD, GG, 2>(p, groups, items, st)               \
-                          : launch_prefill_f8<T, DD, GG, 4>(p, groups, items, st);
+    if (items <= 0) return cudaSuccess;
+#define PA_CASE(DD, GG) \
+    if (D == DD && G == GG) return run_prefill_f8<T, DD, GG>(p, groups, items, st);
     PA_CASE(64, 1) PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
     PA_CASE(128, 1) PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
 #undef PA_CASE
