@@ -330,6 +330,16 @@ struct WarpAttnF8 {
     }
 };
 
+// d += a . b on the f16 tensor cores, free for the compiler to schedule among
+// the conversions that feed its neighbours.
+__device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Sixteen query rows at once: the (query token, head) pairs of a multi-token
 // query that share one KV head, each with its own causal limit, in the
 // layouts of WarpAttnF8.  Lane (g, t) scores rows g ("lo") and g + 8 ("hi");
@@ -426,18 +436,23 @@ struct WarpAttnF8x16 {
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
         float s2[4] = {0.f, 0.f, 0.f, 0.f}, s3[4] = {0.f, 0.f, 0.f, 0.f};
         const int r0 = fp8_tile_token(g), r1 = 8 + r0;
+        uint2 kc[2][KK];
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            const uint2 k0 = lds64(kt + fp8_swz<D>(r0, 32 * kk + 8 * t));
-            const uint2 k1 = lds64(kt + fp8_swz<D>(r1, 32 * kk + 8 * t));
+            kc[0][kk] = lds64(kt + fp8_swz<D>(r0, 32 * kk + 8 * t));
+            kc[1][kk] = lds64(kt + fp8_swz<D>(r1, 32 * kk + 8 * t));
+        }
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            const uint2 k0 = kc[0][kk], k1 = kc[1][kk];
             const uint32_t *a = qa[2 * kk], *b = qa[2 * kk + 1];
-            Mma<__half>::run4(s0, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k0.x),
+            mma_f16(s0, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k0.x),
                               f16x2_from_e4m3x2(k0.x >> 16));
-            Mma<__half>::run4(s1, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k1.x),
+            mma_f16(s1, a[0], a[1], a[2], a[3], f16x2_from_e4m3x2(k1.x),
                               f16x2_from_e4m3x2(k1.x >> 16));
-            Mma<__half>::run4(s2, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k0.y),
+            mma_f16(s2, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k0.y),
                               f16x2_from_e4m3x2(k0.y >> 16));
-            Mma<__half>::run4(s3, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k1.y),
+            mma_f16(s3, b[0], b[1], b[2], b[3], f16x2_from_e4m3x2(k1.y),
                               f16x2_from_e4m3x2(k1.y >> 16));
         }
         return Scores{{{s0[0] + s2[0], s0[1] + s2[1], s1[0] + s3[0], s1[1] + s3[1]},
@@ -500,12 +515,12 @@ struct WarpAttnF8x16 {
             const uint32_t hi01 = prmt(wc[w], wd[w], 0x5140), hi23 = prmt(wc[w], wd[w], 0x7362);
             const uint32_t a0 = f16x2_from_e4m3x2(lo01), a1 = f16x2_from_e4m3x2(lo01 >> 16);
             const uint32_t a2 = f16x2_from_e4m3x2(hi01), a3 = f16x2_from_e4m3x2(hi01 >> 16);
-            Mma<__half>::run4(acc[0][2 * w], a0, a1, a2, a3, pb[0][0], pb[0][1]);
-            Mma<__half>::run4(acc[1][2 * w], a0, a1, a2, a3, pb[1][0], pb[1][1]);
+            mma_f16(acc[0][2 * w], a0, a1, a2, a3, pb[0][0], pb[0][1]);
+            mma_f16(acc[1][2 * w], a0, a1, a2, a3, pb[1][0], pb[1][1]);
             const uint32_t c0 = f16x2_from_e4m3x2(lo23), c1 = f16x2_from_e4m3x2(lo23 >> 16);
             const uint32_t c2 = f16x2_from_e4m3x2(hi23), c3 = f16x2_from_e4m3x2(hi23 >> 16);
-            Mma<__half>::run4(acc[0][2 * w + 1], c0, c1, c2, c3, pb[0][0], pb[0][1]);
-            Mma<__half>::run4(acc[1][2 * w + 1], c0, c1, c2, c3, pb[1][0], pb[1][1]);
+            mma_f16(acc[0][2 * w + 1], c0, c1, c2, c3, pb[0][0], pb[0][1]);
+            mma_f16(acc[1][2 * w + 1], c0, c1, c2, c3, pb[1][0], pb[1][1]);
         }
     }
 

@@ -920,9 +920,8 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     bool ok = true;
     if constexpr (SPREAD) {
         // 16-row tiles over E4M3 caches: the scores of block k + 1 are issued before
-        // the softmax and value product of block k (92 -> see below us for 256
-        // sequences of four rows), so the matrix instructions of one run beside
-        // the exchanges and exponentials of the other
+        // the softmax and value product of block k, so the matrix instructions of
+        // one run beside the exchanges and exponentials of the other
         auto stage_of = [&](int k) { return my_stages + (size_t)(k % S) * 2 * TILE; };
         auto wait_stage = [&](int k) -> bool {
             const bool w = mbar_wait_bounded(&my_bars[k % S], (uint32_t)((k / S) & 1), p.err);
