@@ -7,10 +7,11 @@
 // accepted from w = p of the row behind the last one: the first v whose
 // cumulative weight C_v exceeds u W (W the row's sum).  The vocabulary's
 // cumulative sums decide a whole number, and a row has 10^4 to 10^5 borders that
-// u W can fall next to, so a sum is a pair of floats (the rounding error of
-// every addition is kept and added up beside it: about 46 bits) up to a warp's
-// run of the row, and binary64 above.  Binary64 throughout costs more than the
-// row's traffic: the GPU adds about two a clock and SM.
+// u W can fall next to, so every sum is a pair of floats (the rounding error of
+// every addition is kept and added up beside it: about 46 bits), as Knuth's
+// two-sum gives it without a comparison.  Binary64 would be simpler and
+// costs more than the row's traffic: a batch of 64 over 131071 tokens spent
+// 5 of its 19 us in the 16 binary64 steps that one warp took.
 //
 // Bound by HBM for batches (one or two rows of the vocabulary per sequence),
 // by latency for one sequence.  A cluster of C blocks takes one sequence: the
@@ -61,51 +62,110 @@ struct Pair {
     __device__ __forceinline__ bool above(const Pair &o) const { return (hi - o.hi) + (lo - o.lo) > 0.f; }
 };
 
+__device__ __forceinline__ Pair shfl(const Pair &a, int src) {
+    return Pair{__shfl_sync(0xffffffffu, a.hi, src), __shfl_sync(0xffffffffu, a.lo, src)};
+}
 __device__ __forceinline__ Pair shfl_xor(const Pair &a, int o) {
     return Pair{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
 }
-__device__ __forceinline__ Pair shfl_up(const Pair &a, int o) {
-    return Pair{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
-}
-__device__ __forceinline__ Pair pair_of(double x) {
-    const float hi = (float)x;
-    return Pair{hi, (float)(x - (double)hi)};
+// Inclusive sums over the first W lanes; *before: the lanes below this one.
+template <int W>
+__device__ __forceinline__ Pair scan(const Pair &a, int lane, Pair *before) {
+    Pair inc = a;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const Pair y{__shfl_up_sync(0xffffffffu, inc.hi, o), __shfl_up_sync(0xffffffffu, inc.lo, o)};
+        if (lane >= o) inc.add(y);
+    }
+    *before = Pair{__shfl_up_sync(0xffffffffu, inc.hi, 1), __shfl_up_sync(0xffffffffu, inc.lo, 1)};
+    if (lane == 0) *before = Pair{0.f, 0.f};
+    return inc;
 }
 
-// This lane's part of the weights of [lo, hi): elements lane, lane + 32, ...,
-// U of them in flight.
-template <typename T, bool TWO, int U>
-__device__ __forceinline__ Pair sum_run(const Row<T> &row, int64_t lo, int64_t hi, int lane) {
-    Pair acc{0.f, 0.f};
-    const T *p = row.p + lo + lane, *q = TWO ? row.q + lo + lane : nullptr;
-    const int64_t hole = row.hole - lo - lane;
-    const int n = (int)(hi - lo) - lane;            // elements from this lane on
-    for (int i = 0; i < n; i += 32 * U) {
-        float x[U], y[U];
-#pragma unroll
-        for (int e = 0; e < U; ++e) {
-            const bool in = i + 32 * e < n;
-            x[e] = in ? Elem<T>::load1(p + i + 32 * e) : 0.f;
-            y[e] = TWO && in ? Elem<T>::load1(q + i + 32 * e) : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < U; ++e) {
-            const float w = weight_of(x[e], y[e]);
-            acc.add(i + 32 * e == hole ? 0.f : w);
-        }
+// u q < p for u, p, q >= 0, exactly: the product's rounding error is one fma
+// away where it does not underflow.
+__device__ __forceinline__ bool product_below(float u, float q, float p) {
+    if (u > 0x1p-60f && q > 0x1p-60f) {
+        const float h = u * q, e = fmaf(u, q, -h);
+        return h < p || (h == p && e < 0.f);
     }
+    return (double)u * (double)q < (double)p;
+}
+
+// Two Pairs in the packed arithmetic: x - y as fma(y, -1, x), rounded once.
+struct Pair2 {
+    float2 hi, lo;
+    __device__ __forceinline__ static float2 sub(float2 x, float2 y) {
+        return fma2(y, make_float2(-1.f, -1.f), x);
+    }
+    __device__ __forceinline__ void add(float2 x) {
+        const float2 s = add2(hi, x), z = sub(s, hi);
+        lo = add2(lo, add2(sub(hi, sub(s, z)), sub(x, z)));
+        hi = s;
+    }
+    __device__ __forceinline__ Pair sum() const {
+        Pair r{hi.x, lo.x};
+        r.add(Pair{hi.y, lo.y});
+        return r;
+    }
+};
+
+// This lane's part of the weights of n elements: lane + 32 i, 2 U of them in
+// flight.  Element `hole` (one row only) is left out.  Infinite entries are not
+// dropped here: they make the sum infinite or NaN, which the caller looks for.
+template <typename T, bool TWO, int U>
+__device__ __forceinline__ Pair sum_run(const T *p, const T *q, int n, int hole, int lane) {
+    Pair2 acc{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    constexpr int STEP = 64 * U;
+    p += lane;
+    q += lane;
+    n -= lane;
+    hole -= lane;
+    auto step = [&](int at, auto &&in) {
+        T x[2 * U];
+        [[maybe_unused]] T y[2 * U];
+#pragma unroll
+        for (int e = 0; e < 2 * U; ++e) {
+            x[e] = in(at + 32 * e) ? p[at + 32 * e] : T(0.f);
+            if constexpr (TWO) y[e] = in(at + 32 * e) ? q[at + 32 * e] : T(0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < 2 * U; e += 2) {
+            float2 w = make_float2((float)x[e], (float)x[e + 1]);
+            if constexpr (TWO)
+                w = Pair2::sub(w, make_float2(fmaxf((float)y[e], 0.f), fmaxf((float)y[e + 1], 0.f)));
+            w = make_float2(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f));
+            if constexpr (!TWO) {
+                w.x = at + 32 * e == hole ? 0.f : w.x;
+                w.y = at + 32 * e + 32 == hole ? 0.f : w.y;
+            }
+            acc.add(w);
+        }
+    };
+    int at = 0;
+    for (; at + STEP - 32 < n; at += STEP) step(at, [](int) { return true; });
+    if (at < n) step(at, [&](int i) { return i < n; });
+    return acc.sum();
+}
+
+// The same with every check, one element at a time: a run with an infinite
+// entry.
+template <typename T>
+__device__ __forceinline__ Pair sum_run_checked(const Row<T> &row, int64_t lo, int64_t hi, int lane) {
+    Pair acc{0.f, 0.f};
+    for (int64_t v = lo + lane; v < hi; v += 32) acc.add(row.at(v));
     return acc;
 }
 
-__device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(addr), "d"(v) : "memory");
+__device__ __forceinline__ void st_dsmem(uint32_t addr, const Pair &v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" :: "r"(addr), "f"(v.hi), "f"(v.lo) : "memory");
 }
 
 template <typename T>
-__global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(VF_THREADS, 2) verify_drafts_kernel(const __grid_constant__ VerifyParams p) {
     __shared__ int sh_acc, sh_reject;               // accepted drafts; whether one was rejected
     __shared__ Pair sh_warp[VF_WARPS];              // sums of the warps' runs
-    __shared__ double sh_blocks[2][VF_MAX_CLUSTER]; // of the cluster's blocks, a pass each
+    __shared__ Pair sh_blocks[2][VF_MAX_CLUSTER];   // of the cluster's blocks, a pass each
     __shared__ int sh_own;                          // run that holds the border, -1: another block's,
                                                     // -2: nothing to draw from
     __shared__ Pair sh_goal;                        // the border from the run's start
@@ -146,8 +206,7 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
                 if (x >= 0 && x < V) {
                     const float pt = weight_of(Elem<T>::load1(target + (r - 1) * p.target_stride + x), 0.f);
                     const float qt = draft ? fmaxf(Elem<T>::load1(draft + r * p.draft_stride + x), 0.f) : 1.f;
-                    // the product of two floats is exact in binary64
-                    ok = (double)u * (double)qt < (double)pt;
+                    ok = product_below(u, qt, pt);
                 } else {
                     outside = true;
                 }
@@ -194,51 +253,50 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
     for (int pass = 0; pass < 2; ++pass) {
         // ---- sums of the runs, and of the blocks
         const int64_t lo = run_lo(warp), hi = run_lo(warp + 1);
-        constexpr int U = sizeof(T) == 4 ? 8 : 16;
-        Pair sum = row.q ? sum_run<T, true, 8>(row, lo, hi, lane) : sum_run<T, false, U>(row, lo, hi, lane);
+        const int len = (int)(hi - lo);
+        const int hole = row.hole >= lo && row.hole < hi ? (int)(row.hole - lo) : -1;
+        Pair sum = row.q ? sum_run<T, true, 4>(row.p + lo, row.q + lo, len, -1, lane)
+                         : sum_run<T, false, 4>(row.p + lo, row.p + lo, len, hole, lane);
+        if (__any_sync(0xffffffffu, !(sum.hi < INFINITY && sum.lo < INFINITY)))
+            sum = sum_run_checked(row, lo, hi, lane);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum.add(shfl_xor(sum, o));
         if (lane == 0) sh_warp[warp] = sum;
         __syncthreads();
-        double mine = 0., inc = 0.;                 // lane w of warp 0: run w's sum, and up to it
+        Pair mine{0.f, 0.f}, upto, below;           // lane w of warp 0: run w's sum, up to it, below it
         if (warp == 0) {
-            if (lane < VF_WARPS) mine = (double)sh_warp[lane].hi + (double)sh_warp[lane].lo;
-            inc = mine;
-#pragma unroll
-            for (int o = 1; o < VF_WARPS; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const double block = __shfl_sync(0xffffffffu, inc, VF_WARPS - 1);
-            if (lane < C) st_dsmem_f64(map_to_rank(&sh_blocks[pass][rank], (uint32_t)lane), block);
+            if (lane < VF_WARPS) mine = sh_warp[lane];
+            upto = scan<VF_WARPS>(mine, lane, &below);
+            const Pair block = shfl(upto, VF_WARPS - 1);
+            if (lane < C) st_dsmem(map_to_rank(&sh_blocks[pass][rank], (uint32_t)lane), block);
         }
         cluster_sync();
-        // ---- the border u W: the block whose sums reach past it, and the run
+        // ---- the border u W: the first block whose sums reach past it (or the
+        // last with any weight), and the run
         if (warp == 0) {
-            const double b = lane < C ? sh_blocks[pass][lane] : 0.;
-            double upto = b;                        // blocks 0 .. lane
-#pragma unroll
-            for (int o = 1; o < VF_MAX_CLUSTER; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
-            const double W = __shfl_sync(0xffffffffu, upto, VF_MAX_CLUSTER - 1);
-            const double u = us > 0.f ? (us < 1.f ? (double)us : 1.) : 0.;
-            const double x = u * W;
-            // the first block with sums past x, or the last with any weight
-            const unsigned past = __ballot_sync(0xffffffffu, lane < C && b > 0. && x < upto);
-            const unsigned any = __ballot_sync(0xffffffffu, lane < C && b > 0.);
+            const Pair b = lane < C ? sh_blocks[pass][lane] : Pair{0.f, 0.f};
+            Pair before;
+            const Pair sums = scan<VF_MAX_CLUSTER>(b, lane, &before);      // blocks 0 .. lane
+            const Pair W = shfl(sums, VF_MAX_CLUSTER - 1);
+            const float u = us > 0.f ? fminf(us, 1.f) : 0.f;
+            Pair x;                                 // u W
+            x.hi = u * W.hi;
+            x.lo = fmaf(u, W.hi, -x.hi) + u * W.lo;
+            const unsigned past = __ballot_sync(0xffffffffu, lane < C && b.hi > 0.f && sums.above(x));
+            const unsigned any = __ballot_sync(0xffffffffu, lane < C && b.hi > 0.f);
             int o = -2;
-            if (W > 0. && W < INFINITY) {
+            if (any && W.hi < INFINITY && W.lo < INFINITY) {
                 const int blk = past ? __ffs(past) - 1 : 31 - __clz(any);
                 o = -1;
                 if (blk == rank) {
-                    double before = __shfl_sync(0xffffffffu, upto, blk) - __shfl_sync(0xffffffffu, b, blk);
-                    const unsigned rp = __ballot_sync(0xffffffffu, mine > 0. && x < before + inc);
-                    const unsigned ra = __ballot_sync(0xffffffffu, mine > 0.);
+                    const Pair base = shfl(before, blk);
+                    x.add(Pair{-base.hi, -base.lo});               // from the block's start
+                    const unsigned rp = __ballot_sync(0xffffffffu, mine.hi > 0.f && upto.above(x));
+                    const unsigned ra = __ballot_sync(0xffffffffu, mine.hi > 0.f);
                     o = rp ? __ffs(rp) - 1 : 31 - __clz(ra);
-                    before += __shfl_sync(0xffffffffu, inc - mine, o);
-                    if (lane == 0) sh_goal = pair_of(x - before);
+                    const Pair run = shfl(below, o);
+                    x.add(Pair{-run.hi, -run.lo});                 // from the run's start
+                    if (lane == 0) sh_goal = x;
                 }
             }
             if (lane == 0) sh_own = o;
@@ -262,14 +320,8 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
     const int64_t e0 = lo + min(len, per * tid), e1 = lo + min(len, per * (tid + 1));
     Pair sum{0.f, 0.f};
     for (int64_t v = e0; v < e1; ++v) sum.add(row.at(v));
-    Pair inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Pair y = shfl_up(inc, o);
-        if (lane >= o) inc.add(y);
-    }
-    Pair before = shfl_up(inc, 1);                  // the warp's lanes before this one
-    if (lane == 0) before = Pair{0.f, 0.f};
+    Pair before;                                    // the warp's lanes below this one
+    const Pair inc = scan<32>(sum, lane, &before);
     if (lane == 31) sh_scan[warp] = inc;
     __syncthreads();
     Pair base{0.f, 0.f};
@@ -299,11 +351,10 @@ __global__ void __launch_bounds__(VF_THREADS) verify_drafts_kernel(const __grid_
 
 template <typename T>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
-#ifndef PA_VERIFY_BLOCKS
-#define PA_VERIFY_BLOCKS 2
-#endif
     const int sms = sm_count_of_current_device();
-    const int64_t slots = (int64_t)(sms > 0 ? sms : 152) * PA_VERIFY_BLOCKS;
+    // two blocks per SM fit; more would queue behind each other's chains of loads
+    // (64 sequences of 131071 tokens: 18.4 us at 4 blocks each, 22.5 at 8)
+    const int64_t slots = (int64_t)(sms > 0 ? sms : 152) * 2;
     int C = 1;
     while (C < VF_MAX_CLUSTER && (int64_t)p.num_seqs * C * 2 <= slots) C *= 2;
     if ((int64_t)p.num_seqs * C > (int64_t)INT32_MAX) return cudaErrorNotSupported;
