@@ -91,7 +91,7 @@ struct RopeParams {
     int64_t q_stride, q_out_stride, k_stride, v_stride;
     float eps;
     int num_heads, num_kv_heads, head_dim, rot_dim, interleaved;
-    int parts, part_heads;                    // warps per token, heads of each
+    int parts, part_iters;                    // warps per token, iterations of each
     unsigned int *err;
 };
 cudaError_t rope_and_cache(const RopeParams &p, int dtype, cudaStream_t st);

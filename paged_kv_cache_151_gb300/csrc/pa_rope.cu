@@ -154,36 +154,38 @@ __device__ __forceinline__ void load_factors(Factors &f, const void *weight, con
     }
 }
 
-// One warp per (token, part of its heads); L lanes per head, 32 / L heads at
-// a time.  The heads of a token are numbered q, then k, then v.  q may be
-// q_out: a head is read and written by the same lanes, reads first.
-template <typename T, bool F8, int L>
-__global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
+// Five blocks of four warps per SM, two iterations in flight (32768 tokens of
+// 32 + 8 + 8 heads of 128 into E4M3): 148 us; one iteration 170, four blocks 157, six
+// (which spill) 213.
+constexpr int ROPE_THREADS = 128, ROPE_BLOCKS = 5, ROPE_AHEAD = 2;
+
+// One warp per (token, part of its heads); L lanes per head, HW = 32 / L heads
+// an iteration, of one kind: ceil(H / HW) iterations of q, then of k, then of v.
+// Loads run AHEAD iterations ahead, across the kinds.  q may be q_out: a head is
+// read and written by the same lanes, reads first.
+template <typename T, bool F8, bool INTER, int L>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
     launch_dependents();      // a decode launched next may set up meanwhile
-    constexpr int HW = 32 / L;                      // heads of one iteration
+    constexpr int HW = 32 / L;
+    constexpr int AHEAD = ROPE_AHEAD;
     const int lane = threadIdx.x & 31, l = lane % L, sub = lane / L;
     const unsigned item = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const unsigned t = item / (unsigned)p.parts, part = item - t * (unsigned)p.parts;
     if (t >= (unsigned)p.num_tokens) return;
     const int D = p.head_dim, R = p.rot_dim, H = p.num_heads, Hkv = p.num_kv_heads;
-    const int h0 = (int)part * p.part_heads, h1 = min(H + 2 * Hkv, h0 + p.part_heads);
+    const int nq = (H + HW - 1) / HW, nk = (Hkv + HW - 1) / HW;
+    const int it0 = (int)part * p.part_iters;
+    int it1 = min(nq + 2 * nk, it0 + p.part_iters);
     const bool lane_ok = l < D / 16;
 
     const int64_t slot = p.slot_mapping[t];
     const int64_t pos = R > 0 ? p.positions[t] : 0;
-    const bool write = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && part == 0 && lane == 0) set_error(p.err, ERR_SLOT);
-    if (R > 0 && (pos < 0 || pos >= p.num_positions)) {
-        // a padding token may have any position; nothing of the token is written
-        if (slot >= 0 && part == 0 && lane == 0) set_error(p.err, ERR_POSITION);
-        return;
-    }
 
-    // this lane's two chunks
+    // this lane's two chunks (of v: any two do)
     const int RL = R / 16;                          // lanes that rotate
     const bool rot = l < RL;
     int ea, eb;
-    if (p.interleaved) {
+    if (INTER) {
         ea = 16 * l;
         eb = ea + 8;
     } else if (rot) {
@@ -193,28 +195,65 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_consta
         ea = R + 8 * (l - RL);
         eb = ea + (D - R) / 2;
     }
+    const T *q = reinterpret_cast<const T *>(p.q) + (int64_t)t * p.q_stride;
+    const T *k = reinterpret_cast<const T *>(p.k) + (int64_t)t * p.k_stride;
+    const T *v = reinterpret_cast<const T *>(p.v) + (int64_t)t * p.v_stride;
+    Raw8<T> na[AHEAD] = {}, nb[AHEAD] = {};
+    auto fetch = [&](int it, Raw8<T> &xa, Raw8<T> &xb) {
+        const bool is_q = it < nq, is_k = !is_q && it < nq + nk;
+        const int h = (it - (is_q ? 0 : is_k ? nq : nq + nk)) * HW + sub;
+        const T *src = (is_q ? q : is_k ? k : v) + h * D;
+        if (lane_ok && it < it1 && h < (is_q ? H : Hkv)) {
+            xa = load_raw8<T>(src + ea);
+            xb = load_raw8<T>(src + eb);
+        }
+    };
+    // k and v of a padding token are not looked at, so its loads wait for the slot
+    if (slot < 0 || slot >= p.num_slots) it1 = min(it1, nq);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(it0 + i, na[i], nb[i]);
+
+    if (slot >= p.num_slots && part == 0 && lane == 0) set_error(p.err, ERR_SLOT);
+    if (R > 0 && (pos < 0 || pos >= p.num_positions)) {
+        // a padding token may have any position; nothing of the token is written
+        if (slot >= 0 && part == 0 && lane == 0) set_error(p.err, ERR_POSITION);
+        return;
+    }
     const float *tr = p.rope_table + pos * R + 8 * l;
     const float inv_d = 1.f / (float)D;
+    T *qo = reinterpret_cast<T *>(p.q_out) + (int64_t)t * p.q_out_stride;
+    const int64_t row0 = ((slot >> 4) * Hkv * 16 + (slot & 15)) * D;   // KV head 0's row (block_size 16)
+    Factors f;
 
-    // heads [lo, hi) of q (or of k): from src on, the result to put(head, a, b)
-    auto turn = [&](const T *src, int lo, int hi, const void *weight, auto &&put) {
-        if (lo >= hi) return;
-        Raw8<T> na = {}, nb = {};
-        auto fetch = [&](int h) {
-            if (lane_ok && h < hi) {
-                na = load_raw8<T>(src + (int64_t)h * D + ea);
-                nb = load_raw8<T>(src + (int64_t)h * D + eb);
+    auto body = [&](int it, Raw8<T> &xa, Raw8<T> &xb) {
+        const bool is_q = it < nq, is_v = it >= nq + nk;
+        const int h = (it - (is_q ? 0 : is_v ? nq + nk : nq)) * HW + sub;
+        const bool live = lane_ok && h < (is_q ? H : Hkv);
+        const int64_t at = row0 + (int64_t)h * 16 * D;
+        if (is_v && !F8) {                          // bit for bit
+            const Raw8<T> ya = xa, yb = xb;
+            fetch(it + AHEAD, xa, xb);
+            if (live) {
+                store_raw8<T>(static_cast<T *>(p.v_cache) + at + ea, ya);
+                store_raw8<T>(static_cast<T *>(p.v_cache) + at + eb, yb);
             }
-        };
-        fetch(lo + sub);
-        Factors f;
-        load_factors<T>(f, weight, tr, R / 2, rot, lane_ok, p.interleaved, ea, eb);
-        for (int hb = lo; hb < hi; hb += HW) {
-            const int h = hb + sub;
-            float a[8], b[8];
-            widen8<T>(na, a);
-            widen8<T>(nb, b);
-            fetch(h + HW);
+            return;
+        }
+        const void *weight = is_q ? p.q_weight : p.k_weight;
+        if (!is_v && (it == it0 || it == nq))
+            load_factors<T>(f, weight, tr, R / 2, rot, lane_ok, INTER, ea, eb);
+        float a[8], b[8];
+        widen8<T>(xa, a);
+        widen8<T>(xb, b);
+        fetch(it + AHEAD, xa, xb);
+        float ra[8], rb[8];
+        if (is_v) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ra[e] = a[e];
+                rb[e] = b[e];
+            }
+        } else {
             float g = 1.f;
             if (weight) {                           // the sum needs every lane of the warp
                 float2 ss = make_float2(0.f, 0.f);
@@ -223,19 +262,18 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_consta
                     const float2 x = make_float2(a[e], a[e + 1]), y = make_float2(b[e], b[e + 1]);
                     ss = fma2(x, x, fma2(y, y, ss));
                 }
-                float sum = lane_ok ? ss.x + ss.y : 0.f;
+                float sum = live ? ss.x + ss.y : 0.f;
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 g = rsqrtf(sum * inv_d + p.eps);
             }
-            float ra[8], rb[8];
             if (!rot) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     ra[e] = a[e] * f.A1[e] * g;
                     rb[e] = b[e] * f.B1[e] * g;
                 }
-            } else if (p.interleaved) {
+            } else if (INTER) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     ra[e] = (a[e] * f.A1[e] - a[e + 1] * f.A2[e]) * g;
@@ -250,88 +288,57 @@ __global__ void __launch_bounds__(256) rope_and_cache_kernel(const __grid_consta
                     rb[e] = (b[e] * f.B1[e] + a[e] * f.B2[e]) * g;
                 }
             }
-            if (lane_ok && h < hi) put(h, ra, rb);
+        }
+        if (!live) return;
+        if (F8 && !is_q) {
+            const float sc = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+            const float r = sc > 0x1p-100f && sc < 0x1p100f ? 1.f / sc : 0.f;
+            unsigned char *dst = static_cast<unsigned char *>(is_v ? p.v_cache : p.k_cache) + at;
+            *reinterpret_cast<uint2 *>(dst + ea) = e4m3_of8(ra, sc, r);
+            *reinterpret_cast<uint2 *>(dst + eb) = e4m3_of8(rb, sc, r);
+        } else {
+            T *dst = is_q ? qo + h * D : static_cast<T *>(p.k_cache) + at;
+            store_raw8<T>(dst + ea, narrow8<T>(ra));
+            store_raw8<T>(dst + eb, narrow8<T>(rb));
         }
     };
-
-    T *qo = reinterpret_cast<T *>(p.q_out) + (int64_t)t * p.q_out_stride;
-    turn(reinterpret_cast<const T *>(p.q) + (int64_t)t * p.q_stride, h0, min(h1, H), p.q_weight,
-         [&](int h, const float *a, const float *b) {
-             store_raw8<T>(qo + (int64_t)h * D + ea, narrow8<T>(a));
-             store_raw8<T>(qo + (int64_t)h * D + eb, narrow8<T>(b));
-         });
-    if (!write) return;
-
-    // a row of KV head j of this token (block_size 16); chunk ea of it
-    auto cache_at = [&](int j) { return (((slot >> 4) * Hkv + j) * 16 + (slot & 15)) * D; };
-    auto recip = [&](float sc) { return sc > 0x1p-100f && sc < 0x1p100f ? 1.f / sc : 0.f; };
-    turn(reinterpret_cast<const T *>(p.k) + (int64_t)t * p.k_stride, max(h0 - H, 0),
-         min(h1 - H, Hkv), p.k_weight, [&](int j, const float *a, const float *b) {
-             if constexpr (F8) {
-                 const float sc = __ldg(p.k_scale + j), r = recip(sc);
-                 unsigned char *dst = static_cast<unsigned char *>(p.k_cache) + cache_at(j);
-                 *reinterpret_cast<uint2 *>(dst + ea) = e4m3_of8(a, sc, r);
-                 *reinterpret_cast<uint2 *>(dst + eb) = e4m3_of8(b, sc, r);
-             } else {
-                 T *dst = static_cast<T *>(p.k_cache) + cache_at(j);
-                 store_raw8<T>(dst + ea, narrow8<T>(a));
-                 store_raw8<T>(dst + eb, narrow8<T>(b));
-             }
-         });
-    // v: as it is (16-byte chunks l and D/16 + l of the head's 8-element ones)
-    const T *v = reinterpret_cast<const T *>(p.v) + (int64_t)t * p.v_stride;
-    const int va = 8 * l, vb = D / 2 + 8 * l;
-    for (int j = max(h0 - H - Hkv, 0) + sub; j < h1 - H - Hkv; j += HW) {
-        if (!lane_ok) continue;
-        const Raw8<T> ra = load_raw8<T>(v + (int64_t)j * D + va);
-        const Raw8<T> rb = load_raw8<T>(v + (int64_t)j * D + vb);
-        if constexpr (F8) {
-            const float sc = __ldg(p.v_scale + j), r = recip(sc);
-            unsigned char *dst = static_cast<unsigned char *>(p.v_cache) + cache_at(j);
-            float a[8], b[8];
-            widen8<T>(ra, a);
-            widen8<T>(rb, b);
-            *reinterpret_cast<uint2 *>(dst + va) = e4m3_of8(a, sc, r);
-            *reinterpret_cast<uint2 *>(dst + vb) = e4m3_of8(b, sc, r);
-        } else {
-            T *dst = static_cast<T *>(p.v_cache) + cache_at(j);
-            store_raw8<T>(dst + va, ra);
-            store_raw8<T>(dst + vb, rb);
-        }
+    for (int it = it0; it < it1; it += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (it + i < it1) body(it + i, na[i], nb[i]);
     }
 }
 
-template <typename T, bool F8, int L>
+template <typename T, bool F8, bool INTER, int L>
 cudaError_t launch_rope(RopeParams p, cudaStream_t st) {
     constexpr int HW = 32 / L;
-    const int rows = p.num_heads + 2 * p.num_kv_heads;
-    const int most = (rows + HW - 1) / HW;          // parts of one iteration each
+    const int iters = (p.num_heads + HW - 1) / HW + 2 * ((p.num_kv_heads + HW - 1) / HW);
     const int sms = sm_count_of_current_device();
     const int64_t want = (int64_t)(sms > 0 ? sms : 152) * 32;
     int64_t parts = (want + p.num_tokens - 1) / p.num_tokens;
-    if (parts > most) parts = most;
-    const int iters = (int)((most + parts - 1) / parts);
-    p.part_heads = iters * HW;
-    p.parts = (rows + p.part_heads - 1) / p.part_heads;
+    if (parts > iters) parts = iters;
+    p.part_iters = (int)((iters + parts - 1) / parts);
+    p.parts = (iters + p.part_iters - 1) / p.part_iters;
     const int64_t items = p.num_tokens * p.parts;
     if (items > (int64_t)INT32_MAX) return cudaErrorNotSupported;
-    const int threads = 256;
-    const int64_t blocks = (items * 32 + threads - 1) / threads;
-    prefer_shared_carveout<rope_and_cache_kernel<T, F8, L>>();
-    rope_and_cache_kernel<T, F8, L><<<(unsigned)blocks, threads, 0, st>>>(p);
+    const int64_t blocks = (items * 32 + ROPE_THREADS - 1) / ROPE_THREADS;
+    prefer_shared_carveout<rope_and_cache_kernel<T, F8, INTER, L>>();
+    rope_and_cache_kernel<T, F8, INTER, L><<<(unsigned)blocks, ROPE_THREADS, 0, st>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, bool F8>
+template <typename T, bool F8, bool INTER>
 cudaError_t dispatch_lanes(const RopeParams &p, cudaStream_t st) {
-    if (p.head_dim <= 64) return launch_rope<T, F8, 4>(p, st);
-    if (p.head_dim <= 128) return launch_rope<T, F8, 8>(p, st);
-    return launch_rope<T, F8, 16>(p, st);
+    if (p.head_dim <= 64) return launch_rope<T, F8, INTER, 4>(p, st);
+    if (p.head_dim <= 128) return launch_rope<T, F8, INTER, 8>(p, st);
+    return launch_rope<T, F8, INTER, 16>(p, st);
 }
 
 template <typename T>
 cudaError_t dispatch_cache(const RopeParams &p, cudaStream_t st) {
-    return p.k_scale ? dispatch_lanes<T, true>(p, st) : dispatch_lanes<T, false>(p, st);
+    if (p.interleaved)
+        return p.k_scale ? dispatch_lanes<T, true, true>(p, st) : dispatch_lanes<T, false, true>(p, st);
+    return p.k_scale ? dispatch_lanes<T, true, false>(p, st) : dispatch_lanes<T, false, false>(p, st);
 }
 
 }  // namespace
