@@ -693,11 +693,12 @@ extern "C" int pa_decode_multi_fp8(
     p.num_seqs = num_seqs; p.num_heads = num_heads; p.num_kv_heads = num_kv_heads;
     p.max_blocks = max_blocks_per_seq;
     p.scale_log2 = scale * pa::LOG2E;
-    // as for 16-bit caches: runs of at least PREFILL_GROUP_ROWS (token, head) rows
-    // go to the tcgen05 kernel, the others to the persistent kernel
-    const bool split = rows >= pa::PREFILL_GROUP_ROWS;
-    const int64_t small_rows = split ? pa::PREFILL_GROUP_ROWS - 1 : rows;
-    p.mq_split_rows = split ? pa::PREFILL_GROUP_ROWS : 0;
+    // as for 16-bit caches: runs of many (token, head) rows go to the tcgen05 kernel,
+    // the others to the persistent kernel
+    const int min_rows = pa::prefill_f8_min_rows(num_seqs);
+    const bool split = rows >= min_rows;
+    const int64_t small_rows = split ? min_rows - 1 : rows;
+    p.mq_split_rows = split ? min_rows : 0;
     if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
     if (!prepare_maps(p, PA_E4M3, head_dim)) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

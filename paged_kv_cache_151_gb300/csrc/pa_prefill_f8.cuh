@@ -704,9 +704,9 @@ cudaError_t run_prefill_f8(const DecodeParams &p, int groups, long long items, c
 template <typename T>
 cudaError_t dispatch_prefill_f8(const DecodeParams &p, int D, int G, int groups, cudaStream_t st) {
     // at most `groups` items a run, and one more than the full items of all rows
-    // for each run (a run has at least PREFILL_GROUP_ROWS rows)
+    // for each run (a run has at least mq_split_rows rows)
     const long long rows_all = (long long)p.num_q_rows * G;
-    long long runs = rows_all / PREFILL_GROUP_ROWS;
+    long long runs = rows_all / p.mq_split_rows;
     if (runs > p.num_seqs) runs = p.num_seqs;
     long long items = rows_all / PF8_ROWS + runs;
     if (items > groups * (long long)p.num_seqs) items = groups * (long long)p.num_seqs;
