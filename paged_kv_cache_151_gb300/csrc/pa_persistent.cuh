@@ -363,6 +363,25 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     const int NWC = C * NW;                  // warps of the cluster
     const int gw = rank * NW + warp;         // this warp's index in the cluster
 
+    // Behind the prefill kernel there may be no short run at all: leave before the
+    // set-up then (every block of the grid finds the same), once that kernel is
+    // done.  A bad length or range takes the long way, which flags it.
+    if constexpr (SPREAD) {
+        if (p.mq_split_rows > 0) {
+            bool some = false;
+            for (int i = tid; i < B; i += NT) {
+                const int a = p.query_start[i], b = p.query_start[i + 1], L = p.seq_lens[i];
+                const bool good = a >= 0 && b >= a && b <= p.num_q_rows && b - a <= p.max_query_len &&
+                                  b - a <= L && L <= cap;
+                some = some || !good || (b > a && (long long)(b - a) * G < p.mq_split_rows);
+            }
+            if (!__syncthreads_or(some)) {
+                grid_dependency_wait();
+                return;
+            }
+        }
+    }
+
     // split-KV partitions are always followed by their merge, which waits for
     // this whole grid before it reads anything: let it become resident early
     if constexpr (PARTIAL) launch_dependents();
