@@ -62,10 +62,10 @@
  * pa_device_error, which reads device memory synchronously.  The decode
  * kernels are launched with programmatic stream serialization: when the
  * kernel before them in the stream is a cache write of this library
- * (pa_reshape_and_cache, pa_rope_and_cache, and their _fp8 forms), they start
- * while it finishes and read seq_lens, block_tables and query_start meanwhile --
- * the cache writes never touch those -- and touch the caches, q and out only
- * after it has completed.  After any other kernel they start as usual.
+ * (pa_reshape_and_cache, pa_reshape_and_cache_fp8, or pa_rope_and_cache and its
+ * _fp8 form without queries), they start while it finishes and read seq_lens,
+ * block_tables and query_start meanwhile -- the cache writes never touch those --
+ * and touch the caches, q and out only after it has completed.  After any other kernel they start as usual.
  *
  * Errors.  Calls return PA_OK (0) or a negative pa_status; nothing is
  * launched when the host-side checks fail.  Contents of device arrays are not
@@ -152,7 +152,7 @@ int pa_reshape_and_cache(const void *k, const void *v, void *k_cache,
  *             p = positions[t].  Elements past rot_dim pass.
  * q_out[t][h] is the result for q, and the slot of t receives the result for
  * k in k_cache and v[t][j] bit for bit in v_cache.  Arithmetic is fp32 with one
- * rounding at the end.
+ * rounding at the end (squares have to stay inside the binary32 range).
  *
  * rope_table is float32 [num_positions][rot_dim], contiguous.  q and q_out are
  * [num_tokens][num_heads][head_dim] with heads contiguous and token strides of
@@ -488,7 +488,12 @@ int pa_decode_partitioned_fp8(void *out, const void *q, const void *k_cache,
  * per sequence (drafts to verify, or a chunk of a prompt), causal among
  * themselves, K_s[t] and V_s[t] dequantised as in pa_decode_fp8.  `dtype` is the
  * type of q and out, PA_BF16 or PA_F16 (q is rounded to f16: |q| < 65504).
- * Rows, query_start, errors and requirements as pa_decode_multi.
+ * Rows, query_start, errors and requirements as pa_decode_multi.  As there, a
+ * NaN among the values of a run's new tokens may also reach rows of the run that
+ * stand before it (the product with a weight of 0); every other row past a
+ * row's limit, and past the sequence, may hold anything.  The result of a row
+ * is the same for every physical placement of the blocks; its rounding depends
+ * on the sizes of the call (how its keys are split).
  */
 int pa_decode_multi_fp8(void *out, const void *q, const void *k_cache,
                         const void *v_cache, const float *k_scale,

@@ -396,7 +396,7 @@ struct WarpAttnF8x16 {
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                const uint4 w = src[h] ? __ldg(reinterpret_cast<const uint4 *>(src[h] + 32 * kk + 8 * t))
+                const uint4 w = src[h] ? *reinterpret_cast<const uint4 *>(src[h] + 32 * kk + 8 * t)
                                        : make_uint4(0, 0, 0, 0);
                 qa[2 * kk][h] = WarpAttnF8<T, D, 1>::to_f16x2(w.x);          // d 32kk+8t + {0,1}
                 qa[2 * kk][2 + h] = WarpAttnF8<T, D, 1>::to_f16x2(w.y);      //            {2,3}

@@ -818,7 +818,8 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
                     for (int c = 0; c < CG; ++c) {
                         const float Mn = fmaxf(M[c], mw[c]);
-                        if (Mn == -INFINITY) continue;     // nothing seen yet
+                        // nothing seen yet (with a sum: only NaN, which stays)
+                        if (Mn == -INFINITY && !(SPREAD && lw[c] != 0.f)) continue;
                         const float a = M[c] == -INFINITY ? 0.f : ex2(M[c] - Mn);
                         const float b = mw[c] == -INFINITY ? 0.f : ex2(mw[c] - Mn);
                         Ls[c] = fmaf(b, lw[c], Ls[c] * a);
@@ -1135,6 +1136,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                         for (int i = 0; i < AHEAD; ++i) {
                             const int w = wb + i;
                             mw[i] = -INFINITY;
+                            lw[i] = 0.f;
                             if (w > w1 || range_lo(w) == range_lo(w + 1)) continue;
                             const float *pw = part_of(w, (w == w1 && w != w0) ? 0 : 1);
                             const uint32_t rw = (uint32_t)(w / NW);
@@ -1147,9 +1149,10 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                         }
 #pragma unroll
                         for (int i = 0; i < AHEAD; ++i) {
-                            if (mw[i] == -INFINITY) continue;      // no partial, or nothing seen
+                            if (lw[i] == 0.f) continue;    // no partial, or nothing seen
                             const float Mn = fmaxf(M, mw[i]);
-                            const float a = M == -INFINITY ? 0.f : ex2(M - Mn), b = ex2(mw[i] - Mn);
+                            const float a = M == -INFINITY ? 0.f : ex2(M - Mn);
+                            const float b = mw[i] == -INFINITY ? 0.f : ex2(mw[i] - Mn);   // (0 * NaN is NaN)
                             Ls = fmaf(b, lw[i], Ls * a);
 #pragma unroll
                             for (int e = 0; e < V; ++e) O[e] = fmaf(b, ow[i][e], O[e] * a);

@@ -39,11 +39,21 @@
 //
 // Roles of the 16 warps: 0-3 and 4-7 softmax of tile 0 and 1; 8, 9 convert K and
 // 10, 11 V (32 rows of a step each: 16-byte loads of codes two steps ahead in
-// registers, f16 to the 128-byte swizzled stages of K and V); lane 0 of warps 12 and 13 issues S of tile 0 and 1, of warps 14 and 15
-// P V (an issue blocks while the pipe is busy, so one warp for both would hold
-// the next S back behind a P V, or the reverse).  Completion comes back through
-// tcgen05.commit on mbarriers; one lane of a warp polls.  Every wait is bounded;
-// on a timeout the block stops and the error word says so.
+// registers, f16 to the 128-byte swizzled stages of K and V); lane 0 of warps 12
+// and 13 issues S of tile 0 and 1, of warps 14 and 15 P V (an issue blocks while
+// the pipe is busy, so one warp for both would hold the next S back behind a
+// P V, or the reverse).  Completion comes back through tcgen05.commit on
+// mbarriers; one lane of a warp polls.  Every wait is bounded; on a timeout the
+// block stops and the error word says so.
+//
+// Measured: 2048 rows of 32 query heads (8 KV heads of 128) over 14 to 16 thousand
+// keys 495 us in a long run (441 us in a short one, before the power limit):
+// 1.03 PFLOP/s, 0.54 of the measured bf16 peak; 256 items are 1.68 waves of the
+// 152 SMs, so the SMs that work run at 0.65.  Three runs of 200 to 500 tokens
+// (16 heads over 2, head_dim 64) over up to 6000 keys: 53 us.  A step of one tile
+// alone takes 0.82 us: the chain S, wait, load, softmax, wait, store, P V, not
+// its arithmetic (without the exponentials, the maximum or the sum 0.80 us and
+// more), so short lists of items are bound by it.
 #pragma once
 
 #include <atomic>
@@ -244,7 +254,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             if (!more) return;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
-                if (64 * (it.step0 + c) + 32 * half + 16 * b < it.L) pb[b] = __ldg(tab + 4 * c + b);
+                if (64 * (it.step0 + c) + 32 * half + 16 * b < it.L) pb[b] = tab[4 * c + b];
         };
         item_next();
         blocks_of();
@@ -264,7 +274,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 #pragma unroll
                 for (int i = 0; i < NI / 2; ++i)
                     buf[b * (NI / 2) + i] = i * RPI + r0 < rows
-                        ? __ldg(reinterpret_cast<const uint4 *>(src + i * RPI * D)) : make_uint4(0, 0, 0, 0);
+                        ? *reinterpret_cast<const uint4 *>(src + i * RPI * D) : make_uint4(0, 0, 0, 0);
             }
             if (++c == it.nsteps) item_next();
             blocks_of();
@@ -420,7 +430,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     uint32_t w[32];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 x = row_ok ? __ldg(reinterpret_cast<const uint4 *>(q + 64 * h) + i)
+                        const uint4 x = row_ok ? reinterpret_cast<const uint4 *>(q + 64 * h)[i]
                                                : make_uint4(0, 0, 0, 0);
                         w[4 * i] = WarpAttnF8<T, D, 1>::to_f16x2(x.x) ^ sign;
                         w[4 * i + 1] = WarpAttnF8<T, D, 1>::to_f16x2(x.y) ^ sign;
@@ -555,12 +565,14 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                 }
                 st_dsmem_f32x2(xs + rank * 1024, m_run, l_run);
                 if (!wait_cluster(&x_full[t], kt)) { ok = false; break; }
-                // the common level, each block's weight, and the sum
+                // the common level, each block's weight, and the sum; a block that saw
+                // nothing of the row has l = 0, one that saw a NaN has l = NaN (at any
+                // level) and makes the row NaN
                 float w[C], M = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < C; ++i) {
                     const float2 ml = lds_f32x2(xs + i * 1024);
-                    w[i] = ml.y > 0.f ? ml.x : -INFINITY;
+                    w[i] = ml.y == 0.f ? -INFINITY : ml.x == -INFINITY ? 0.f : ml.x;
                     M = fmaxf(M, w[i]);
                 }
 #pragma unroll
@@ -577,11 +589,12 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     for (int e = 0; e < CH; ++e) x[e] = 0.f;
 #pragma unroll
                     for (int i = 0; i < C; ++i) {
+                        // nothing of the row there (or no step at all): no O to read
+                        if (lds_f32x2(xs + i * 1024).y == 0.f) continue;
                         if (i == rank) {
-                            // nothing of this row here (or no step at all): O is not read
 #pragma unroll
-                            for (int e = 0; e < CH; ++e) x[e] = w[i] != 0.f ? fmaf(w[i], v[e], x[e]) : x[e];
-                        } else if (w[i] != 0.f) {
+                            for (int e = 0; e < CH; ++e) x[e] = fmaf(w[i], v[e], x[e]);
+                        } else {
                             const uint32_t from = xo + (i < rank ? i : i - 1) * (DC * 512) + c0 * 512;
 #pragma unroll
                             for (int e = 0; e < CH; e += 4) {

@@ -165,7 +165,10 @@ constexpr int ROPE_THREADS = 128, ROPE_BLOCKS = 5, ROPE_AHEAD = 2;
 // read and written by the same lanes, reads first.
 template <typename T, bool F8, bool INTER, int L>
 __global__ void __launch_bounds__(ROPE_THREADS, ROPE_BLOCKS) rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
-    launch_dependents();      // a decode launched next may set up meanwhile
+    // Without queries this is a cache write like the others: a decode launched
+    // next may set up meanwhile.  With queries it may not: the decodes read q
+    // through the non-coherent path, which must not see it being written.
+    if (p.num_heads == 0) launch_dependents();
     constexpr int HW = 32 / L;
     constexpr int AHEAD = ROPE_AHEAD;
     const int lane = threadIdx.x & 31, l = lane % L, sub = lane / L;

@@ -236,6 +236,79 @@ def test_large_scores(cuda_lib):
     assert_close(gpu_multi(cuda_lib, b), oracle_multi(b), "large scores")
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_scale_zero_and_negative(cuda_lib, scale):
+    """A scale of 0 is the mean of the visible values; a negative one turns the
+    scores round."""
+    b = batch(760, num_seqs=4, min_ctx=10, max_ctx=200, n_new=[3, 70, 300, 1], num_heads=8,
+              num_kv_heads=2, head_dim=128, dtype="bf16")
+    b.scale = scale
+    assert_close(gpu_multi(cuda_lib, b), oracle_multi(b), f"scale {scale}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [31, 32, 33, 127, 128, 129, 255, 256, 257])
+def test_rows_around_the_tiles(cuda_lib, D, rows):
+    """One query head per KV head, so a token is a row: the sizes at which a run
+    changes kernel, tile and item, over a context that several blocks share."""
+    b = batch(770 + rows, num_seqs=2, min_ctx=1000, max_ctx=1100, n_new=[rows, rows + 1],
+              num_heads=2, num_kv_heads=2, head_dim=D, dtype="bf16")
+    assert_close(gpu_multi(cuda_lib, b), oracle_multi(b), f"rows {rows}")
+
+
+@pytest.mark.parametrize("seqs,n", [(1, 64), (3, 200), (20, 300), (60, 100)])
+def test_items_shared_by_none_two_and_four_blocks(cuda_lib, seqs, n):
+    """Few items to many; contexts of less than one step a block too."""
+    b = batch(780 + seqs, num_seqs=seqs, min_ctx=0, max_ctx=700, n_new=n, num_heads=8,
+              num_kv_heads=2, head_dim=128, dtype="f16")
+    assert_close(gpu_multi(cuda_lib, b), oracle_multi(b), f"{seqs} x {n}")
+
+
+@pytest.mark.parametrize("n", [4, 100])
+@pytest.mark.parametrize("ctx", [50, 3000])
+def test_nan_keys(cuda_lib, n, ctx):
+    """A NaN key makes the rows that see it NaN, whatever blocks or warps share
+    their keys, and no row before it."""
+    b = batch(790, num_seqs=1, min_ctx=ctx, max_ctx=ctx, n_new=n, num_heads=4, num_kv_heads=1,
+              head_dim=128, dtype="bf16")
+    ref = gpu_multi(cuda_lib, b)
+    L = int(b.seq_lens[0])
+    for at, rows in ((L - 1, n - 1), (L - 2, n - 2), (7, 0)):      # position, first row that sees it
+        kc = b.k_cache.clone()
+        kc[int(b.block_tables[0, at // 16]), :, at % 16] = 0x7F
+        out = gpu_multi(cuda_lib, b, k_cache=kc)
+        assert torch.equal(out[:rows], ref[:rows]) and out[rows:].isnan().all()
+    kc = torch.full_like(b.k_cache, 0x7F)          # nothing but NaN
+    assert gpu_multi(cuda_lib, b, k_cache=kc).isnan().all()
+
+
+@pytest.mark.parametrize("n", [4, 90])
+def test_many_blocks_past_32_bits_of_cache(cuda_lib, n):
+    """A pool of more than 2^31 codes: the blocks used lie at its end."""
+    b = batch(800, num_seqs=2, min_ctx=100, max_ctx=300, n_new=n, num_heads=8, num_kv_heads=8,
+              head_dim=128, dtype="bf16")
+    N = 135_000                                    # x 8 x 16 x 128 codes = 2.2e9 each
+    out = gpu_multi(cuda_lib, b)
+    shift = N - b.num_blocks
+    big = [torch.empty(N, 8, 16, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for dst, src in zip(big, (b.k_cache, b.v_cache)):
+        dst[shift:] = src
+    tables = np.where(b.block_tables < b.num_blocks, b.block_tables + shift, b.block_tables)
+    assert torch.equal(gpu_multi(cuda_lib, b, k_cache=big[0], v_cache=big[1],
+                                 block_tables=tables), out)
+
+
+def test_wait_that_runs_out(cuda_lib):
+    """A copy that never completes: the call ends with PA_DEVERR_TIMEOUT, and
+    the next one is right."""
+    b = batch(810, num_seqs=8, min_ctx=100, max_ctx=300, n_new=4, num_heads=8, num_kv_heads=2,
+              head_dim=128, dtype="bf16")
+    cuda_lib.pa_test_stall_next_decode()
+    gpu_multi(cuda_lib, b)
+    assert cuda_lib.pa_device_error(clear=True) == cuda_lib.PA_DEVERR_TIMEOUT
+    assert_close(gpu_multi(cuda_lib, b), oracle_multi(b), "after the timeout")
+
+
 def test_on_another_stream(cuda_lib):
     b = batch(750, num_seqs=5, min_ctx=0, max_ctx=300, n_new=(1, 90), num_heads=8,
               num_kv_heads=2, head_dim=128, dtype="bf16")

@@ -148,6 +148,26 @@ def test_steps_back_to_back_see_their_own_writes(cuda_lib):
         assert all(torch.equal(a, b) for a, b in zip(got, st.results()))
 
 
+def test_queries_rotated_in_place_reach_the_attention(cuda_lib):
+    """q rotated inside the projection's output, then attention on that view at
+    once: the same as with a synchronisation between."""
+    st = Step(6, [4] * 30, [41 * i for i in range(30)])
+    q, k, v = (x.view(st.T, -1, D) for x in st.qkv.split([H * D, HKV * D, HKV * D], 1))
+    for seed in range(20):
+        got = []
+        for wait in (False, True):
+            st.fill(seed)
+            torch.cuda.synchronize()
+            cuda_lib.pa_rope_and_cache_fp8(q, q, k, v, st.kc, st.vc, st.ks, st.vs, st.table,
+                                           st.positions, st.slots, q_weight=st.w, k_weight=st.w)
+            if wait:
+                torch.cuda.synchronize()
+            cuda_lib.pa_decode_multi_fp8(st.o, q, st.kc, st.vc, st.ks, st.vs, st.bt, st.sl,
+                                         st.qst, 4, D ** -0.5, HKV)
+            got.append(st.o.clone())
+        assert torch.equal(*got)
+
+
 @pytest.mark.parametrize("n,ctx", [SHAPES[0], SHAPES[2]], ids=["drafts", "chunk"])
 def test_step_captured_and_replayed(cuda_lib, n, ctx):
     st = Step(3, n, list(ctx))
