@@ -351,6 +351,12 @@ __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint
 // reference level moves only when a score exceeds it by more than
 // 2^RESCALE_LOG2, and only then do its lanes exchange their maxima: (m, l, acc)
 // are to that level, not to the true maximum.
+//
+// Measured: 256 sequences of four rows (312 MB of codes) 91.5 us = 3.4 TB/s, 0.51
+// of the measured copy rate.  The issue of dependent conversions and MMAs
+// bounds it (443 instructions a block, 5.4 cycles each, two warps a scheduler:
+// 221 registers leave no room for more), not the tensor pipe (17 % busy) nor
+// shared memory.
 template <typename T, int D>
 struct WarpAttnF8x16 {
     static_assert(sizeof(T) == 2, "q and out are 16-bit");

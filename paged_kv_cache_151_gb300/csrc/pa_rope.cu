@@ -22,6 +22,11 @@
 // same pairs for every head of a token, so a warp folds weights, cos and sin
 // into four factors a pair once and runs over several heads with them, the
 // next heads' loads in flight.
+//
+// Measured: 32768 tokens (32 + 8 + 8 heads of 128, norms, E4M3 cache; 755 MB) 150 us =
+// 5.0 TB/s, 0.75 of the measured copy rate; 1024 tokens 10.3 us and one token
+// 4.1 us on the device, where a warp's chain of slot and position, table and data
+// loads counts.
 #include <type_traits>
 
 #include "pa_common.cuh"
