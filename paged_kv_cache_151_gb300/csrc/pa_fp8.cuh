@@ -346,17 +346,16 @@ __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint
 // the value product takes the rows as two tiles of eight columns, which share
 // the V fragments, so a block's codes are converted once for 16 rows.
 //
-// The scores of a block and its softmax and value product are two calls, so
-// that the scores of the next block run beside the softmax of this one.  A row's
-// reference level moves only when a score exceeds it by more than
+// A row's reference level moves only when a score exceeds it by more than
 // 2^RESCALE_LOG2, and only then do its lanes exchange their maxima: (m, l, acc)
 // are to that level, not to the true maximum.
 //
-// Measured: 256 sequences of four rows (312 MB of codes) 91.5 us = 3.4 TB/s, 0.51
-// of the measured copy rate.  The issue of dependent conversions and MMAs
-// bounds it (443 instructions a block, 5.4 cycles each, two warps a scheduler:
-// 221 registers leave no room for more), not the tensor pipe (17 % busy) nor
-// shared memory.
+// Measured: 256 sequences of four rows (312 MB of codes) 91 us = 3.4 TB/s, 0.51 of
+// the measured copy rate.  The warp-level matrix pipe bounds it: 32 MMAs a
+// block, every row and column of them in use, keep it busy for two thirds of the
+// time with set-up and tail counted (123 of 183 thousand cycles).  Neither twelve
+// warps an SM instead of eight (two stages each) nor the scores of the next
+// block issued beside the values of this one changes the 91 us.
 template <typename T, int D>
 struct WarpAttnF8x16 {
     static_assert(sizeof(T) == 2, "q and out are 16-bit");
@@ -392,11 +391,10 @@ struct WarpAttnF8x16 {
         }
     }
 
-    // query rows (nullptr: no such row); their causal limits go to `lims`
-    __device__ __forceinline__ void load_q(const T *q_lo, const T *q_hi, int lo_lim, int hi_lim,
-                                           int (&lims)[2]) {
-        lims[0] = q_lo ? lo_lim : -1;
-        lims[1] = q_hi ? hi_lim : -1;
+    // query rows (nullptr: no such row) and their causal limits
+    __device__ __forceinline__ void load_q(const T *q_lo, const T *q_hi, int lo_lim, int hi_lim) {
+        lim[0] = q_lo ? lo_lim : -1;
+        lim[1] = q_hi ? hi_lim : -1;
         const T *src[2] = {q_lo, q_hi};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -528,6 +526,10 @@ struct WarpAttnF8x16 {
             mma_f16(acc[0][2 * w + 1], c0, c1, c2, c3, pb[0][0], pb[0][1]);
             mma_f16(acc[1][2 * w + 1], c0, c1, c2, c3, pb[1][0], pb[1][1]);
         }
+    }
+
+    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int pos0, float scale_log2) {
+        values(scores(kt), vt, pos0, scale_log2);
     }
 
     // bytes DL*g .. DL*g + DL-1 of V row `row`

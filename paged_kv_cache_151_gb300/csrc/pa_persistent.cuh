@@ -301,8 +301,9 @@ __host__ __device__ constexpr int persistent_warps() {
 
 // Blocks per SM the kernel is built for: eight warps of 16-bit tiles per SM
 // (one block of eight or two of four); E4M3 tiles are half the bytes, so
-// three blocks of four fit and hide more latency (two for multi-token queries,
-// whose partials of 16 rows take the room of the third).
+// three blocks of four fit and hide more latency (two for multi-token queries:
+// their partials of 16 rows would leave a third block two stages a warp, and
+// the matrix pipe is what they wait for: 91 us either way).
 template <typename KV, int NW, int MODE>
 __host__ __device__ constexpr int persistent_blocks_per_sm() {
     return sizeof(KV) == 1 ? (MODE == MODE_MULTI ? 2 : PA_F8_BLOCKS_PER_SM) : (NW >= 8 ? 1 : 2);
@@ -938,159 +939,73 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     float unit_scale = p.scale_log2;               // score scale (x K's scale for E4M3)
     int k_done = 0;
     bool ok = true;
-    if constexpr (SPREAD) {
-        // 16-row tiles over E4M3 caches: the scores of block k + 1 are issued before
-        // the softmax and value product of block k, so the matrix instructions of
-        // one run beside the exchanges and exponentials of the other
-        auto stage_of = [&](int k) { return my_stages + (size_t)(k % S) * 2 * TILE; };
-        auto wait_stage = [&](int k) -> bool {
-            const bool w = mbar_wait_bounded(&my_bars[k % S], (uint32_t)((k / S) & 1), p.err);
-            return __all_sync(0xffffffffu, w);
-        };
-        // block k: its unit, its position and whether it can be read
-        int ui = -1, pbk = 0, pos = 0;
-        bool good = false;
-        int lims[2] = {-1, -1};
-        float next_scale = 0.f;
-        typename W::Scores sv = {};
-        // move to block k (the one after the present one, or the first): returns
-        // false after a timeout
-        auto enter = [&](int k, int &ui_k, int &pos_k, bool &good_k, typename W::Scores &sv_k) -> bool {
-            if (k - c0 == 32) {
-                c0 += 32;
-                ui_cur = ui_nxt;
-                pb_cur = pb_nxt;
-                fetch(c0 + 32 + lane, ui_nxt, pb_nxt);
-            }
-            of(k, ui_k, pbk);
-            if (ui_k != ui) {
-                const UnitRec &u = units[ui_k];
+    for (int k = 0; k < n_mine; ++k) {
+        if (k - c0 == 32) {
+            c0 += 32;
+            ui_cur = ui_nxt;
+            pb_cur = pb_nxt;
+            fetch(c0 + 32 + lane, ui_nxt, pb_nxt);
+        }
+        int ui, pbk;
+        of(k, ui, pbk);
+        if (ui != cur) {
+            if (cur >= 0) leave_unit(cur, false);
+            cur = ui;
+            if constexpr (MQ) {
+                const UnitRec &u = units[ui];
                 const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
-                wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G, lims);
-                next_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
-                pos_k = pos_of(k, ui_k);
+                wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
+                if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
             } else {
-                pos_k = pos + 16;
-            }
-            if (!wait_stage(k)) return false;
-            k_done = k + 1;
-            good_k = pbk >= 0 && (long long)pbk < p.num_blocks;
-            if (good_k) sv_k = wa.scores(smem_u32(stage_of(k)));
-            return true;
-        };
-        if (n_mine > 0) {
-            int first = -1;
-            ok = enter(0, first, pos, good, sv);
-            cur = ui = first;
-            wa.lim[0] = lims[0];
-            wa.lim[1] = lims[1];
-            unit_scale = next_scale;
-        }
-        for (int k = 0; ok && k < n_mine; ++k) {
-            int ui_n = ui, pos_n = 0;
-            bool good_n = false;
-            typename W::Scores sv_n = {};
-            if (k + 1 < n_mine && !enter(k + 1, ui_n, pos_n, good_n, sv_n)) {
-                ok = false;
-                break;
-            }
-            if (good) {
-                unsigned char *Vt = stage_of(k) + TILE;
-                const int rows = min(16, units[ui].L - pos);
-                if (rows < 16) {                   // other tokens' data behind the sequence
-                    W::zero_rows(Vt, rows, lane);
-                    fence_proxy_async_smem();      // before the next copy into the stage
-                    __syncwarp();
+                auto qptr = [&](int q) {
+                    const UnitRec &u = units[q];
+                    return reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
+                           (long long)u.j * G * D;
+                };
+                if (qnext != ui) wa.prefetch_q(qptr(ui));
+                if constexpr (TC) wa.take_q();
+                else wa.take_q(p.scale_log2);
+                if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + units[ui].j);
+                // load the next unit's query while this one streams
+                qnext = -1;
+                if (ui + 1 < nu && cum[ui + 1] < my_hi && units[ui + 1].nb > 0) {
+                    qnext = ui + 1;
+                    wa.prefetch_q(qptr(qnext));
                 }
-                wa.values(sv, smem_u32(Vt), pos, unit_scale);
             }
-            __syncwarp();                          // every lane is done with the stage
-            const int kn = k + S;
-            if (kn < n_mine) {
-                int uin, pbn;
-                of(kn, uin, pbn);
-                if (lane == 0) issue(kn, uin, pbn);
-            }
-            if (ui_n != ui) {
-                leave_unit(ui, false);
-                cur = ui_n;
-                wa.lim[0] = lims[0];
-                wa.lim[1] = lims[1];
-                unit_scale = next_scale;
-            }
-            ui = ui_n;
-            pos = pos_n;
-            good = good_n;
-            sv = sv_n;
         }
-    } else {
-        for (int k = 0; k < n_mine; ++k) {
-            if (k - c0 == 32) {
-                c0 += 32;
-                ui_cur = ui_nxt;
-                pb_cur = pb_nxt;
-                fetch(c0 + 32 + lane, ui_nxt, pb_nxt);
-            }
-            int ui, pbk;
-            of(k, ui, pbk);
-            if (ui != cur) {
-                if (cur >= 0) leave_unit(cur, false);
-                cur = ui;
-                if constexpr (MQ) {
-                    const UnitRec &u = units[ui];
-                    const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
-                    wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
-                } else {
-                    auto qptr = [&](int q) {
-                        const UnitRec &u = units[q];
-                        return reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
-                               (long long)u.j * G * D;
-                    };
-                    if (qnext != ui) wa.prefetch_q(qptr(ui));
-                    if constexpr (TC) wa.take_q();
-                    else wa.take_q(p.scale_log2);
-                    if constexpr (F8) unit_scale = p.scale_log2 * __ldg(p.k_scale + units[ui].j);
-                    // load the next unit's query while this one streams
-                    qnext = -1;
-                    if (ui + 1 < nu && cum[ui + 1] < my_hi && units[ui + 1].nb > 0) {
-                        qnext = ui + 1;
-                        wa.prefetch_q(qptr(qnext));
+        const int st = k % S;
+        const bool waited = mbar_wait_bounded(&my_bars[st], (uint32_t)((k / S) & 1), p.err);
+        if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
+        k_done = k + 1;
+        if (pbk >= 0 && (long long)pbk < p.num_blocks) {
+            unsigned char *Kt = my_stages + (size_t)st * 2 * TILE;
+            const int rows = rows_of(k, ui);
+            if constexpr (TC) {
+                // tail rows hold other tokens' data: the one-token block math
+                // drops them in registers; the others clear them in the tile
+                if (F8 || MQ) {
+                    if (rows < 16) {
+                        if constexpr (F8) W::zero_rows(Kt + TILE, rows, lane);
+                        else WarpAttnTC<T, D, G>::zero_rows(Kt + TILE, rows, lane);
+                        // these generic writes must be ordered before the next
+                        // bulk copy into the stage
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
                 }
+                if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
+                else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
+            } else {
+                wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
             }
-            const int st = k % S;
-            const bool waited = mbar_wait_bounded(&my_bars[st], (uint32_t)((k / S) & 1), p.err);
-            if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
-            k_done = k + 1;
-            if (pbk >= 0 && (long long)pbk < p.num_blocks) {
-                unsigned char *Kt = my_stages + (size_t)st * 2 * TILE;
-                const int rows = rows_of(k, ui);
-                if constexpr (TC) {
-                    // tail rows hold other tokens' data: the one-token block math
-                    // drops them in registers; the others clear them in the tile
-                    if (F8 || MQ) {
-                        if (rows < 16) {
-                            if constexpr (F8) W::zero_rows(Kt + TILE, rows, lane);
-                            else WarpAttnTC<T, D, G>::zero_rows(Kt + TILE, rows, lane);
-                            // these generic writes must be ordered before the next
-                            // bulk copy into the stage
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), p.scale_log2);
-                    else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
-                } else {
-                    wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
-                }
-            }
-            __syncwarp();                              // every lane is done with the stage
-            const int kn = k + S;
-            if (kn < n_mine) {
-                int uin, pbn;
-                of(kn, uin, pbn);
-                if (lane == 0) issue(kn, uin, pbn);
-            }
+        }
+        __syncwarp();                              // every lane is done with the stage
+        const int kn = k + S;
+        if (kn < n_mine) {
+            int uin, pbn;
+            of(kn, uin, pbn);
+            if (lane == 0) issue(kn, uin, pbn);
         }
     }
     // a timeout leaves the unit unmerged (its output is not written; the
@@ -1171,8 +1086,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
 
     // after a timeout: wait (bounded) for this warp's copies still in flight
     if (!ok) {
-        // (the E4M3 multi-token loop is one block ahead of its copies)
-        const int issued = min(n_mine, S + (SPREAD ? max(k_done - 1, 0) : k_done));
+        const int issued = min(n_mine, k_done + S);
         for (int k = k_done; k < issued; ++k)
             mbar_wait_bounded(&my_bars[k % S], (uint32_t)((k / S) & 1), p.err);
     }
