@@ -322,7 +322,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         const bool sside = warp < PF8_MMA_WARP + 2;
         bool ok = true;
         unsigned g = 0, gt = 0;                    // steps so far; of this tile
-        unsigned kt = 0;                           // items with this tile
+        unsigned kt = 0;                           // items with this tile and steps
         Item it;
         const uint64_t dk = tc5_desc_sw128(smem_u32(smem + Lay::OFF_K), 16, 1024);
         const uint64_t dv = tc5_desc_sw128(smem_u32(smem + Lay::OFF_V), PF8_KEYS * 128, 1024);
@@ -341,7 +341,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     ok = wait(&full[g % NS], g / NS);
                     if (ok) mbar_arrive(&empty[g % NS]);
                 }
-            } else if (lane == 0 && sside) {
+            } else if (lane == 0 && sside && n > 0) {
                 ok = wait(&q_full[t], kt++);
                 for (int c = 0; ok && c < n; ++c, ++g, ++gt) {
                     const unsigned st = g % NS;
@@ -421,8 +421,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 
             // -- Q of this row as f16: the first 64 elements to TMEM as pairs, the
             // rest to shared memory (128-byte swizzle); the item before is done
-            // with both
-            {
+            // with both.  Only for an item with steps here: S of its first step then
+            // shows that q_full was seen before the next item completes it again.
+            if (C == 1 || it.nsteps > 0) {
                 const T *q = static_cast<const T *>(p.q) + (long long)(it.q0 + tok) * p.q_seq_stride +
                              (long long)(it.j * G + head) * D;
 #pragma unroll

@@ -264,6 +264,18 @@ def test_items_shared_by_none_two_and_four_blocks(cuda_lib, seqs, n):
     assert_close(gpu_multi(cuda_lib, b), oracle_multi(b), f"{seqs} x {n}")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs", [50, 52])
+def test_items_without_steps_for_some_blocks(cuda_lib, seqs, D):
+    """Around a hundred items of one or two steps, shared by four blocks: most
+    blocks have no step of most items, several items in a row."""
+    b = batch(785 + seqs, num_seqs=seqs, min_ctx=0, max_ctx=70, n_new=(9, 16), num_heads=8,
+              num_kv_heads=2, head_dim=D, dtype="bf16")
+    ref = oracle_multi(b)
+    for _ in range(20):
+        assert_close(gpu_multi(cuda_lib, b), ref, f"{seqs} short items")
+
+
 @pytest.mark.parametrize("n", [4, 100])
 @pytest.mark.parametrize("ctx", [50, 3000])
 def test_nan_keys(cuda_lib, n, ctx):
