@@ -751,6 +751,9 @@ int rope_common(pa::RopeParams &p, bool fp8, int64_t num_blocks, int32_t block_s
     if (p.num_heads > 0 && (!aligned16(p.q) || !aligned16(p.q_out) || !strided16(p.q_stride, es) ||
                             !strided16(p.q_out_stride, es)))
         return PA_ERR_INVALID_ARG;
+    // in place, a token's row is written where it was read
+    if (p.num_heads > 0 && p.q_out == p.q && p.num_tokens > 1 && p.q_out_stride != p.q_stride)
+        return PA_ERR_INVALID_ARG;
     if (!aligned16(p.q_weight) || !aligned16(p.k_weight)) return PA_ERR_INVALID_ARG;
     if (p.rot_dim > 0 && !aligned16(p.rope_table)) return PA_ERR_INVALID_ARG;
     p.num_slots = num_blocks * 16;

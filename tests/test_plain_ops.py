@@ -117,6 +117,14 @@ def test_append_refusals(lib, fp8, kw, status):
     assert _rope(lib, fp8, **kw) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(qs=640), dict(qos=640),                   # in place, one stride
+    dict(q_out=32, qs=504), dict(q_out=32, qos=504), dict(q_out=32, qs=516),
+    dict(q_out=32, qos=516)])
+def test_append_strides_in_place_and_apart(lib, kw):
+    assert _rope(lib, **kw) == _rope(lib, True, **kw) == -1
+
+
 def test_append_fp8_needs_scales(lib):
     assert _rope(lib, True, k_scale=None) == -1 and _rope(lib, True, v_scale=None) == -1
 
