@@ -16,9 +16,11 @@
 // Bound by HBM for batches (one or two rows of the vocabulary per sequence),
 // by latency for one sequence.  A cluster of C blocks takes one sequence: the
 // row is cut into C * 16 runs, one per warp, each summed in one pass; the
-// block sums meet through distributed shared memory, and only the run that
-// holds the border is read again, by the whole block that owns it.  One launch,
-// no workspace, no atomics on global memory, a fixed order of additions.
+// block sums meet through distributed shared memory (after a first cluster
+// barrier, whose wait the sums hide: no peer is written to before it is known to
+// run), and only the run that holds the border is read again, by the whole block
+// that owns it.  One launch, no workspace, no atomics on global memory, a fixed
+// order of additions.
 //
 // Measured: one sequence over 32000 tokens 6.8 us on the device (rows, tokens and
 // uniforms 1 us, the sums 1.5, the cluster's exchange 1.2, the border and its
@@ -193,6 +195,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_drafts_kernel(const __gr
         }
         return;
     }
+    if (C > 1) cluster_arrive();                    // this block runs (see cluster_wait below)
     const float us = p.sample_u[s];
     const T *target = static_cast<const T *>(p.target);
     const T *draft = static_cast<const T *>(p.draft);
@@ -269,12 +272,15 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_drafts_kernel(const __gr
         for (int o = 16; o > 0; o >>= 1) sum.add(shfl_xor(sum, o));
         if (lane == 0) sh_warp[warp] = sum;
         __syncthreads();
+        // a peer's shared memory may be written once that block is known to run
+        if (pass == 0 && C > 1) cluster_wait();
         Pair mine{0.f, 0.f}, upto, below;           // lane w of warp 0: run w's sum, up to it, below it
         if (warp == 0) {
             if (lane < VF_WARPS) mine = sh_warp[lane];
             upto = scan<VF_WARPS>(mine, lane, &below);
             const Pair block = shfl(upto, VF_WARPS - 1);
             if (lane < C) st_dsmem(map_to_rank(&sh_blocks[pass][rank], (uint32_t)lane), block);
+            __syncwarp();                           // the barrier below is one of whole warps
         }
         cluster_sync();
         // ---- the border u W: the first block whose sums reach past it (or the
