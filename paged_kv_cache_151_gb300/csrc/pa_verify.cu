@@ -91,9 +91,10 @@ __device__ __forceinline__ Pair scan(const Pair &a, int lane, Pair *before) {
 }
 
 // u q < p for u, p, q >= 0, exactly: the product's rounding error is one fma
-// away where it does not underflow.
+// away where it does not underflow.  It is a multiple of the factors' last bits,
+// 2^-73 each above 2^-50, and those of 2^-149 are binary32 numbers.
 __device__ __forceinline__ bool product_below(float u, float q, float p) {
-    if (u > 0x1p-60f && q > 0x1p-60f) {
+    if (u > 0x1p-50f && q > 0x1p-50f) {
         const float h = u * q, e = fmaf(u, q, -h);
         return h < p || (h == p && e < 0.f);
     }
