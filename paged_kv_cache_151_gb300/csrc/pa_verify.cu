@@ -292,10 +292,13 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_drafts_kernel(const __gr
             const Pair sums = scan<VF_MAX_CLUSTER>(b, lane, &before);      // blocks 0 .. lane
             const Pair W = shfl(sums, VF_MAX_CLUSTER - 1);
             const float u = us > 0.f ? fminf(us, 1.f) : 0.f;
+            // u = 1 takes the last weight, however far below the sums' last bit it
+            // is: no sum is past the border then, at any level
+            const bool last = u == 1.f;
             Pair x;                                 // u W
             x.hi = u * W.hi;
             x.lo = fmaf(u, W.hi, -x.hi) + u * W.lo;
-            const unsigned past = __ballot_sync(0xffffffffu, lane < C && b.hi > 0.f && sums.above(x));
+            const unsigned past = __ballot_sync(0xffffffffu, lane < C && b.hi > 0.f && !last && sums.above(x));
             const unsigned any = __ballot_sync(0xffffffffu, lane < C && b.hi > 0.f);
             int o = -2;
             if (any && W.hi < INFINITY && W.lo < INFINITY) {
@@ -304,12 +307,12 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_drafts_kernel(const __gr
                 if (blk == rank) {
                     const Pair base = shfl(before, blk);
                     x.add(Pair{-base.hi, -base.lo});               // from the block's start
-                    const unsigned rp = __ballot_sync(0xffffffffu, mine.hi > 0.f && upto.above(x));
+                    const unsigned rp = __ballot_sync(0xffffffffu, mine.hi > 0.f && !last && upto.above(x));
                     const unsigned ra = __ballot_sync(0xffffffffu, mine.hi > 0.f);
                     o = rp ? __ffs(rp) - 1 : 31 - __clz(ra);
                     const Pair run = shfl(below, o);
                     x.add(Pair{-run.hi, -run.lo});                 // from the run's start
-                    if (lane == 0) sh_goal = x;
+                    if (lane == 0) sh_goal = last ? Pair{INFINITY, 0.f} : x;
                 }
             }
             if (lane == 0) sh_own = o;

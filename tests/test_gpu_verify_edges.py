@@ -45,3 +45,17 @@ def test_accept_products_next_to_the_target(cuda_lib):
     out, acc = check(cuda_lib, t, d, np.ones(2 * B, dtype=np.int32), au, np.full(B, 0.5),
                      np.arange(0, 2 * B + 1, 2))
     assert np.array_equal(acc, want)
+
+
+@pytest.mark.parametrize("V", [64, 3000, 40000])
+@pytest.mark.parametrize("B", [1, 9, 60, 200])
+def test_uniform_of_one_takes_the_last_weight(cuda_lib, B, V):
+    """Peaked rows, whose last weights are far below the last bit of their sum."""
+    r = np.random.default_rng(V + B)
+    logits = 12 * r.standard_normal((B, V))
+    w = np.exp(logits - logits.max(1, keepdims=True)).astype(np.float32)
+    w[:, V - V // 8:] = 0                          # no weight at the end of the row
+    t = torch.from_numpy(w).cuda()
+    out, acc = check(cuda_lib, t, None, np.zeros(B), np.zeros(B),
+                     np.where(np.arange(B) % 2 == 0, 1.0, 2.5), np.arange(B + 1))
+    assert np.array_equal(out[:, 0], [np.flatnonzero(x)[-1] for x in w])
