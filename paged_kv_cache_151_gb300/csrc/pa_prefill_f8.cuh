@@ -160,6 +160,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     uint64_t *mma_idle = q_full + 14;      // the block's MMAs are all done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::OFF_TMEM);
     __shared__ PrefillSched sched;
+    __shared__ int bad_seq[8];             // softmax warps: sequence of an item with bad blocks
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hkv = p.num_kv_heads, H = p.num_heads;
@@ -412,7 +413,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             const bool row_ok = 128 * t + r < it.nrows;
             // last visible position; rows past the run see what its last row sees
             const int lim = it.L - it.nq + min(tok, it.nq - 1);
-            const int cmask = (__reduce_min_sync(0xffffffffu, lim) + 1) / PF8_KEYS;   // steps before: no mask
+            int cmask = (__reduce_min_sync(0xffffffffu, lim) + 1) / PF8_KEYS;   // steps before: no mask
             // the score scale; a negative one moves its sign to q, and one of 0 is
             // a tiny one, so that masked scores stay -inf
             float sl2 = p.scale_log2 * __ldg(p.k_scale + it.j);
@@ -453,6 +454,23 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                 if (lane == 0) mbar_arrive(&q_full[t]);
             }
 
+            // If this block's steps name a block outside the pool, its keys (zeros in
+            // the stages) are masked, as if no row saw them: every step goes through
+            // the masks below then (cmask < 0).
+            {
+                const int32_t *tab = p.block_tables + (long long)it.s * p.max_blocks;
+                const int end = min(4 * (it.step0 + it.nsteps), (it.L + 15) >> 4);
+                bool bad = false;
+#pragma unroll 8
+                for (int i = 4 * it.step0 + lane; i < end; i += 32)
+                    bad |= (unsigned long long)(long long)tab[i] >= (unsigned long long)p.num_blocks;
+                if (__any_sync(0xffffffffu, bad)) {
+                    cmask = -1;
+                    if (lane == 0) bad_seq[warp] = it.s;   // no register over the steps
+                    __syncwarp();
+                }
+            }
+
             float m_run = -INFINITY, l_run = 0.f;
             for (int c = 0; c < it.nsteps; ++c, ++g) {
                 const int step = it.step0 + c;
@@ -464,8 +482,20 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                 if (lane == 0) mbar_arrive(&s_free[t]);
                 if (step >= cmask) {
                     const int nvis = lim - step * PF8_KEYS + 1;     // positions of this step the row sees
+                    uint64_t vis = nvis >= 64 ? ~0ull : nvis > 0 ? (1ull << nvis) - 1 : 0ull;
+                    if (cmask < 0) {
+                        const int s = *(volatile int *)&bad_seq[warp];
+                        const int32_t *tab = p.block_tables + (long long)s * p.max_blocks + 4 * step;
+                        const int left = p.seq_lens[s] - step * PF8_KEYS;
+                        for (int b = 0; b < 4; ++b)
+                            if (16 * b < left &&
+                                (unsigned long long)(long long)tab[b] >= (unsigned long long)p.num_blocks)
+                                vis &= ~(0xffffull << (16 * b));
+                    }
+                    const uint32_t vl = (uint32_t)vis, vh = (uint32_t)(vis >> 32);
 #pragma unroll
-                    for (int e = 0; e < PF8_KEYS; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
+                    for (int e = 0; e < PF8_KEYS; ++e)
+                        sv[e] = ((e < 32 ? vl : vh) >> (e & 31)) & 1 ? sv[e] : -INFINITY;
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
