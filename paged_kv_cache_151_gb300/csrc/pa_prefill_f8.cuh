@@ -415,10 +415,10 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             const int lim = it.L - it.nq + min(tok, it.nq - 1);
             int cmask = (__reduce_min_sync(0xffffffffu, lim) + 1) / PF8_KEYS;   // steps before: no mask
             // the score scale; a negative one moves its sign to q, and one of 0 is
-            // a tiny one, so that masked scores stay -inf
+            // a tiny one, so that masked scores stay -inf; a NaN stays one
             float sl2 = p.scale_log2 * __ldg(p.k_scale + it.j);
             const uint32_t sign = sl2 < 0.f ? 0x80008000u : 0u;
-            sl2 = fmaxf(fabsf(sl2), 1e-30f);
+            sl2 = fabsf(sl2) < 1e-30f ? 1e-30f : fabsf(sl2);
 
             // -- Q of this row as f16: the first 64 elements to TMEM as pairs, the
             // rest to shared memory (128-byte swizzle); the item before is done

@@ -1,5 +1,5 @@
 """Corners of pa_decode_multi_fp8 at which its two kernels (runs of few rows, runs
-of many) have to say the same: bad blocks."""
+of many) have to say the same: bad blocks, a NaN scale."""
 import numpy as np
 import pytest
 import torch
@@ -64,3 +64,16 @@ def test_rows_that_see_bad_blocks_alone_are_zero(cuda_lib, n):
     for s in range(2):
         assert (out[qs[s]:qs[s] + min(n, 16 * len(bad))] == 0).all()
         assert_close(out[qs[s]:qs[s + 1]], attend_64(b, s, bad), "no keys")
+
+
+@pytest.mark.parametrize("n", [2, 50])
+@pytest.mark.parametrize("ctx", [40, 3000])
+def test_nan_key_scale(cuda_lib, ctx, n):
+    """A KV head whose scale is NaN has NaN scores; the others keep their rows."""
+    b = batch(930, num_seqs=2, min_ctx=ctx, max_ctx=ctx, n_new=n, num_heads=8, num_kv_heads=2,
+              head_dim=128, dtype="bf16")
+    good = gpu_multi(cuda_lib, b)
+    b.meta["k_scale"] = b.meta["k_scale"].clone()
+    b.meta["k_scale"][1] = float("nan")
+    out = gpu_multi(cuda_lib, b)
+    assert out[:, 4:].isnan().all() and torch.equal(out[:, :4], good[:, :4])
