@@ -123,6 +123,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+// a += the low f16 of w, b += the high one (the mixed-precision add of sm_100 and
+// later: exact widening, one rounding).
+__device__ __forceinline__ void add_halves(float &a, float &b, uint32_t w) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "add.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+        : "+f"(a), "+f"(b) : "r"(w));
+}
 
 constexpr float LOG2E = 1.4426950408889634f;   // log2(e)
 constexpr float LN2 = 0.6931471805599453f;     // ln(2)

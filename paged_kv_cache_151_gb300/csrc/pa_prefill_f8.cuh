@@ -517,9 +517,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 #pragma unroll
                 for (int e = 0; e < PF8_KEYS / 2; ++e) {
                     const float2 x = fma2(make_float2(sv[2 * e], sv[2 * e + 1]), sc2, nm2);
-                    const float2 pe = make_float2(ex2(x.x), ex2(x.y));
-                    pw[e] = Mma<__half>::pack(pe.x, pe.y);
-                    acc[e & 3] = add2(acc[e & 3], pe);
+                    pw[e] = Mma<__half>::pack(ex2(x.x), ex2(x.y));
+                    // the weights as P V uses them: their rounding cancels in O / l
+                    add_halves(acc[e & 3].x, acc[e & 3].y, pw[e]);
                 }
                 const float2 a2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
                 l_run = l_run * alpha + (a2.x + a2.y);

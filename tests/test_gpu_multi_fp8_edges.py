@@ -1,5 +1,7 @@
 """Corners of pa_decode_multi_fp8 at which its two kernels (runs of few rows, runs
-of many) have to say the same: bad blocks, a NaN scale."""
+of many) have to say the same: bad blocks, a NaN scale, weights that f16 rounds."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -77,3 +79,40 @@ def test_nan_key_scale(cuda_lib, ctx, n):
     b.meta["k_scale"][1] = float("nan")
     out = gpu_multi(cuda_lib, b)
     assert out[:, 4:].isnan().all() and torch.equal(out[:, :4], good[:, :4])
+
+
+def one_key_above(pa, S, L, n, D, v_first, v_rest, v_scales, B=1):
+    """Every row's first key scores S above the others in log2, all others 0, over L
+    keys and n tokens of 4 heads a KV head; the values are v_first and v_rest.  B
+    sequences have the same blocks.  Returns the rows [B, n, Hkv, 4, D] in 64 bits
+    and the number of other keys of each token."""
+    Hkv, nb = len(v_scales), (L + 15) // 16
+    code = lambda x: int(torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8))  # noqa: E731
+    kc = torch.zeros(nb, Hkv, 16, D, dtype=torch.uint8, device="cuda")
+    kc[0, :, 0, 0] = code(1.0)
+    vc = torch.full((nb, Hkv, 16, D), code(v_rest), dtype=torch.uint8, device="cuda")
+    vc[0, :, 0] = code(v_first)
+    q = torch.zeros(B * n, 4 * Hkv, D, device="cuda", dtype=torch.float16)
+    q[:, :, 0] = 1
+    out = torch.full_like(q, float("nan"))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    pa.pa_decode_multi_fp8(out, q, kc, vc, torch.ones(Hkv, device="cuda"),
+                           torch.tensor(v_scales, dtype=torch.float32, device="cuda"),
+                           torch.arange(nb, dtype=torch.int32, device="cuda")[None].repeat(B, 1),
+                           i32([L] * B), i32([n * s for s in range(B + 1)]), n, S * math.log(2), Hkv)
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy().reshape(B, n, Hkv, 4, D), (L - n + np.arange(n)).astype(float)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [2, 8, 9, 100])
+def test_equal_values_come_back_whatever_the_weights(cuda_lib, n, D):
+    """All values of a head equal v: the result is v.  With S = -log2(0.50024) the
+    other keys' weight lies just below the middle of two f16 numbers and loses
+    4.8e-4 of itself in P, which the sum has to lose too.  What is left: the
+    output's half step 2^-11 |v|, V's scale and the division (4 of 2^-24), and
+    the accumulation of 4000 keys sixteen at a time, 2^-23 each."""
+    vs = np.float32(1 + 1.2e-4 * np.arange(8))
+    out, _ = one_key_above(cuda_lib, -math.log2(0.50024), 4000, n, D, 1.0, 1.0, vs.tolist())
+    v = vs.astype(float)[None, :, None, None]
+    assert (np.abs(out - v) <= v * (2.0**-11 + 4 * 2.0**-24 + 4000 / 16 * 2.0**-23)).all()
