@@ -340,6 +340,15 @@ __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Reference levels of multi-token rows (log2 units): a level is set F8_BELOW_LOG2
+// under a maximum and stays until a score is more than F8_TOP_LOG2 above it.
+// The weights 2^(score - level) thus stay below 2^15, inside f16, whose rounding
+// of them is 2^-11 of the weight down to 2^-21 of the largest and 2^-32 of that
+// below: less than what the fp32 accumulators drop, which is keys below 2^-25 of
+// what they hold.  (With levels at the maximum, a weight of 2^-24.9 became 2^-24
+// and 60000 of them 3.6e-3 of the row instead of 1.9e-3.)
+constexpr float F8_BELOW_LOG2 = 7.f, F8_TOP_LOG2 = 15.f;
+
 // Sixteen query rows at once: the (query token, head) pairs of a multi-token
 // query that share one KV head, each with its own causal limit, in the
 // layouts of WarpAttnF8.  Lane (g, t) scores rows g ("lo") and g + 8 ("hi");
@@ -347,7 +356,7 @@ __device__ __forceinline__ void mma_f16(float *d, uint32_t a0, uint32_t a1, uint
 // the V fragments, so a block's codes are converted once for 16 rows.
 //
 // A row's reference level moves only when a score exceeds it by more than
-// 2^RESCALE_LOG2, and only then do its lanes exchange their maxima: (m, l, acc)
+// F8_TOP_LOG2, and only then do its lanes exchange their maxima: (m, l, acc)
 // are to that level, not to the true maximum.
 //
 // Measured: 256 sequences of four rows (312 MB of codes) 91 us = 3.4 TB/s, 0.51 of
@@ -483,12 +492,12 @@ struct WarpAttnF8x16 {
         float mx[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) mx[h] = fmaxf(max3f(sc[h][0], sc[h][1], sc[h][2]), sc[h][3]);
-        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + RESCALE_LOG2 || mx[1] > m_run[1] + RESCALE_LOG2)) {
+        if (__any_sync(0xffffffffu, mx[0] > m_run[0] + F8_TOP_LOG2 || mx[1] > m_run[1] + F8_TOP_LOG2)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
                 mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                const float m_new = mx[h] > m_run[h] + RESCALE_LOG2 ? mx[h] : m_run[h];
+                const float m_new = mx[h] > m_run[h] + F8_TOP_LOG2 ? mx[h] - F8_BELOW_LOG2 : m_run[h];
                 const float alpha = m_new == m_run[h] ? 1.f : ex2(m_run[h] - m_new);
                 m_run[h] = m_new;
                 l_run[h] *= alpha;

@@ -506,8 +506,8 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     m4[3] = max3f(m4[3], sv[e + 6], sv[e + 7]);
                 }
                 const float mxs = max3f(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
-                // lazy rescaling: the reference level moves only by more than 2^RESCALE_LOG2
-                const float m_new = mxs > m_run + RESCALE_LOG2 ? mxs : m_run;
+                // lazy rescaling: see F8_BELOW_LOG2
+                const float m_new = mxs > m_run + F8_TOP_LOG2 ? mxs - F8_BELOW_LOG2 : m_run;
                 const float ms = m_new == -INFINITY ? 0.f : m_new;
                 const float alpha = m_new == m_run ? 1.f : ex2(m_run - ms);
                 uint32_t pw[PF8_KEYS / 2];

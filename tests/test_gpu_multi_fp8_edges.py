@@ -116,3 +116,26 @@ def test_equal_values_come_back_whatever_the_weights(cuda_lib, n, D):
     out, _ = one_key_above(cuda_lib, -math.log2(0.50024), 4000, n, D, 1.0, 1.0, vs.tolist())
     v = vs.astype(float)[None, :, None, None]
     assert (np.abs(out - v) <= v * (2.0**-11 + 4 * 2.0**-24 + 4000 / 16 * 2.0**-23)).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,n", [(1, 2), (1, 8), (1, 9), (1, 100), (600, 2), (76, 64)])
+@pytest.mark.parametrize("S", [24.9, 25.2, 27.0])
+def test_one_key_above_a_long_tail(cuda_lib, S, B, n, D):
+    """60000 keys 2^-S below one: together 1.9e-3 (S = 24.9) to 4.5e-4 of its weight,
+    in few pieces (many sequences) or many.  The result is v (1 - x) / (1 + x), x
+    the tail's share, for values v and -v.  Allowed: the output's half step 2^-11,
+    the accumulation of the keys sixteen at a time (2^-23 each), a tail off by
+    half of a 16th (its weights are f16 numbers of four bits at the least), which
+    moves the result by 2 x / 32.
+
+    Where S > 25 the tail may be missing from the products' sum: that is kept in
+    binary32 with the first key's weight in it, 1 + 2^-S is 1 there (the last bit
+    of 1 is 2^-23, half of it 2^-24), and the matrix instructions align every
+    product to the sum on its own.  (1 - x) / (1 + x) becomes 1 / (1 + x): x more."""
+    L = 60000
+    out, others = one_key_above(cuda_lib, S, L, n, D, 1.0, -1.0, [1.0, 0.5], B)
+    x = others * 2.0**-S
+    want = ((1 - x) / (1 + x))[:, None, None, None] * np.array([1.0, 0.5])[None, :, None, None]
+    tol = 2.0**-11 + L / 16 * 2.0**-23 + 2 * x.max() / 32 + (x.max() if S > 25 else 0)
+    assert (np.abs(out - want) <= tol * np.abs(want)).all(), np.abs(out / want - 1).max()
