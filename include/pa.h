@@ -616,10 +616,11 @@ int pa_device_error(uint32_t *flags, int clear);
  * pa_test_stall_next_decode -- test hook for the kernels' bounded waits.  The
  * next decode call (any pa_decode* entry point, from any host thread) makes
  * the first copy of every warp of its persistent kernel expect 16 bytes more
- * than it delivers, so the wait for that copy runs out at its 1 s limit: the
- * kernel sets PA_DEVERR_TIMEOUT, waits (bounded) for its copies in flight and
- * returns, leaving that call's output incomplete (the call takes ~2 s).  The
- * context stays usable.  For tests of the error path only.  Returns PA_OK.
+ * than it delivers -- in the long runs of pa_decode_multi_fp8, the first keys of
+ * every thread block never count as arrived -- so the wait for it runs out at its
+ * 1 s limit: the kernel sets PA_DEVERR_TIMEOUT, waits (bounded) for its copies in
+ * flight and returns, leaving that call's output incomplete (the call takes ~2 s).
+ * The context stays usable.  For tests of the error path only.  Returns PA_OK.
  */
 int pa_test_stall_next_decode(void);
 

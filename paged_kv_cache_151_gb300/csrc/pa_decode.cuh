@@ -82,7 +82,8 @@ struct DecodeParams {
     const float *v_scale;
     float scale_log2;         // scale * log2(e)
     int test_stall = 0;       // test hook (pa_test_stall_next_decode): each warp's
-                              // first copy expects 16 bytes it never gets
+                              // first copy expects 16 bytes it never gets; in the
+                              // E4M3 prefill kernel a block's first K never arrives
     unsigned int *err;        // device error word
     // 16-bit and E4M3 caches, persistent kernel: the caches as 3-D tensors
     // [num_blocks*num_kv_heads][16 rows][head_dim], read in swizzled boxes

@@ -169,7 +169,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     // for this grid before it touches the caches or out
     launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < 4 * NS; ++i) mbar_init(&bars[i], 2);
+        // test hook: with one arrival more than there are, a block's first K never
+        // counts as converted, and the waits for it and for what it holds up run out
+        for (int i = 0; i < 4 * NS; ++i) mbar_init(&bars[i], i == 0 && p.test_stall ? 3 : 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 4);
             mbar_init(&s_full[t], 1);

@@ -1,13 +1,15 @@
 """Corners of pa_decode_multi_fp8 at which its two kernels (runs of few rows, runs
-of many) have to say the same: bad blocks, a NaN scale, weights that f16 rounds."""
+of many) have to say the same: bad blocks, a NaN scale, weights that f16 rounds,
+waits that run out."""
 import math
+import time
 
 import numpy as np
 import pytest
 import torch
 
 from test_gpu_multi_fp8 import (_clean_error_word, assert_close, batch, dequantised,  # noqa: F401
-                                gpu_multi)
+                                gpu_multi, oracle_multi)
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +141,19 @@ def test_one_key_above_a_long_tail(cuda_lib, S, B, n, D):
     want = ((1 - x) / (1 + x))[:, None, None, None] * np.array([1.0, 0.5])[None, :, None, None]
     tol = 2.0**-11 + L / 16 * 2.0**-23 + 2 * x.max() / 32 + (x.max() if S > 25 else 0)
     assert (np.abs(out - want) <= tol * np.abs(want)).all(), np.abs(out / want - 1).max()
+
+
+@pytest.mark.parametrize("seqs,n", [(38, 64), (15, 64), (1, 64), (1, 3)])
+def test_long_runs_that_wait_too_long(cuda_lib, seqs, n):
+    """Keys that never arrive, for runs of many rows in items of one, two and four
+    blocks: the call ends with PA_DEVERR_TIMEOUT, and the next one is right."""
+    b = batch(940 + seqs, num_seqs=seqs, min_ctx=100, max_ctx=700, n_new=n, num_heads=8,
+              num_kv_heads=2, head_dim=128, dtype="bf16")
+    ref = oracle_multi(b)
+    assert_close(gpu_multi(cuda_lib, b), ref, "before")
+    t0 = time.perf_counter()
+    cuda_lib.pa_test_stall_next_decode()
+    gpu_multi(cuda_lib, b)
+    assert cuda_lib.pa_device_error(clear=True) == cuda_lib.PA_DEVERR_TIMEOUT
+    assert time.perf_counter() - t0 < 30
+    assert_close(gpu_multi(cuda_lib, b), ref, "after the timeout")
