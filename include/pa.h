@@ -65,7 +65,8 @@
  * (pa_reshape_and_cache, pa_reshape_and_cache_fp8, or pa_rope_and_cache and its
  * _fp8 form without queries), they start while it finishes and read seq_lens,
  * block_tables and query_start meanwhile -- the cache writes never touch those --
- * and touch the caches, q and out only after it has completed.  After any other kernel they start as usual.
+ * and touch the caches, q and out only after it has completed.  After any other
+ * kernel they start as usual.
  *
  * Errors.  Calls return PA_OK (0) or a negative pa_status; nothing is
  * launched when the host-side checks fail.  Contents of device arrays are not
@@ -344,9 +345,10 @@ int pa_decode_multi(void *out, const void *q, const void *k_cache,
  *         (or target_probs[r-1] with w_x = 0 without draft probabilities; if
  *         nothing is left, target_probs[r-1] itself);
  *   w_v = target_probs[last row][v]                          if all are accepted.
- * The difference is rounded to binary32, sums are taken as in binary64:
- * the token is the first v with w_0 + .. + w_v > u * sum(w), u =
- * sample_uniform[s] clamped to [0, 1] (at u = 1 the last v with a weight).  Entries
+ * The difference is rounded to binary32; a sum is a pair of binary32 numbers,
+ * itself and what its roundings lost (about 46 bits together).  The token is the
+ * first v with w_0 + .. + w_v > u * sum(w), u = sample_uniform[s] clamped to
+ * [0, 1] and NaN as 0 (at u = 1 the last v with a weight).  Entries
  * that are negative or NaN count as 0, and an infinite entry leaves weight 0;
  * a row without any weight gives token -1.  Sums must stay inside the binary32
  * range.
@@ -487,7 +489,12 @@ int pa_decode_partitioned_fp8(void *out, const void *q, const void *k_cache,
  * pa_decode_multi_fp8 -- pa_decode_multi over E4M3 caches: several new tokens
  * per sequence (drafts to verify, or a chunk of a prompt), causal among
  * themselves, K_s[t] and V_s[t] dequantised as in pa_decode_fp8.  `dtype` is the
- * type of q and out, PA_BF16 or PA_F16 (q is rounded to f16: |q| < 65504).
+ * type of q and out, PA_BF16 or PA_F16.  q is rounded to f16: |q| < 65504, in
+ * steps of 2^-24 below 2^-14 (a bf16 query under 2^-25 counts as 0).  Weights are
+ * rounded to f16 relative to the row's largest (half a step 2^-11; the sum that
+ * divides is of the rounded ones) and sums are fp32: keys each below 2^-25 of
+ * what a row has summed so far may add nothing, n of them up to n 2^-25 of the
+ * row.  A block id outside the pool is left out of every row that would see it.
  * Rows, query_start, errors and requirements as pa_decode_multi.  As there, a
  * NaN among the values of a run's new tokens may also reach rows of the run that
  * stand before it (the product with a weight of 0); every other row past a
@@ -625,7 +632,10 @@ int pa_device_error(uint32_t *flags, int clear);
 int pa_test_stall_next_decode(void);
 
 /* ABI version of this header (increments when the signature or the meaning of a
- * declared function changes; functions may be added without). */
+ * declared function changes).  Additions raised it up to 4, and no longer do:
+ * pa_rope_and_cache, pa_rope_and_cache_fp8, pa_decode_multi_fp8 and
+ * pa_verify_drafts came to version 4, so a loader that may meet an older library
+ * looks these four up by name. */
 int pa_abi_version(void);
 
 #ifdef __cplusplus

@@ -113,9 +113,9 @@ cudaError_t verify_drafts(const VerifyParams &p, int dtype, cudaStream_t st);
 constexpr int PREFILL_F8_ROWS = 256;       // rows of one item
 // Runs of at least so many rows go there.  Two 16-row tiles (20 rows, 4 heads a
 // group) read their keys twice on the persistent kernel and are still faster
-// there in a batch (32 sequences x 6000 keys 185 us against 242, 128 x 500: 79
-// against 101); with three tiles (36 rows) it is the other way round (273 against
-// 243, 109 against 103), and a single sequence is even.  The kernel looks its
+// there in a batch (32 sequences x 6000 keys 184 us against 245, 128 x 500: 81
+// against 112); with three tiles (36 rows) it is 268 against 246 over 6000 keys
+// and 111 against 114 over 500, and a single sequence is even (36.6 against 35).  The kernel looks its
 // items up by walking the sequences when there are more than 256.
 constexpr int prefill_f8_min_rows(int num_seqs) { return num_seqs <= 256 ? 33 : PREFILL_GROUP_ROWS; }
 cudaError_t prefill_f8_bf16(const DecodeParams &p, int D, int G, int groups, cudaStream_t st);

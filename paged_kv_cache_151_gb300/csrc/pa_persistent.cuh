@@ -302,8 +302,8 @@ __host__ __device__ constexpr int persistent_warps() {
 // Blocks per SM the kernel is built for: eight warps of 16-bit tiles per SM
 // (one block of eight or two of four); E4M3 tiles are half the bytes, so
 // three blocks of four fit and hide more latency (two for multi-token queries:
-// their partials of 16 rows would leave a third block two stages a warp, and
-// the matrix pipe is what they wait for: 91 us either way).
+// their partials of 16 rows would leave a third block two stages a warp: 91 us
+// either way).
 template <typename KV, int NW, int MODE>
 __host__ __device__ constexpr int persistent_blocks_per_sm() {
     return sizeof(KV) == 1 ? (MODE == MODE_MULTI ? 2 : PA_F8_BLOCKS_PER_SM) : (NW >= 8 ? 1 : 2);

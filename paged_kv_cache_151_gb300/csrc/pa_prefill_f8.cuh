@@ -47,13 +47,16 @@
 // block stops and the error word says so.
 //
 // Measured: 2048 rows of 32 query heads (8 KV heads of 128) over 14 to 16 thousand
-// keys 495 us in a long run (441 us in a short one, before the power limit):
-// 1.03 PFLOP/s, 0.54 of the measured bf16 peak; 256 items are 1.68 waves of the
-// 152 SMs, so the SMs that work run at 0.65.  Three runs of 200 to 500 tokens
-// (16 heads over 2, head_dim 64) over up to 6000 keys: 53 us.  A step of one tile
-// alone takes 0.82 us: the chain S, wait, load, softmax, wait, store, P V, not
-// its arithmetic (without the exponentials, the maximum or the sum 0.80 us and
-// more), so short lists of items are bound by it.
+// keys 510 us a call over three sets of inputs in turn: 1.00 PFLOP/s, 0.53 of the
+// measured bf16 peak (467 us over one set, whose codes stay in L2); 256 items are
+// 1.68 waves of the 152 SMs, so the SMs that work run at 0.63.  Three
+// runs of 200 to 500 tokens (16 heads over 2, head_dim 64) over up to 6000 keys:
+// 54.6 us.  A step of one tile alone takes 0.82 us and not for its arithmetic
+// (without the exponentials, the maximum or the sum 0.80 us and more): what is
+// left is the chain S, wait, load, softmax, wait, store, P V and the converters'
+// loads, which were not timed apart.  Short lists of items are bound by the step.
+// Summing the weights as rounded instead of in fp32 is 2 % of both, the masks of
+// bad blocks 1.5 %.
 #pragma once
 
 #include <atomic>

@@ -26,7 +26,10 @@
 // Measured: 32768 tokens (32 + 8 + 8 heads of 128, norms, E4M3 cache; 755 MB) 150 us =
 // 5.0 TB/s, 0.75 of the measured copy rate; 1024 tokens 10.3 us and one token
 // 4.1 us on the device, where a warp's chain of slot and position, table and data
-// loads counts.
+// loads counts.  The launch cuts a call for 32 warps an SM and 20 fit: 1024
+// tokens are 4096 warps of three iterations, 1.35 waves of 3040, and 4099 tokens
+// of 16 + 4 + 4 heads of 64 are 8198 of two, 2.70 waves (10.3 us as well), so the
+// chain is paid more than once.
 #include <type_traits>
 
 #include "pa_common.cuh"

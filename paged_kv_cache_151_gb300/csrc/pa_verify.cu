@@ -22,11 +22,12 @@
 // that owns it.  One launch, no workspace, no atomics on global memory, a fixed
 // order of additions.
 //
-// Measured: one sequence over 32000 tokens 6.8 us on the device (rows, tokens and
-// uniforms 1 us, the sums 1.5, the cluster's exchange 1.2, the border and its
-// run 2); 64 sequences over 131071 tokens in fp32 (53 MB) 18.4 us, 8 to 10 of
-// them streaming; 256 over 50021 in bf16 without draft probabilities (26 MB)
-// 16.4 us, read two bytes a lane (rows of an odd stride start anywhere).
+// Measured, calls of a captured graph: one sequence over 32000 tokens 5.7 us (rows,
+// tokens and uniforms 1 us, the sums 1.5, the cluster's exchange 1.2, the border
+// and its run 2); 64 sequences over 131071 tokens in fp32 (53 MB) 17.2 us, 8 to 10
+// of them streaming; 256 over 50021 in bf16 without draft probabilities (26 MB)
+// 14.6 us, read two bytes a lane (rows of an odd stride start anywhere), eight
+// loads in flight: some twelve round trips to memory in a row.
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -369,7 +370,7 @@ template <typename T>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st) {
     const int sms = sm_count_of_current_device();
     // two blocks per SM fit; more would queue behind each other's chains of loads
-    // (64 sequences of 131071 tokens: 18.4 us at 4 blocks each, 22.5 at 8)
+    // (64 sequences of 131071 tokens: 18.5 us a call at 4 blocks each, 22.5 at 8)
     const int64_t slots = (int64_t)(sms > 0 ? sms : 152) * 2;
     int C = 1;
     while (C < VF_MAX_CLUSTER && (int64_t)p.num_seqs * C * 2 <= slots) C *= 2;
