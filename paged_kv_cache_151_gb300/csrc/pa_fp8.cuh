@@ -360,9 +360,9 @@ constexpr float F8_BELOW_LOG2 = 7.f, F8_TOP_LOG2 = 15.f;
 // are to that level, not to the true maximum.
 //
 // Measured: 256 sequences of four rows (312 MB of codes) 91 us = 3.4 TB/s, 0.51 of
-// the measured copy rate.  Latency bounds it: two warps a scheduler at 221
+// the measured copy rate.  Latency bounds it: two warps a scheduler at 226
 // registers, each going through wait, fragments, scores, softmax and values of
-// one block after the other, issue on 29 % of the cycles.  The matrix pipe does
+// one block after the other, issue on 36 % of the cycles.  The matrix pipe does
 // not: a loop of these instructions on registers runs at 1024 multiply-adds a
 // clock and SM, so the 32 of a block are 64 clocks of it, 17 % of the time.
 // Neither twelve warps an SM instead of eight (two stages each) nor the scores of
