@@ -24,6 +24,13 @@
  *   *_fp8                  the cache writes, decode, split-KV decode and
  *                          multi-token attention over an FP8 (E4M3) cache
  *                          with per-KV-head scales
+ *   *_fp4                  the cache write, its reading, decode, split-KV decode
+ *                          and multi-token attention over a cache of 4-bit
+ *                          (E2M1) codes with a scale for every 16 of them
+ *   pa_build_step          block tables, lengths, positions and slots of a step
+ *   pa_trim_blocks         from lengths on the device; blocks given back
+ *   pa_process_logits      penalties, biases, masks, temperature and softmax
+ *                          between the model's logits and pa_verify_drafts
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -62,7 +69,7 @@
  * pa_device_error, which reads device memory synchronously.  The decode
  * kernels are launched with programmatic stream serialization: when the
  * kernel before them in the stream is a cache write of this library
- * (pa_reshape_and_cache, pa_reshape_and_cache_fp8, or pa_rope_and_cache and its
+ * (pa_reshape_and_cache and its _fp8 and _fp4 forms, or pa_rope_and_cache and its
  * _fp8 form without queries), they start while it finishes and read seq_lens,
  * block_tables and query_start meanwhile -- the cache writes never touch those --
  * and touch the caches, q and out only after it has completed.  After any other
@@ -93,7 +100,8 @@ typedef enum {
     PA_F32 = 0,
     PA_BF16 = 1,
     PA_F16 = 2,
-    PA_E4M3 = 3      /* FP8 E4M3 cache storage (the *_fp8 entry points only) */
+    PA_E4M3 = 3,     /* FP8 E4M3 cache storage (the *_fp8 entry points only) */
+    PA_E2M1 = 4      /* FP4 E2M1 cache storage (the *_fp4 entry points only) */
 } pa_dtype;
 
 typedef enum {
@@ -112,7 +120,9 @@ typedef enum {
 #define PA_DEVERR_SLOT       0x4u  /* a slot >= num_blocks*block_size was skipped */
 #define PA_DEVERR_TIMEOUT    0x8u  /* a wait on an asynchronous copy exceeded its limit */
 #define PA_DEVERR_POSITION   0x10u /* a position outside the rotation table: its token was skipped */
-#define PA_DEVERR_TOKEN      0x20u /* a drafted token outside the vocabulary was rejected */
+#define PA_DEVERR_TOKEN      0x20u /* a drafted token outside the vocabulary was rejected, or a
+                                      token of pa_process_logits outside it was left out */
+#define PA_DEVERR_NO_BLOCKS  0x40u /* pa_build_step: the free list ran out, sequences were refused */
 
 /*
  * pa_reshape_and_cache -- write the step's new keys and values into the cache.
@@ -513,6 +523,198 @@ int pa_decode_multi_fp8(void *out, const void *q, const void *k_cache,
                         float scale, int32_t dtype, void *stream);
 
 /*
+ * FP4 KV cache.
+ *
+ * What the FP8 cache is to the 16-bit one ("vLLM: Architecture, PagedAttention &
+ * Internals", *The knobs that actually matter*, item 5: a smaller cache entry
+ * enlarges the effective pool), once more.  An element is an OCP E2M1 code (1 sign,
+ * 2 exponent bits with bias 1, 1 fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives); every 16 neighbouring elements of a row share an E4M3 scale (its NaN
+ * makes all 16 NaN), and a KV head a float scale as in the FP8 cache:
+ *     value = E2M1(code) * E4M3(scale of the group) * k_scale[j]   (or v_scale[j]).
+ * A tile, the 16 rows of a (block, KV head), is 9 * head_dim contiguous bytes: the
+ * codes of row 0, head_dim / 2 bytes with element 2i in the low half of byte i, of
+ * row 1 and so on; then the scales of row 0, head_dim / 16 bytes, and so on.
+ * k_cache and v_cache are [num_blocks, num_kv_heads, 9, head_dim] bytes.
+ *
+ * pa_reshape_and_cache_fp4 -- the cache write.  For the 16 elements x of a group of
+ * KV head j: y = x / k_scale[j] (rounded to binary32); scale = E4M3(max |y| / 6), the
+ * quotient rounded to binary32 and then to nearest, ties to even, saturating at 448;
+ * code = E2M1(y / scale), likewise, saturating at 6.  A scale of 0 (max |y| at most
+ * 6 * 2^-10) has codes of 0; an infinite y is 6 * 448; a NaN makes its group NaN.
+ * Requirements as pa_reshape_and_cache_fp8, and head_dim <= 1024.
+ *
+ * pa_gather_cache_fp4 -- the rows at the given slots as values: k_out[t] and
+ * v_out[t] ([num_tokens, num_kv_heads, head_dim] of `dtype`, strides as for k and
+ * v) receive what the cache holds at slot_mapping[t], rounded to binary32 and then
+ * to `dtype`.  A negative slot leaves its row as it is, and so does one past the
+ * pool, with PA_DEVERR_SLOT.  Requirements as the write.
+ */
+int pa_reshape_and_cache_fp4(const void *k, const void *v, void *k_cache,
+                             void *v_cache, const float *k_scale,
+                             const float *v_scale, const int64_t *slot_mapping,
+                             int64_t num_tokens, int32_t num_kv_heads,
+                             int32_t head_dim, int64_t k_token_stride,
+                             int64_t v_token_stride, int64_t num_blocks,
+                             int32_t block_size, int32_t dtype, void *stream);
+
+int pa_gather_cache_fp4(void *k_out, void *v_out, const void *k_cache,
+                        const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int64_t *slot_mapping,
+                        int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                        int64_t k_token_stride, int64_t v_token_stride,
+                        int64_t num_blocks, int32_t block_size, int32_t dtype,
+                        void *stream);
+
+/*
+ * pa_decode_fp4, pa_decode_partitioned_fp4, pa_decode_multi_fp4 -- pa_decode_fp8,
+ * pa_decode_partitioned_fp8 and pa_decode_multi_fp8 over E2M1 caches: arguments,
+ * requirements, errors and the rounding of q and of the weights as there (an
+ * element's code times its group's scale is exact).  In the workspace of the
+ * partitioned form m_part is the level that a partition's weights are relative to,
+ * 7 ln 2 to 15 ln 2 below the largest scale * q.k of the partition, and l_part
+ * their sum to that level.  Tokens past a sequence's
+ * end, NaN scales among them, change nothing; a NaN scale of a value reaches the
+ * rows that see its token, and rows of the same run that stand before it.
+ */
+int pa_decode_fp4(void *out, const void *q, const void *k_cache,
+                  const void *v_cache, const float *k_scale, const float *v_scale,
+                  const int32_t *block_tables, const int32_t *seq_lens,
+                  int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                  int32_t head_dim, int64_t num_blocks, int32_t block_size,
+                  int32_t max_blocks_per_seq, int64_t q_seq_stride, float scale,
+                  int32_t dtype, void *stream);
+
+int pa_decode_partitioned_fp4(void *out, const void *q, const void *k_cache,
+                              const void *v_cache, const float *k_scale,
+                              const float *v_scale, const int32_t *block_tables,
+                              const int32_t *seq_lens, int32_t num_seqs,
+                              int32_t num_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int64_t num_blocks,
+                              int32_t block_size, int32_t max_blocks_per_seq,
+                              int64_t q_seq_stride, float scale, int32_t dtype,
+                              int32_t partition_size, int32_t max_seq_len,
+                              void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+int pa_decode_multi_fp4(void *out, const void *q, const void *k_cache,
+                        const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int32_t *block_tables,
+                        const int32_t *seq_lens, const int32_t *query_start,
+                        int32_t num_seqs, int32_t num_q_rows, int32_t max_query_len,
+                        int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int64_t num_blocks, int32_t block_size,
+                        int32_t max_blocks_per_seq, int64_t q_row_stride,
+                        float scale, int32_t dtype, void *stream);
+
+/*
+ * pa_build_step -- what the other calls of a step read, built on the device from
+ * the requests' lengths: "vLLM: Architecture, PagedAttention & Internals", *The free
+ * list and the block table* (ceil(n / block_size) blocks a request, a new one only
+ * when the next token starts it) and *The forward step in detail* (slot = block *
+ * block_size + offset).  For steps whose lengths are on the device, as behind
+ * pa_verify_drafts; blocks that requests share are the host block manager's
+ * (pa_blocks.h), which gives tables that are complete (no free list here).
+ *
+ * State, updated in place:
+ *   request_tables  int32 [num_requests][request_width], the blocks of each request
+ *   request_blocks  int32 [num_requests], how many of them it holds
+ *   free_blocks     int32 [free_capacity], free block ids, taken from the end of the
+ *                   first free_count[0] (its entries are not changed); both NULL:
+ *                   there is nothing to take
+ * The step: request_ids int32 [num_seqs], the request that sequence s runs (distinct;
+ * NULL: request s); context_lens[s], its tokens in the cache; new_lens[s], its new
+ * rows (NULL: one each).  With want = ceil((context + new) / 16), sequence s needs
+ * max(want - request_blocks, 0) blocks; sequences are served in order, each if the
+ * list still holds what it and those before it need.  Then, for a sequence served,
+ *   request_tables[id][held ..] and request_blocks[id] receive its new blocks,
+ *   block_tables[s][0 .. want) its blocks (entries behind stay as they are),
+ *   seq_lens[s] context + new;
+ * and always query_start (int32 [num_seqs + 1], the sums of new_lens), and for row r
+ * = query_start[s] + i positions[r] = context + i and slot_mapping[r] (both int64
+ * [num_rows]); rows behind the last one get position 0 and slot -1.
+ *
+ * A sequence not served has seq_lens 0, slots -1 and its request unchanged: the list
+ * holds too little (PA_DEVERR_NO_BLOCKS; sequences behind it that need blocks are
+ * not served either), or its request id, a length or its rows' place is out of
+ * bounds -- context + new past 16 * the narrower table, rows past num_rows -- with
+ * PA_DEVERR_SEQ_LEN (query_start stays within num_rows).  A table entry outside
+ * [0, num_blocks) gives slot -1 and PA_DEVERR_BLOCK_ID, a free_count outside [0,
+ * free_capacity] the latter too.  A request named twice in a step has undefined
+ * contents.  num_seqs <= 65535.  Calls on one state must be ordered by the caller.
+ */
+int pa_build_step(int32_t *block_tables, int32_t *seq_lens, int32_t *query_start,
+                  int64_t *positions, int64_t *slot_mapping,
+                  int32_t *request_tables, int32_t *request_blocks,
+                  const int32_t *request_ids, const int32_t *context_lens,
+                  const int32_t *new_lens, const int32_t *free_blocks,
+                  int32_t *free_count, int32_t num_seqs, int32_t num_requests,
+                  int32_t max_blocks_per_seq, int32_t request_width,
+                  int64_t num_rows, int64_t free_capacity, int64_t num_blocks,
+                  int32_t block_size, void *stream);
+
+/*
+ * pa_trim_blocks -- blocks past a length go back to the free list: after rejected
+ * drafts (keep_lens = the accepted length) or when a request ends (0).  For each
+ * named request (request_ids as above) the blocks past ceil(keep_lens[s] / 16) are
+ * put behind the first free_count[0] entries of free_blocks so that the first
+ * sequence's first one is taken next -- a step built and trimmed to its context
+ * leaves the list as it was -- and request_blocks and free_count follow.  A bad id or
+ * length changes nothing of its request (PA_DEVERR_SEQ_LEN); if the blocks do not
+ * fit into free_capacity nothing changes at all (PA_DEVERR_BLOCK_ID).
+ */
+int pa_trim_blocks(const int32_t *request_tables, int32_t *request_blocks,
+                   const int32_t *request_ids, const int32_t *keep_lens,
+                   int32_t *free_blocks, int32_t *free_count, int32_t num_seqs,
+                   int32_t num_requests, int32_t request_width,
+                   int64_t free_capacity, int32_t block_size, void *stream);
+
+/*
+ * pa_process_logits -- logits made ready for sampling, or the target_probs of
+ * pa_verify_drafts.  Rows as there: sequence s owns rows query_start[s] ..
+ * query_start[s+1]-1 of logits ([num_rows][vocab_size] of `dtype`) and out (of `dtype`
+ * or PA_F32), rows contiguous with strides of any alignment.
+ *
+ * For token v of row i of sequence s, with x its logit, c the times v occurs in the
+ * output so far -- history[s][prompt_lens[s] .. history_lens[s]), which ends with the
+ * token of the sequence's first row, and tokens[query_start[s] + 1 .. + i], the drafts
+ * before the row's prediction -- and seen if c > 0 or v is among history[s][0 ..
+ * prompt_lens[s]):
+ *   x <- x / repetition[s] if x > 0, else x * repetition[s]        (seen only)
+ *   x <- x - frequency[s] * c - presence[s] * [c > 0]
+ *   x <- x + the values of every entry e of bias_start[s] .. bias_start[s+1]-1 with
+ *        bias_tokens[e] = v
+ *   x <- -inf if bit v % 32 of allowed[row][v / 32] is 0 (whatever x was)
+ *   x <- x / temperature[s] if that is above 0
+ * out receives x, or with probs != 0 softmax(x) over the row; with a temperature
+ * not above 0 then a 1 at the first largest x and 0 elsewhere.  A row that allows
+ * nothing is 0 throughout (-inf without probs); a NaN or an infinity of the largest
+ * x makes a row of probabilities NaN.  Arithmetic is fp32, rounded once at the end
+ * (divisions as products with the fp32 reciprocal).
+ *
+ * NULL for repetition, frequency, presence or temperature is 1, 0, 0 or 1; history,
+ * tokens, bias_start and allowed may be NULL (nothing there); prompt_lens NULL is 0.
+ * history is int32 [num_seqs][history_stride], bias_start int32 [num_seqs + 1] into
+ * num_bias entries, allowed int32 rows of allowed_stride words.  Token ids outside
+ * the vocabulary are left out, with PA_DEVERR_TOKEN; lengths or bias ranges out of
+ * bounds are clamped or left out, with PA_DEVERR_SEQ_LEN.  Rows of no sequence stay as
+ * they are.  out may be logits itself with the same type and stride, and may not
+ * overlap it otherwise.  vocab_size <= 2^30.
+ */
+int pa_process_logits(void *out, const void *logits, const int32_t *query_start,
+                      const int32_t *tokens, const int32_t *history,
+                      const int32_t *prompt_lens, const int32_t *history_lens,
+                      const float *repetition, const float *frequency,
+                      const float *presence, const int32_t *bias_start,
+                      const int32_t *bias_tokens, const float *bias_values,
+                      const int32_t *allowed, const float *temperature,
+                      int32_t num_seqs, int32_t num_rows, int32_t vocab_size,
+                      int64_t logits_row_stride, int64_t out_row_stride,
+                      int64_t history_stride, int64_t allowed_stride,
+                      int64_t num_bias, int32_t probs, int32_t dtype,
+                      int32_t out_dtype, void *stream);
+
+/*
  * pa_decode_cascade_workspace_size -- bytes of workspace pa_decode_cascade
  * needs for these sizes (fp32 partial results in the layout documented at
  * pa_decode_partitioned_workspace_size, with one partition per prefix chunk
@@ -623,7 +825,7 @@ int pa_device_error(uint32_t *flags, int clear);
  * pa_test_stall_next_decode -- test hook for the kernels' bounded waits.  The
  * next decode call (any pa_decode* entry point, from any host thread) makes
  * the first copy of every warp of its persistent kernel expect 16 bytes more
- * than it delivers -- in the long runs of pa_decode_multi_fp8, the first keys of
+ * than it delivers -- in the long runs of pa_decode_multi_fp8 and _fp4, the first keys of
  * every thread block never count as arrived -- so the wait for it runs out at its
  * 1 s limit: the kernel sets PA_DEVERR_TIMEOUT, waits (bounded) for its copies in
  * flight and returns, leaving that call's output incomplete (the call takes ~2 s).
@@ -633,9 +835,10 @@ int pa_test_stall_next_decode(void);
 
 /* ABI version of this header (increments when the signature or the meaning of a
  * declared function changes).  Additions raised it up to 4, and no longer do:
- * pa_rope_and_cache, pa_rope_and_cache_fp8, pa_decode_multi_fp8 and
- * pa_verify_drafts came to version 4, so a loader that may meet an older library
- * looks these four up by name. */
+ * pa_rope_and_cache, pa_rope_and_cache_fp8, pa_decode_multi_fp8,
+ * pa_verify_drafts, the *_fp4 functions, pa_build_step, pa_trim_blocks and
+ * pa_process_logits came to version 4, so a loader that may meet an older library
+ * looks these up by name. */
 int pa_abi_version(void);
 
 #ifdef __cplusplus

@@ -104,6 +104,9 @@ cudaError_t run_split(const pa::DecodeParams &p, int dtype, int D, int G, dim3 g
 #ifndef PA_F8_CLUSTER
 #define PA_F8_CLUSTER 4
 #endif
+#ifndef PA_F4_CLUSTER
+#define PA_F4_CLUSTER 4
+#endif
 
 cudaError_t run_persistent(const pa::DecodeParams &p, int dtype, int D, int G, bool partial,
                            long long unit_bound, cudaStream_t st) {
@@ -182,7 +185,7 @@ std::atomic<int> g_test_stall{0};
 // caches (kv_dtype: the caches' storage type).
 bool prepare_maps(pa::DecodeParams &p, int32_t kv_dtype, int32_t head_dim) {
     p.test_stall = g_test_stall.exchange(0, std::memory_order_acq_rel);
-    if (kv_dtype == PA_F32) return true;
+    if (kv_dtype == PA_F32 || kv_dtype == PA_E2M1) return true;   // plain bulk copies
     if (p.num_blocks <= 0) return true;            // nothing can be read
     if (!encode_cache_map(&p.tmap_k, p.k_cache, p.num_blocks, p.num_kv_heads, head_dim,
                           kv_dtype) ||
@@ -553,9 +556,10 @@ int pa_reshape_and_cache_fp8(const void *k, const void *v, void *k_cache, void *
 
 namespace {
 
-// Shared by the FP8 decode entry points: checks, parameters, launch of the
-// persistent kernel (and, for partitions, the merge).
-int decode_fp8_common(void *out, const void *q, const void *k_cache, const void *v_cache,
+// Shared by the FP8 and FP4 decode entry points (kv_dtype: the caches' storage
+// type): checks, parameters, launch of the persistent kernel (and, for partitions,
+// the merge).
+int decode_codes_common(int32_t kv_dtype, void *out, const void *q, const void *k_cache, const void *v_cache,
                       const float *k_scale, const float *v_scale,
                       const int32_t *block_tables, const int32_t *seq_lens, int32_t num_seqs,
                       int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -604,13 +608,18 @@ int decode_fp8_common(void *out, const void *q, const void *k_cache, const void 
         unit_bound *= P;
     }
     if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
-    if (!prepare_maps(p, PA_E4M3, head_dim)) return PA_ERR_CUDA;
+    if (!prepare_maps(p, kv_dtype, head_dim)) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = num_heads / num_kv_heads;
-    const int cluster = partial ? 1 : PA_F8_CLUSTER;
-    cudaError_t e = dtype == PA_BF16
-                        ? pa::decode_fp8_bf16(p, head_dim, G, partial, unit_bound, cluster, st)
-                        : pa::decode_fp8_f16(p, head_dim, G, partial, unit_bound, cluster, st);
+    const bool f4 = kv_dtype == PA_E2M1;
+    const int cluster = partial ? 1 : f4 ? PA_F4_CLUSTER : PA_F8_CLUSTER;
+    cudaError_t e;
+    if (f4)
+        e = dtype == PA_BF16 ? pa::decode_fp4_bf16(p, head_dim, G, partial, unit_bound, cluster, st)
+                             : pa::decode_fp4_f16(p, head_dim, G, partial, unit_bound, cluster, st);
+    else
+        e = dtype == PA_BF16 ? pa::decode_fp8_bf16(p, head_dim, G, partial, unit_bound, cluster, st)
+                             : pa::decode_fp8_f16(p, head_dim, G, partial, unit_bound, cluster, st);
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return PA_ERR_CUDA;
     if (!partial) return PA_OK;
@@ -637,7 +646,7 @@ int pa_decode_fp8(void *out, const void *q, const void *k_cache, const void *v_c
                   int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
                   int32_t block_size, int32_t max_blocks_per_seq, int64_t q_seq_stride,
                   float scale, int32_t dtype, void *stream) {
-    return decode_fp8_common(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+    return decode_codes_common(PA_E4M3, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                              seq_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
                              block_size, max_blocks_per_seq, q_seq_stride, scale, dtype,
                              false, 0, 0, nullptr, 0, stream);
@@ -652,7 +661,7 @@ int pa_decode_partitioned_fp8(void *out, const void *q, const void *k_cache,
                               int64_t q_seq_stride, float scale, int32_t dtype,
                               int32_t partition_size, int32_t max_seq_len, void *workspace,
                               size_t workspace_bytes, void *stream) {
-    return decode_fp8_common(out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+    return decode_codes_common(PA_E4M3, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                              seq_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
                              block_size, max_blocks_per_seq, q_seq_stride, scale, dtype, true,
                              partition_size, max_seq_len, workspace, workspace_bytes, stream);
@@ -662,8 +671,10 @@ int pa_decode_partitioned_fp8(void *out, const void *q, const void *k_cache,
 
 // ---- multi-token queries over E4M3 caches -----------------------------------
 
-extern "C" int pa_decode_multi_fp8(
-    void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+namespace {
+
+int decode_multi_codes(
+    int32_t kv_dtype, void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
     const float *v_scale, const int32_t *block_tables, const int32_t *seq_lens,
     const int32_t *query_start, int32_t num_seqs, int32_t num_q_rows, int32_t max_query_len,
     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
@@ -695,27 +706,265 @@ extern "C" int pa_decode_multi_fp8(
     p.scale_log2 = scale * pa::LOG2E;
     // as for 16-bit caches: runs of many (token, head) rows go to the tcgen05 kernel,
     // the others to the persistent kernel
+    const bool f4 = kv_dtype == PA_E2M1;
     const int min_rows = pa::prefill_f8_min_rows(num_seqs);
     const bool split = rows >= min_rows;
     const int64_t small_rows = split ? min_rows - 1 : rows;
     p.mq_split_rows = split ? min_rows : 0;
     if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
-    if (!prepare_maps(p, PA_E4M3, head_dim)) return PA_ERR_CUDA;
+    if (!prepare_maps(p, kv_dtype, head_dim)) return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (split) {
         const int groups = (int)((rows + pa::PREFILL_F8_ROWS - 1) / pa::PREFILL_F8_ROWS);
-        const cudaError_t e = dtype == PA_BF16 ? pa::prefill_f8_bf16(p, head_dim, G, groups, st)
-                                               : pa::prefill_f8_f16(p, head_dim, G, groups, st);
+        const cudaError_t e =
+            f4 ? (dtype == PA_BF16 ? pa::prefill_f4_bf16(p, head_dim, G, groups, st)
+                                   : pa::prefill_f4_f16(p, head_dim, G, groups, st))
+               : (dtype == PA_BF16 ? pa::prefill_f8_bf16(p, head_dim, G, groups, st)
+                                   : pa::prefill_f8_f16(p, head_dim, G, groups, st));
         if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
     const long long unit_bound = (long long)num_seqs * num_kv_heads * ((small_rows + 15) / 16);
-    const cudaError_t e = dtype == PA_BF16
-                        ? pa::decode_multi_fp8_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
-                        : pa::decode_multi_fp8_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st);
+    const cudaError_t e =
+        f4 ? (dtype == PA_BF16 ? pa::decode_multi_fp4_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
+                               : pa::decode_multi_fp4_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st))
+           : (dtype == PA_BF16 ? pa::decode_multi_fp8_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
+                               : pa::decode_multi_fp8_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st));
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
+
+}  // namespace
+
+extern "C" {
+
+int pa_decode_multi_fp8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                        const int32_t *seq_lens, const int32_t *query_start, int32_t num_seqs,
+                        int32_t num_q_rows, int32_t max_query_len, int32_t num_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                        int32_t block_size, int32_t max_blocks_per_seq, int64_t q_row_stride,
+                        float scale, int32_t dtype, void *stream) {
+    return decode_multi_codes(PA_E4M3, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                              seq_lens, query_start, num_seqs, num_q_rows, max_query_len, num_heads,
+                              num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq,
+                              q_row_stride, scale, dtype, stream);
+}
+
+// ---- FP4 (E2M1) KV cache ----------------------------------------------------
+
+int pa_decode_fp4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                  const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                  const int32_t *seq_lens, int32_t num_seqs, int32_t num_heads,
+                  int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                  int32_t block_size, int32_t max_blocks_per_seq, int64_t q_seq_stride,
+                  float scale, int32_t dtype, void *stream) {
+    return decode_codes_common(PA_E2M1, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                               seq_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                               block_size, max_blocks_per_seq, q_seq_stride, scale, dtype,
+                               false, 0, 0, nullptr, 0, stream);
+}
+
+int pa_decode_partitioned_fp4(void *out, const void *q, const void *k_cache,
+                              const void *v_cache, const float *k_scale,
+                              const float *v_scale, const int32_t *block_tables,
+                              const int32_t *seq_lens, int32_t num_seqs, int32_t num_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                              int32_t block_size, int32_t max_blocks_per_seq,
+                              int64_t q_seq_stride, float scale, int32_t dtype,
+                              int32_t partition_size, int32_t max_seq_len, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    return decode_codes_common(PA_E2M1, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                               seq_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                               block_size, max_blocks_per_seq, q_seq_stride, scale, dtype, true,
+                               partition_size, max_seq_len, workspace, workspace_bytes, stream);
+}
+
+int pa_decode_multi_fp4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                        const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                        const int32_t *seq_lens, const int32_t *query_start, int32_t num_seqs,
+                        int32_t num_q_rows, int32_t max_query_len, int32_t num_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                        int32_t block_size, int32_t max_blocks_per_seq, int64_t q_row_stride,
+                        float scale, int32_t dtype, void *stream) {
+    return decode_multi_codes(PA_E2M1, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                              seq_lens, query_start, num_seqs, num_q_rows, max_query_len, num_heads,
+                              num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq,
+                              q_row_stride, scale, dtype, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the write into E2M1 caches and the reading of their rows.
+int fp4_rows(pa::Fp4RowsParams &p, const void *k, const void *v, bool gather, int64_t num_blocks,
+             int32_t block_size, int32_t dtype, void *stream) {
+    if (p.num_tokens < 0 || p.num_kv_heads <= 0 || p.head_dim <= 0 || num_blocks < 0)
+        return PA_ERR_INVALID_ARG;
+    const int es = elem_size(dtype);
+    if (es == 0) return PA_ERR_UNSUPPORTED;
+    if (block_size != 16) return PA_ERR_UNSUPPORTED;
+    if (p.head_dim % 16 || p.head_dim > 1024 || p.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_blocks > (int64_t)INT32_MAX || p.num_tokens > (int64_t)INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (p.num_tokens == 0) return PA_OK;
+    if (!k || !v || !p.k_cache || !p.v_cache || !p.k_scale || !p.v_scale || !p.slot_mapping)
+        return PA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)p.num_kv_heads * p.head_dim;
+    if (p.k_stride < row || p.v_stride < row) return PA_ERR_INVALID_ARG;
+    // 16 elements per thread, in 16-byte accesses
+    if (!aligned16(k) || !aligned16(v) || (p.k_stride * es) % 16 || (p.v_stride * es) % 16 ||
+        !aligned16(p.k_cache) || !aligned16(p.v_cache))
+        return PA_ERR_INVALID_ARG;
+    p.num_slots = num_blocks * 16;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = gather ? pa::gather_cache_fp4(p, dtype, st) : pa::reshape_and_cache_fp4(p, dtype, st);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_reshape_and_cache_fp4(const void *k, const void *v, void *k_cache, void *v_cache,
+                             const float *k_scale, const float *v_scale,
+                             const int64_t *slot_mapping, int64_t num_tokens,
+                             int32_t num_kv_heads, int32_t head_dim, int64_t k_token_stride,
+                             int64_t v_token_stride, int64_t num_blocks, int32_t block_size,
+                             int32_t dtype, void *stream) {
+    pa::Fp4RowsParams p;
+    std::memset(&p, 0, sizeof p);
+    p.k = k; p.v = v; p.k_cache = k_cache; p.v_cache = v_cache;
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.slot_mapping = slot_mapping; p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads; p.head_dim = head_dim;
+    p.k_stride = k_token_stride; p.v_stride = v_token_stride;
+    return fp4_rows(p, k, v, false, num_blocks, block_size, dtype, stream);
+}
+
+int pa_gather_cache_fp4(void *k_out, void *v_out, const void *k_cache, const void *v_cache,
+                        const float *k_scale, const float *v_scale, const int64_t *slot_mapping,
+                        int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                        int64_t k_token_stride, int64_t v_token_stride, int64_t num_blocks,
+                        int32_t block_size, int32_t dtype, void *stream) {
+    pa::Fp4RowsParams p;
+    std::memset(&p, 0, sizeof p);
+    p.k_out = k_out; p.v_out = v_out;
+    p.k_cache = const_cast<void *>(k_cache); p.v_cache = const_cast<void *>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.slot_mapping = slot_mapping; p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads; p.head_dim = head_dim;
+    p.k_stride = k_token_stride; p.v_stride = v_token_stride;
+    return fp4_rows(p, k_out, v_out, true, num_blocks, block_size, dtype, stream);
+}
+
+// ---- maps of a step, built on the device ---------------------------------------
+
+int pa_build_step(int32_t *block_tables, int32_t *seq_lens, int32_t *query_start,
+                  int64_t *positions, int64_t *slot_mapping, int32_t *request_tables,
+                  int32_t *request_blocks, const int32_t *request_ids,
+                  const int32_t *context_lens, const int32_t *new_lens,
+                  const int32_t *free_blocks, int32_t *free_count, int32_t num_seqs,
+                  int32_t num_requests, int32_t max_blocks_per_seq, int32_t request_width,
+                  int64_t num_rows, int64_t free_capacity, int64_t num_blocks,
+                  int32_t block_size, void *stream) {
+    if (num_seqs < 0 || num_requests < 0 || max_blocks_per_seq < 0 || request_width < 0 ||
+        num_rows < 0 || free_capacity < 0 || num_blocks < 0)
+        return PA_ERR_INVALID_ARG;
+    if (block_size != 16) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || num_blocks > (int64_t)INT32_MAX || num_rows > (int64_t)INT32_MAX ||
+        free_capacity > (int64_t)INT32_MAX || max_blocks_per_seq > (1 << 26) || request_width > (1 << 26))
+        return PA_ERR_UNSUPPORTED;
+    if (!query_start || (num_rows > 0 && (!positions || !slot_mapping))) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!seq_lens || !context_lens || !request_blocks ||
+                         (!block_tables && max_blocks_per_seq > 0) || (!request_tables && request_width > 0)))
+        return PA_ERR_INVALID_ARG;
+    if ((free_blocks == nullptr) != (free_count == nullptr)) return PA_ERR_INVALID_ARG;
+    pa::StepParams p;
+    std::memset(&p, 0, sizeof p);
+    p.block_tables = block_tables; p.seq_lens = seq_lens; p.query_start = query_start;
+    p.positions = positions; p.slot_mapping = slot_mapping;
+    p.request_tables = request_tables; p.request_blocks = request_blocks;
+    p.request_ids = request_ids; p.context_lens = context_lens; p.new_lens = new_lens;
+    p.free_blocks = const_cast<int32_t *>(free_blocks); p.free_count = free_count;
+    p.num_blocks = num_blocks; p.num_rows = num_rows; p.free_capacity = free_blocks ? free_capacity : 0;
+    p.num_seqs = num_seqs; p.num_requests = num_requests;
+    p.max_blocks = max_blocks_per_seq; p.request_width = request_width;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    const cudaError_t e = pa::build_step(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+int pa_trim_blocks(const int32_t *request_tables, int32_t *request_blocks,
+                   const int32_t *request_ids, const int32_t *keep_lens, int32_t *free_blocks,
+                   int32_t *free_count, int32_t num_seqs, int32_t num_requests,
+                   int32_t request_width, int64_t free_capacity, int32_t block_size, void *stream) {
+    if (num_seqs < 0 || num_requests < 0 || request_width < 0 || free_capacity < 0)
+        return PA_ERR_INVALID_ARG;
+    if (block_size != 16) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || free_capacity > (int64_t)INT32_MAX || request_width > (1 << 26))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!request_blocks || !keep_lens || !free_blocks || !free_count ||
+        (!request_tables && request_width > 0))
+        return PA_ERR_INVALID_ARG;
+    pa::StepParams p;
+    std::memset(&p, 0, sizeof p);
+    p.request_tables = const_cast<int32_t *>(request_tables); p.request_blocks = request_blocks;
+    p.request_ids = request_ids; p.context_lens = keep_lens;
+    p.free_blocks = free_blocks; p.free_count = free_count; p.free_capacity = free_capacity;
+    p.num_seqs = num_seqs; p.num_requests = num_requests; p.request_width = request_width;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    const cudaError_t e = pa::trim_blocks(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ---- logits before sampling or verification --------------------------------------
+
+int pa_process_logits(void *out, const void *logits, const int32_t *query_start,
+                      const int32_t *tokens, const int32_t *history, const int32_t *prompt_lens,
+                      const int32_t *history_lens, const float *repetition,
+                      const float *frequency, const float *presence, const int32_t *bias_start,
+                      const int32_t *bias_tokens, const float *bias_values,
+                      const int32_t *allowed, const float *temperature, int32_t num_seqs,
+                      int32_t num_rows, int32_t vocab_size, int64_t logits_row_stride,
+                      int64_t out_row_stride, int64_t history_stride, int64_t allowed_stride,
+                      int64_t num_bias, int32_t probs, int32_t dtype, int32_t out_dtype,
+                      void *stream) {
+    if (num_seqs < 0 || num_rows < 0 || vocab_size <= 0 || history_stride < 0 || num_bias < 0)
+        return PA_ERR_INVALID_ARG;
+    const int es = elem_size(dtype), os = elem_size(out_dtype);
+    if (es == 0 || os == 0 || (out_dtype != dtype && out_dtype != PA_F32)) return PA_ERR_UNSUPPORTED;
+    if (vocab_size > (1 << 30) || num_bias > (int64_t)INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_rows == 0) return PA_OK;
+    if (!out || !logits || !query_start) return PA_ERR_INVALID_ARG;
+    if (history && (!history_lens || history_stride > (int64_t)INT32_MAX)) return PA_ERR_INVALID_ARG;
+    if (bias_start && num_bias > 0 && (!bias_tokens || !bias_values)) return PA_ERR_INVALID_ARG;
+    if (logits_row_stride < vocab_size || out_row_stride < vocab_size) return PA_ERR_INVALID_ARG;
+    if (allowed && allowed_stride < ((int64_t)vocab_size + 31) / 32) return PA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) % es || reinterpret_cast<uintptr_t>(out) % os)
+        return PA_ERR_INVALID_ARG;
+    if (out == logits && (out_dtype != dtype || (num_rows > 1 && out_row_stride != logits_row_stride)))
+        return PA_ERR_INVALID_ARG;                 // in place, an element goes where it was read
+    pa::LogitsParams p;
+    std::memset(&p, 0, sizeof p);
+    p.out = out; p.logits = logits; p.query_start = query_start; p.tokens = tokens;
+    p.history = history; p.prompt_lens = prompt_lens; p.history_lens = history_lens;
+    p.repetition = repetition; p.frequency = frequency; p.presence = presence;
+    p.bias_start = num_bias > 0 ? bias_start : nullptr;
+    p.bias_tokens = bias_tokens; p.bias_values = bias_values;
+    p.allowed = reinterpret_cast<const uint32_t *>(allowed); p.temperature = temperature;
+    p.logits_stride = logits_row_stride; p.out_stride = out_row_stride;
+    p.history_stride = history_stride; p.allowed_stride = allowed_stride; p.num_bias = num_bias;
+    p.num_seqs = num_seqs; p.num_rows = num_rows; p.vocab = vocab_size; p.probs = probs != 0;
+    if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
+    const cudaError_t e = pa::process_logits(p, dtype, out_dtype, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
 
 // ---- the cache write with norms and rotation ---------------------------------
 

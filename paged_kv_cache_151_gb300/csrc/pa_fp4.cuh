@@ -1,0 +1,367 @@
+// pa_fp4.cuh -- 4-bit (E2M1) KV cache: conversions and the per-warp attention
+// arithmetic over its tiles.
+//
+// A tile holds the 16 rows of one (block, KV head): the codes of the rows, D/2
+// bytes each (element 2i in the low half of byte i), then the rows' scales, D/16
+// bytes each: one E4M3 number for every 16 neighbouring elements.  With the head's
+// float scale_j an element stands for E2M1(code) * E4M3(scale) * scale_j.  A tile is
+// 9 D contiguous bytes, so one bulk copy fetches it.
+//
+// The first product is exact in f16 (an E2M1 value has two significant bits, an
+// E4M3 one four; 2^-10 <= product <= 2688), so the tiles are dequantised to f16 in
+// registers and both contractions run on the f16 tensor cores with fp32
+// accumulation; scale_j folds into the score scale (keys) and the normalisation
+// (values).  q is rounded to f16 once, P as it is used.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_decode.cuh"
+#include "pa_fp8.cuh"
+#include "pa_mma.cuh"
+
+namespace pa {
+
+struct e2m1 {                              // the cache's storage type, as a tag
+    unsigned char byte;
+};
+
+// Bytes of one tile: 16 rows of D elements of KV.
+template <typename KV, int D>
+__host__ __device__ constexpr int tile_bytes() {
+    return std::is_same<KV, e2m1>::value ? 9 * D : 16 * D * (int)sizeof(KV);
+}
+
+// The eight E2M1 codes of w as f16 pairs, byte i in r[i] (low half: low code).
+__device__ __forceinline__ void f16x2_from_e2m1x8(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+
+// Two binary32 values to E2M1 codes (nearest, ties to even, saturating at 6): lo in
+// bits 0-3, hi in bits 4-7.
+__device__ __forceinline__ uint32_t e2m1x2_from_f32(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.u32.u8 %0, a;\n\t}"
+        : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A transposed 8 x 8 matrix of 16-bit elements: lane (g, t) gives row g, columns 2t
+// and 2t + 1, and gets rows 2t and 2t + 1 of column g.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// Token of row r (0..7) of a score tile.  Every group of rows that one load
+// instruction serves falls on distinct banks (or on two, for 8-byte loads of 64-byte
+// rows): 0 and 1, 2 and 3, .. differ in parity; 0-3, 4-7, the even and the odd rows
+// are all four residues of 4.
+__device__ __forceinline__ int fp4_token(int r) { return r ^ ((r >> 2) & 1); }
+
+// Attention of one warp over E2M1 tiles, for NT tiles of eight query rows that share
+// a KV head: the G heads of one token (NT = 1), or 16 (token, head) pairs of a
+// multi-token query (NT = 2) with a causal limit each.
+//
+// Both contractions have the tokens or head_dim on the 16-row side and the query
+// rows on the 8-column side, so no half of a matrix instruction is padding:
+//   S^T[token][row] = K Q^T    A: K as lane (g, t) holds it, rows fp4_token(g) and
+//       8 more, D/4 neighbouring elements from (D/4) t (two groups at D = 128); the
+//       order of elements in the product is free, q follows it
+//   O^T[d][row] += V^T P^T     B: P^T, the transposed scores (two movmatrix a
+//       tile); A: V^T, lane (g, t): elements (D/8) g .. of the tokens of rows 2t,
+//       2t + 1, 8 + 2t and 9 + 2t
+// Lane (g, t) holds rows 2t and 2t + 1 of each tile throughout (scores, statistics
+// and outputs), so nothing is exchanged when a row is rescaled.
+//
+// A row's reference level moves only when a score exceeds it by more than
+// F8_TOP_LOG2, as in WarpAttnF8x16; (m, l, acc) are to that level.
+template <typename T, int D, int NT>
+struct WarpAttnF4 {
+    static_assert(sizeof(T) == 2, "q and out are 16-bit");
+    static_assert(D == 64 || D == 128, "head_dim");
+    static constexpr int KS = D / 16;      // k-steps of the score product
+    static constexpr int MT = D / 16;      // 16-row tiles of the value product
+    static constexpr int DL = D / 8;       // elements of a lane in it
+    static constexpr int ROWB = D / 2, OFF_SC = 16 * ROWB, SCB = D / 16;
+
+    int lane, g, t;
+    uint32_t qb[NT][KS][2];                // f16 B fragments
+    // acc[n][mt]: elements DL g + 2mt (0, 1) and + 1 (2, 3) of rows 2t and 2t + 1
+    float acc[NT][MT][4];
+    float m_run[NT][2], l_run[NT][2];      // level; this lane's part of the sum
+    int lim[NT][2];                        // last visible position, -1: no such row (multi-token queries)
+
+    __device__ __forceinline__ void init(int lane_) {
+        lane = lane_;
+        g = lane >> 2;
+        t = lane & 3;
+        reset();
+    }
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m_run[n][0] = m_run[n][1] = -INFINITY;
+            l_run[n][0] = l_run[n][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.f;
+        }
+    }
+
+    // query row g of tile n (nullptr: no such row)
+    __device__ __forceinline__ void load_row(int n, const T *q) {
+        constexpr int W = D / 32;          // 16-byte words of a lane
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const uint4 x = q ? *reinterpret_cast<const uint4 *>(q + (D / 4) * t + 8 * i)
+                              : make_uint4(0, 0, 0, 0);
+            qb[n][2 * i][0] = WarpAttnF8<T, D, 1>::to_f16x2(x.x);
+            qb[n][2 * i][1] = WarpAttnF8<T, D, 1>::to_f16x2(x.y);
+            qb[n][2 * i + 1][0] = WarpAttnF8<T, D, 1>::to_f16x2(x.z);
+            qb[n][2 * i + 1][1] = WarpAttnF8<T, D, 1>::to_f16x2(x.w);
+        }
+    }
+
+    // Scores of a block's 16 tokens: v[n][0], [1]: token fp4_token(g) of rows 2t,
+    // 2t + 1; [2], [3]: 8 tokens on.
+    __device__ __forceinline__ void scores(uint32_t kt, float (&v)[NT][4]) const {
+        const int r0 = fp4_token(g);
+        constexpr int W = D / 32;          // 32-bit words of codes of a row
+        uint32_t w0[W], w1[W], s0, s1;
+        if constexpr (D == 128) {
+            const uint4 a = lds128(kt + r0 * ROWB + 16 * t), b = lds128(kt + (r0 + 8) * ROWB + 16 * t);
+            w0[0] = a.x; w0[1] = a.y; w0[2] = a.z; w0[3] = a.w;
+            w1[0] = b.x; w1[1] = b.y; w1[2] = b.z; w1[3] = b.w;
+            s0 = f16x2_from_e4m3x2(lds16(kt + OFF_SC + r0 * SCB + 2 * t));
+            s1 = f16x2_from_e4m3x2(lds16(kt + OFF_SC + (r0 + 8) * SCB + 2 * t));
+        } else {
+            const uint2 a = lds64(kt + r0 * ROWB + 8 * t), b = lds64(kt + (r0 + 8) * ROWB + 8 * t);
+            w0[0] = a.x; w0[1] = a.y;
+            w1[0] = b.x; w1[1] = b.y;
+            s0 = f16x2_from_e4m3x2(lds8(kt + OFF_SC + r0 * SCB + t));
+            s1 = f16x2_from_e4m3x2(lds8(kt + OFF_SC + (r0 + 8) * SCB + t));
+        }
+        // two chains of matrix products a tile
+        float c[NT][2][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[n][0][e] = c[n][1][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            // the low group's scale for the first half of the run, then the high one's
+            const uint32_t sel = D == 128 && i >= W / 2 ? 0x3232 : 0x1010;
+            const uint32_t x0 = prmt(s0, s0, sel), x1 = prmt(s1, s1, sel);
+            uint32_t a[4], b[4];
+            f16x2_from_e2m1x8(w0[i], a);
+            f16x2_from_e2m1x8(w1[i], b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[e] = mul_f16x2(a[e], x0);
+                b[e] = mul_f16x2(b[e], x1);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_f16(c[n][0], a[0], b[0], a[1], b[1], qb[n][2 * i][0], qb[n][2 * i][1]);
+                mma_f16(c[n][1], a[2], b[2], a[3], b[3], qb[n][2 * i + 1][0], qb[n][2 * i + 1][1]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[n][e] = c[n][0][e] + c[n][1][e];
+    }
+
+    // One block.  rows: tokens of it inside the sequence (1..16); pos0: the first
+    // one's position (multi-token queries).  scale_log2 carries K's head scale.
+    template <bool CAUSAL>
+    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int rows, int pos0, float scale_log2) {
+        float sc[NT][4];
+        scores(kt, sc);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[n][e] *= scale_log2;
+        const int tok = fp4_token(g);
+        if constexpr (CAUSAL) {
+            bool cut = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cut = cut || pos0 + 15 > min(lim[n][0], lim[n][1]);
+            if (__any_sync(0xffffffffu, cut)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[n][e] = pos0 + tok + 8 * (e >> 1) <= lim[n][e & 1] ? sc[n][e] : -INFINITY;
+            }
+        } else if (rows < 16) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = tok + 8 * (e >> 1) < rows ? sc[n][e] : -INFINITY;
+        }
+        bool above = false;
+        float mx[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[n][h] = fmaxf(sc[n][h], sc[n][2 + h]);
+                above = above || mx[n][h] > m_run[n][h] + F8_TOP_LOG2;
+            }
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float m = mx[n][h];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const float m_new = m > m_run[n][h] + F8_TOP_LOG2 ? m - F8_BELOW_LOG2 : m_run[n][h];
+                    const float alpha = m_new == m_run[n][h] ? 1.f : ex2(m_run[n][h] - m_new);
+                    m_run[n][h] = m_new;
+                    l_run[n][h] *= alpha;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[n][mt][h] *= alpha;
+                        acc[n][mt][2 + h] *= alpha;
+                    }
+                }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float a = m_run[n][0] == -INFINITY ? 0.f : m_run[n][0];   // a row that sees nothing yet
+            const float b = m_run[n][1] == -INFINITY ? 0.f : m_run[n][1];
+            const uint32_t p0 = Mma<__half>::pack(ex2(sc[n][0] - a), ex2(sc[n][1] - b));
+            const uint32_t p1 = Mma<__half>::pack(ex2(sc[n][2] - a), ex2(sc[n][3] - b));
+            add_halves(l_run[n][0], l_run[n][1], p0);      // the weights as they are used
+            add_halves(l_run[n][0], l_run[n][1], p1);
+            pb[n][0] = transpose8(p0);
+            pb[n][1] = transpose8(p1);
+        }
+        values(vt, rows, pb);
+    }
+
+    __device__ __forceinline__ void values(uint32_t vt, int rows, const uint32_t (&pb)[NT][2]) {
+        const int tok[4] = {fp4_token(2 * t), fp4_token(2 * t + 1), 8 + fp4_token(2 * t), 8 + fp4_token(2 * t + 1)};
+        constexpr int W = D / 64;          // 32-bit words of codes of a token
+        uint32_t w[4][W], s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+                const uint2 v = lds64(vt + tok[i] * ROWB + 8 * g);
+                w[i][0] = v.x; w[i][1] = v.y;
+                s[i] = lds8(vt + OFF_SC + tok[i] * SCB + g);
+            } else {
+                w[i][0] = lds32(vt + tok[i] * ROWB + 4 * g);
+                s[i] = lds8(vt + OFF_SC + tok[i] * SCB + (g >> 1));
+            }
+        }
+        // rows past the sequence hold anything; their weight is 0, so what must not
+        // stay is a scale that is NaN
+        if (rows < 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = tok[i] < rows ? s[i] : 0u;
+        }
+        const uint32_t x01 = f16x2_from_e4m3x2(s[0] | (s[1] << 8)), x23 = f16x2_from_e4m3x2(s[2] | (s[3] << 8));
+        constexpr uint32_t LO = 0x0f0f0f0fu;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            // byte e: the codes of two tokens, element 2 (4i + e) (even) and the one after
+            uint32_t ea[4], oa[4], eb[4], ob[4];
+            f16x2_from_e2m1x8((w[0][i] & LO) | ((w[1][i] << 4) & ~LO), ea);
+            f16x2_from_e2m1x8(((w[0][i] >> 4) & LO) | (w[1][i] & ~LO), oa);
+            f16x2_from_e2m1x8((w[2][i] & LO) | ((w[3][i] << 4) & ~LO), eb);
+            f16x2_from_e2m1x8(((w[2][i] >> 4) & LO) | (w[3][i] & ~LO), ob);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a0 = mul_f16x2(ea[e], x01), a1 = mul_f16x2(oa[e], x01);
+                const uint32_t a2 = mul_f16x2(eb[e], x23), a3 = mul_f16x2(ob[e], x23);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(acc[n][4 * i + e], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            }
+        }
+    }
+
+    // Sum the lanes of each row.
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+            {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l_run[n][h] += __shfl_xor_sync(0xffffffffu, l_run[n][h], o);
+                // only NaN seen: a level that a merge does not take for an empty partial
+                if (m_run[n][h] == -INFINITY && l_run[n][h] != 0.f) m_run[n][h] = 0.f;
+            }
+    }
+
+    // merge slot: Mw, Lw [rows], Aw [rows][D]; rows: 8 n + 2t + h below `rows`
+    __device__ __forceinline__ void store_partial(float *Mw, float *Lw, float *Aw, int rows) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 8 * n + 2 * t + h;
+                if (r >= rows) continue;
+                if (g == 0) {
+                    Mw[r] = m_run[n][h];
+                    Lw[r] = l_run[n][h];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    *reinterpret_cast<float2 *>(Aw + r * D + DL * g + 2 * mt) =
+                        make_float2(acc[n][mt][h], acc[n][mt][2 + h]);
+            }
+    }
+
+    // After finish(): f(row, d, v0, v1, first, m, l) for the normalised outputs at d,
+    // d + 1 of the rows below `rows` that exist.
+    template <typename Fn>
+    __device__ __forceinline__ void for_each_result(int rows, Fn &&f) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 8 * n + 2 * t + h;
+                if (r >= rows || (NT > 1 && lim[n][h] < 0)) continue;
+                const float l = l_run[n][h], inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    f(r, DL * g + 2 * mt, acc[n][mt][h] * inv, acc[n][mt][2 + h] * inv, g == 0 && mt == 0,
+                      m_run[n][h], l);
+            }
+    }
+};
+
+}  // namespace pa

@@ -96,6 +96,53 @@ struct RopeParams {
 };
 cudaError_t rope_and_cache(const RopeParams &p, int dtype, cudaStream_t st);
 
+// rows written into E2M1 caches, or read back (pa_fp4.cu); strides in elements, of
+// k and v or of k_out and v_out
+struct Fp4RowsParams {
+    const void *k, *v;
+    void *k_out, *v_out;
+    void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;           // [num_kv_heads]
+    const int64_t *slot_mapping;              // [num_tokens]
+    int64_t num_tokens, num_slots, k_stride, v_stride;
+    int num_kv_heads, head_dim;
+    unsigned int *err;
+};
+cudaError_t reshape_and_cache_fp4(const Fp4RowsParams &p, int dtype, cudaStream_t st);
+cudaError_t gather_cache_fp4(const Fp4RowsParams &p, int dtype, cudaStream_t st);
+
+// block tables and maps of a step, and blocks given back (pa_step.cu)
+struct StepParams {
+    int32_t *block_tables, *seq_lens, *query_start;   // [num_seqs][max_blocks], [num_seqs], [num_seqs + 1]
+    int64_t *positions, *slot_mapping;        // [num_rows]
+    int32_t *request_tables, *request_blocks; // [num_requests][request_width], [num_requests]
+    const int32_t *request_ids;               // [num_seqs], or nullptr: s
+    const int32_t *context_lens, *new_lens;   // [num_seqs]; new_lens nullptr: one each
+    int32_t *free_blocks, *free_count;        // [free_capacity], [1]; nullptr: nothing to take
+    int64_t num_blocks, num_rows, free_capacity;
+    int num_seqs, num_requests, max_blocks, request_width;
+    unsigned int *err;
+};
+cudaError_t build_step(const StepParams &p, cudaStream_t st);
+cudaError_t trim_blocks(const StepParams &p, cudaStream_t st);
+
+// logits made ready for sampling or verification (pa_logits.cu); strides in elements
+struct LogitsParams {
+    void *out;
+    const void *logits;
+    const int32_t *query_start, *tokens;      // [num_seqs + 1], [num_rows] or nullptr
+    const int32_t *history, *prompt_lens, *history_lens;
+    const float *repetition, *frequency, *presence;   // [num_seqs], nullptr: neutral
+    const int32_t *bias_start, *bias_tokens;  // [num_seqs + 1], [num_bias]
+    const float *bias_values;
+    const uint32_t *allowed;                  // [num_rows] rows of bits, or nullptr
+    const float *temperature;                 // [num_seqs], nullptr: 1
+    int64_t logits_stride, out_stride, history_stride, allowed_stride, num_bias;
+    int num_seqs, num_rows, vocab, probs;
+    unsigned int *err;
+};
+cudaError_t process_logits(const LogitsParams &p, int dtype, int out_dtype, cudaStream_t st);
+
 // verification of drafted tokens (pa_verify.cu); strides in elements
 struct VerifyParams {
     int32_t *out_tokens, *num_accepted;       // [num_seqs][max_query_len], [num_seqs]
@@ -132,6 +179,18 @@ cudaError_t decode_fp8_bf16(const DecodeParams &p, int D, int G, bool partial,
                             long long unit_bound, int cluster, cudaStream_t st);
 cudaError_t decode_fp8_f16(const DecodeParams &p, int D, int G, bool partial,
                            long long unit_bound, int cluster, cudaStream_t st);
+
+// the same over E2M1 caches with a scale for every 16 elements (pa_fp4.cuh)
+cudaError_t decode_fp4_bf16(const DecodeParams &p, int D, int G, bool partial,
+                            long long unit_bound, int cluster, cudaStream_t st);
+cudaError_t decode_fp4_f16(const DecodeParams &p, int D, int G, bool partial,
+                           long long unit_bound, int cluster, cudaStream_t st);
+cudaError_t decode_multi_fp4_bf16(const DecodeParams &p, int D, int G, long long unit_bound,
+                                  int cluster, cudaStream_t st);
+cudaError_t decode_multi_fp4_f16(const DecodeParams &p, int D, int G, long long unit_bound,
+                                 int cluster, cudaStream_t st);
+cudaError_t prefill_f4_bf16(const DecodeParams &p, int D, int G, int groups, cudaStream_t st);
+cudaError_t prefill_f4_f16(const DecodeParams &p, int D, int G, int groups, cudaStream_t st);
 
 // block copies for copy-on-write: every (src, dst) pair of `mapping`, in every cache
 constexpr int COPY_MAX_CACHES = 256;

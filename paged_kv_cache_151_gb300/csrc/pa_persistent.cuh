@@ -41,6 +41,7 @@
 
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
+#include "pa_fp4.cuh"
 #include "pa_fp8.cuh"
 #include "pa_math.cuh"
 #include "pa_mma.cuh"
@@ -60,12 +61,13 @@ struct UnitRec {
     int q0, nq;                   // multi: first query row of the sequence, its count
 };
 
-// Shared-memory layout; KV is the cache's storage type (T itself, or E4M3).
+// Shared-memory layout; KV is the cache's storage type (T itself, E4M3, or E2M1
+// with its groups' scales).
 template <typename T, typename KV, int D, int G, int NW, int S, int MODE>
 struct PersistentLayout {
     static constexpr bool PARTIAL = MODE == MODE_PARTITIONED;
     static constexpr int ROWS = rows_of_mode(MODE, G);
-    static constexpr size_t TILE_BYTES = (size_t)16 * D * sizeof(KV);
+    static constexpr size_t TILE_BYTES = tile_bytes<KV, D>();
     static constexpr int NU_MAX = 128;                    // units per cluster
     static constexpr size_t STAGES = (size_t)NW * S * 2 * TILE_BYTES;
     // one partial: O[ROWS][D], M[ROWS], L[ROWS], padded to 16 bytes
@@ -83,7 +85,8 @@ struct PersistentLayout {
     // to 16 blocks)
     static constexpr size_t CTL_BYTES = ((size_t)(3 * NW + 16 * NW + 1) * 4 + 15) / 16 * 16;
     static constexpr size_t BYTES = OFF_CTL + CTL_BYTES + 1024;   // + alignment of the base
-    static_assert(STAGES % 1024 == 0, "stage buffers: 1024-byte aligned boxes");
+    static_assert(STAGES % 1024 == 0 || std::is_same<KV, e2m1>::value,
+                  "stage buffers: 1024-byte aligned boxes");
     static_assert(S == 0 || (size_t)S * 2 * TILE_BYTES >= PART_FLOATS * 4,
                   "a warp's stages must hold one partial");
     static_assert(OFF_SCR % 16 == 0 && OFF_PARTS % 16 == 0 && OFF_UNITS % 16 == 0 &&
@@ -279,6 +282,12 @@ __host__ __device__ constexpr bool use_tc() { return sizeof(T) == 2; }
 #ifndef PA_F8_BLOCKS_PER_SM
 #define PA_F8_BLOCKS_PER_SM 3
 #endif
+#ifndef PA_F4_BLOCKS_PER_SM
+#define PA_F4_BLOCKS_PER_SM 4
+#endif
+#ifndef PA_F4_MULTI_BLOCKS_PER_SM
+#define PA_F4_MULTI_BLOCKS_PER_SM 3
+#endif
 
 // What a warp pays to enter a unit (load its query, park or write its
 // result), in quarters of one 16-token block; used to split the stream.
@@ -306,6 +315,7 @@ __host__ __device__ constexpr int persistent_warps() {
 // either way).
 template <typename KV, int NW, int MODE>
 __host__ __device__ constexpr int persistent_blocks_per_sm() {
+    if (std::is_same<KV, e2m1>::value) return MODE == MODE_MULTI ? PA_F4_MULTI_BLOCKS_PER_SM : PA_F4_BLOCKS_PER_SM;
     return sizeof(KV) == 1 ? (MODE == MODE_MULTI ? 2 : PA_F8_BLOCKS_PER_SM) : (NW >= 8 ? 1 : 2);
 }
 
@@ -314,6 +324,8 @@ __global__ void __launch_bounds__(NW * 32, (persistent_blocks_per_sm<KV, NW, MOD
 decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     constexpr bool TC = use_tc<T>();
     constexpr bool F8 = std::is_same<KV, e4m3>::value;
+    constexpr bool F4 = std::is_same<KV, e2m1>::value;
+    constexpr bool SCALED = F8 || F4;              // codes with a scale for each KV head
     constexpr bool PARTIAL = MODE == MODE_PARTITIONED;
     constexpr bool MQ = MODE == MODE_MULTI;
     constexpr int ROWS = rows_of_mode(MODE, G);
@@ -322,19 +334,20 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     // of the cluster merge it together instead, a row each, once all are done: one
     // warp would read 16 partials of 16 rows through distributed shared memory,
     // some 25 us of a batch of one.
-    constexpr bool SPREAD = F8 && MQ;
+    constexpr bool SPREAD = SCALED && MQ;
     constexpr int SPREAD_PARTS = 4;
     static_assert(!MQ || TC, "multi-token queries use the tensor-core path");
-    static_assert(F8 || std::is_same<KV, T>::value, "cache type");
-    static_assert(!F8 || TC, "E4M3 caches: 16-bit q");
+    static_assert(SCALED || std::is_same<KV, T>::value, "cache type");
+    static_assert(!SCALED || TC, "E4M3 and E2M1 caches: 16-bit q");
     using W = std::conditional_t<
+        F4, WarpAttnF4<T, D, MQ ? 2 : 1>, std::conditional_t<
         F8, std::conditional_t<MQ, WarpAttnF8x16<T, D>, WarpAttnF8<T, D, G>>,
         std::conditional_t<MQ, WarpAttnTC16<T, D>,
-                           std::conditional_t<TC, WarpAttnTC<T, D, G>, WarpAttn<T, D, G>>>>;
+                           std::conditional_t<TC, WarpAttnTC<T, D, G>, WarpAttn<T, D, G>>>>>;
     using Lay = PersistentLayout<T, KV, D, G, NW, S, MODE>;
     using Sh = Shape<T, D>;                        // chunks of q / out
     constexpr int E = Sh::E;
-    constexpr int ROWB = D * (int)sizeof(KV), TILE = 16 * ROWB;   // cache rows and tiles
+    constexpr int ROWB = D * (int)sizeof(KV), TILE = tile_bytes<KV, D>();   // cache rows (not E2M1's) and tiles
     constexpr int NT = NW * 32;
     constexpr int NU_MAX = Lay::NU_MAX;
     constexpr int WS = warp_scratch_floats<G>();
@@ -389,7 +402,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
 
     // ---- 0. barriers, and the first reads after the set-up started early -----
     if (tid == 0) {
-        if constexpr (TC) {                        // fetch the descriptors early
+        if constexpr (TC && !F4) {                 // fetch the descriptors early
             prefetch_tensormap(&p.tmap_k);
             prefetch_tensormap(&p.tmap_v);
             if constexpr (!F8) {
@@ -658,7 +671,13 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
             return;
         }
         unsigned char *dst = my_stages + (size_t)(k % S) * 2 * TILE;
-        if constexpr (F8) {
+        if constexpr (F4) {
+            // whole tiles, codes and scales in one run each
+            const size_t off = ((size_t)pbk * Hkv + units[ui].j) * TILE;
+            mbar_arrive_expect_tx(bar, 2 * TILE + extra);
+            bulk_g2s(dst, kbase + off, TILE, bar, pol);
+            bulk_g2s(dst + TILE, vbase + off, TILE, bar, pol);
+        } else if constexpr (F8) {
             // whole 16-row tiles, one box of 16 rows x D bytes each
             const int z = pbk * Hkv + units[ui].j;
             mbar_arrive_expect_tx(bar, 2 * TILE + extra);
@@ -735,7 +754,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
 
     // V's dequantisation scale of unit u (E4M3 caches), applied to results
     auto v_scale_of = [&](const UnitRec &u) -> float {
-        if constexpr (F8) return __ldg(p.v_scale + u.j);
+        if constexpr (SCALED) return __ldg(p.v_scale + u.j);
         else return 1.f;
     };
 
@@ -877,8 +896,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         if (!from_before && !to_after) {
             // a unit only this warp touched: write its result from registers
             const float vsc = v_scale_of(u);
-            wa.for_each_result([&](int g, int d, float v0, float v1, bool first, float m,
-                                   float l) {
+            auto write = [&](int g, int d, float v0, float v1, bool first, float m, float l) {
                 v0 *= vsc;
                 v1 *= vsc;
                 if constexpr (PARTIAL) {
@@ -893,11 +911,14 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                     T *o = reinterpret_cast<T *>(p.out) + out_row(u, g) * D + d;
                     store_pair<T>(o, v0, v1);
                 }
-            });
+            };
+            if constexpr (F4) wa.for_each_result(ROWS, write);
+            else wa.for_each_result(write);
         } else {
             float *mine = part_of(gw, (from_before && !to_after) ? 0 : 1);
             // partial layout: O[ROWS][D], M[ROWS], L[ROWS]
-            wa.store_partial(mine + ROWS * D, mine + ROWS * D + ROWS, mine);
+            if constexpr (F4) wa.store_partial(mine + ROWS * D, mine + ROWS * D + ROWS, mine, ROWS);
+            else wa.store_partial(mine + ROWS * D, mine + ROWS * D + ROWS, mine);
             shared_unit = ui;
         }
         __syncwarp();
@@ -951,7 +972,25 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         if (ui != cur) {
             if (cur >= 0) leave_unit(cur, false);
             cur = ui;
-            if constexpr (MQ) {
+            if constexpr (F4) {
+                const UnitRec &u = units[ui];
+                if constexpr (MQ) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        wa.load_row(n, q_row(u, 16 * u.part + 8 * n + (lane >> 2)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = 16 * u.part + 8 * n + 2 * (lane & 3) + h;
+                            wa.lim[n][h] = r < u.nq * G ? u.L - u.nq + r / G : -1;
+                        }
+                    }
+                } else {
+                    const T *qs = reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
+                                  (long long)u.j * G * D;
+                    wa.load_row(0, (lane >> 2) < G ? qs + (lane >> 2) * D : nullptr);
+                }
+                unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
+            } else if constexpr (MQ) {
                 const UnitRec &u = units[ui];
                 const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
                 wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
@@ -984,7 +1023,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
             if constexpr (TC) {
                 // tail rows hold other tokens' data: the one-token block math
                 // drops them in registers; the others clear them in the tile
-                if (F8 || MQ) {
+                if (F8 || (MQ && !F4)) {
                     if (rows < 16) {
                         if constexpr (F8) W::zero_rows(Kt + TILE, rows, lane);
                         else WarpAttnTC<T, D, G>::zero_rows(Kt + TILE, rows, lane);
@@ -994,7 +1033,8 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                         __syncwarp();
                     }
                 }
-                if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
+                if constexpr (F4) wa.template block<MQ>(smem_u32(Kt), smem_u32(Kt + TILE), rows, pos_of(k, ui), unit_scale);
+                else if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
                 else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
             } else {
                 wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
@@ -1103,11 +1143,11 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
 #endif
 template <typename T, typename KV, int D, int G, int MODE, int NW>
 __host__ __device__ constexpr int persistent_stages() {
-    int s = PA_STAGE_KB * 1024 / (int)(2 * 16 * D * sizeof(KV));
+    int s = PA_STAGE_KB * 1024 / (2 * tile_bytes<KV, D>());
     s = s < 2 ? 2 : (s > 6 ? 6 : s);
     const size_t cap = (size_t)(227 / persistent_blocks_per_sm<KV, NW, MODE>()) * 1024;
     while (s > 2 && PersistentLayout<T, KV, D, G, NW, 0, MODE>::BYTES +
-                            (size_t)NW * s * (2 * 16 * D * sizeof(KV) + 8) > cap)
+                            (size_t)NW * s * (2 * tile_bytes<KV, D>() + 8) > cap)
         --s;
     return s;
 }

@@ -63,6 +63,7 @@
 
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
+#include "pa_fp4.cuh"
 #include "pa_fp8.cuh"
 #include "pa_internal.h"
 #include "pa_mma.cuh"
@@ -134,12 +135,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 
-template <typename T, int D, int G, int C>
+template <typename T, typename KV, int D, int G, int C>
 __global__ void __launch_bounds__(PF8_THREADS, 1)
 prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
     static_assert(sizeof(T) == 2 && (D == 64 || D == 128), "16-bit q and out, head_dim 64 or 128");
     static_assert(128 % G == 0, "a tile holds whole tokens");
     static_assert(C == 1 || C == 2 || C == 4, "blocks that share an item");
+    constexpr bool F4 = std::is_same<KV, e2m1>::value;
+    static_assert(F4 || std::is_same<KV, e4m3>::value, "cache type");
     using Lay = PrefillF8Layout<D, C>;
     constexpr uint32_t KVB = Lay::KV_BYTES;
     constexpr int NS = Lay::STAGES;
@@ -231,8 +234,12 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         constexpr int RPI = 512 / D, NI = 32 / RPI;       // rows of an instruction; instructions
         const int jl = (lane & 3) | (D == 128 ? (lane >> 1) & 4 : 0);
         const int r0 = D == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
+        constexpr int ROWB = F4 ? D / 2 : D;              // bytes of a row's codes
+        constexpr int TILE = tile_bytes<KV, D>();
         const unsigned char *cache = static_cast<const unsigned char *>(kside ? p.k_cache : p.v_cache) +
-                                     r0 * D + 16 * jl;
+                                     r0 * ROWB + (ROWB / (D / 16)) * jl;
+        const unsigned char *scales = static_cast<const unsigned char *>(kside ? p.k_cache : p.v_cache) +
+                                      8 * D + r0 * (D / 16) + jl;    // E2M1: of this lane's 16 codes
         // f16 chunk cc of row r lies at cc ^ (r & 7) of its 128-byte group; with
         // four rows an instruction, every second one flips bit 2 of that
         unsigned char *const stage0 = smem + (kside ? Lay::OFF_K : Lay::OFF_V) +
@@ -247,14 +254,14 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         int k = -1, c = 0, pb[2] = {-1, -1};
         const int32_t *tab = nullptr;
         long long joff = 0;
-        const long long bstride = (long long)Hkv * (16 * D);
+        const long long bstride = (long long)Hkv * TILE;
         bool more = false;
         auto item_next = [&]() {                   // the next item with steps of this block's
             do more = item_at(++k, it); while (more && it.nsteps == 0);
             if (!more) return;
             c = 0;
             tab = p.block_tables + (long long)it.s * p.max_blocks + 4 * it.step0 + 2 * half;
-            joff = (long long)it.j * (16 * D);
+            joff = (long long)it.j * TILE;
         };
         auto blocks_of = [&]() {
             if (!more) return;
@@ -264,7 +271,9 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
         };
         item_next();
         blocks_of();
-        auto load = [&](uint4 (&buf)[NI]) -> bool {        // the cursor's step; moves on
+        // 16 codes of a row: E4M3 four words, E2M1 two and their scale
+        using Codes = std::conditional_t<F4, uint3, uint4>;
+        auto load = [&](Codes (&buf)[NI]) -> bool {        // the cursor's step; moves on
             if (!more) return false;
             const int key0 = 64 * (it.step0 + c) + 32 * half;
             const bool whole = key0 + 32 <= it.L;
@@ -276,32 +285,51 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
                     if (kside && lane == 0) set_error(p.err, ERR_BLOCK_ID);
                     rows = 0;
                 }
-                const unsigned char *src = cache + (rows > 0 ? pb[b] : 0) * bstride + joff;
+                const long long off = (rows > 0 ? pb[b] : 0) * bstride + joff;
 #pragma unroll
-                for (int i = 0; i < NI / 2; ++i)
-                    buf[b * (NI / 2) + i] = i * RPI + r0 < rows
-                        ? *reinterpret_cast<const uint4 *>(src + i * RPI * D) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < NI / 2; ++i) {
+                    Codes &x = buf[b * (NI / 2) + i];
+                    x = {};
+                    if (i * RPI + r0 < rows) {
+                        if constexpr (F4) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(cache + off + i * RPI * ROWB);
+                            x = make_uint3(w.x, w.y, scales[off + i * RPI * (D / 16)]);
+                        } else {
+                            x = *reinterpret_cast<const uint4 *>(cache + off + i * RPI * ROWB);
+                        }
+                    }
+                }
             }
             if (++c == it.nsteps) item_next();
             blocks_of();
             return true;
         };
-        auto store = [&](unsigned char *st, const uint4 (&buf)[NI]) {
+        auto store = [&](unsigned char *st, const Codes (&buf)[NI]) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const uint4 w = buf[i];
+                const Codes w = buf[i];
                 const int flip = RPI == 4 && (i & 1) ? 64 : 0;
                 unsigned char *row = st + i * RPI * 128;
-                *reinterpret_cast<uint4 *>(row + (lo0 ^ flip)) =
-                    make_uint4(f16x2_from_e4m3x2(w.x), f16x2_from_e4m3x2(w.x >> 16),
-                               f16x2_from_e4m3x2(w.y), f16x2_from_e4m3x2(w.y >> 16));
-                *reinterpret_cast<uint4 *>(row + (hi0 ^ flip)) =
-                    make_uint4(f16x2_from_e4m3x2(w.z), f16x2_from_e4m3x2(w.z >> 16),
-                               f16x2_from_e4m3x2(w.w), f16x2_from_e4m3x2(w.w >> 16));
+                uint4 lo, hi;
+                if constexpr (F4) {
+                    const uint32_t x = f16x2_from_e4m3x2(w.z | (w.z << 8));
+                    uint32_t a[4], b[4];
+                    f16x2_from_e2m1x8(w.x, a);
+                    f16x2_from_e2m1x8(w.y, b);
+                    lo = make_uint4(mul_f16x2(a[0], x), mul_f16x2(a[1], x), mul_f16x2(a[2], x), mul_f16x2(a[3], x));
+                    hi = make_uint4(mul_f16x2(b[0], x), mul_f16x2(b[1], x), mul_f16x2(b[2], x), mul_f16x2(b[3], x));
+                } else {
+                    lo = make_uint4(f16x2_from_e4m3x2(w.x), f16x2_from_e4m3x2(w.x >> 16),
+                                    f16x2_from_e4m3x2(w.y), f16x2_from_e4m3x2(w.y >> 16));
+                    hi = make_uint4(f16x2_from_e4m3x2(w.z), f16x2_from_e4m3x2(w.z >> 16),
+                                    f16x2_from_e4m3x2(w.w), f16x2_from_e4m3x2(w.w >> 16));
+                }
+                *reinterpret_cast<uint4 *>(row + (lo0 ^ flip)) = lo;
+                *reinterpret_cast<uint4 *>(row + (hi0 ^ flip)) = hi;
             }
         };
         unsigned g = 0;
-        auto put = [&](const uint4 (&buf)[NI]) -> bool {
+        auto put = [&](const Codes (&buf)[NI]) -> bool {
             const int st = (int)(g % NS);
             bool w = true;
             if (lane == 0 && g >= NS) w = mbar_wait_bounded(&empty[st], (g / NS - 1) & 1, p.err);
@@ -313,7 +341,7 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
             ++g;
             return true;
         };
-        uint4 b0[NI], b1[NI];
+        Codes b0[NI], b1[NI];
         bool h0 = load(b0), h1 = load(b1);
         while (h0) {
             if (!put(b0)) break;
@@ -666,11 +694,11 @@ prefill_f8_kernel(const __grid_constant__ DecodeParams p, int groups) {
 
 // Clusters of C blocks that the device holds at once (blocks for C = 1), with the
 // kernel's attributes set; looked up once per device.
-template <typename T, int D, int G, int C>
+template <typename T, typename KV, int D, int G, int C>
 cudaError_t prefill_f8_fit(int *clusters) {
     constexpr size_t smem = PrefillF8Layout<D, C>::BYTES;
     static_assert(smem + sizeof(PrefillSched) + 1024 <= 227 * 1024, "shared memory");
-    auto kern = prefill_f8_kernel<T, D, G, C>;
+    auto kern = prefill_f8_kernel<T, KV, D, G, C>;
     static std::atomic<int> fitted[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -702,7 +730,7 @@ cudaError_t prefill_f8_fit(int *clusters) {
     return cudaSuccess;
 }
 
-template <typename T, int D, int G, int C>
+template <typename T, typename KV, int D, int G, int C>
 cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items, int clusters,
                               cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
@@ -719,7 +747,7 @@ cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_f8_kernel<T, D, G, C>, p, groups);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_f8_kernel<T, KV, D, G, C>, p, groups);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -729,12 +757,12 @@ cudaError_t launch_prefill_f8(const DecodeParams &p, int groups, long long items
 // so what counts is how full the last wave is: with few items the split that
 // fills the SMs wins.  Sharing costs an exchange per item and stages, so the
 // larger split has to be better by an eighth.
-template <typename T, int D, int G>
+template <typename T, typename KV, int D, int G>
 cudaError_t run_prefill_f8(const DecodeParams &p, int groups, long long items, cudaStream_t st) {
     int fit[3];
-    cudaError_t e = prefill_f8_fit<T, D, G, 1>(&fit[0]);
-    if (e == cudaSuccess) e = prefill_f8_fit<T, D, G, 2>(&fit[1]);
-    if (e == cudaSuccess) e = prefill_f8_fit<T, D, G, 4>(&fit[2]);
+    cudaError_t e = prefill_f8_fit<T, KV, D, G, 1>(&fit[0]);
+    if (e == cudaSuccess) e = prefill_f8_fit<T, KV, D, G, 2>(&fit[1]);
+    if (e == cudaSuccess) e = prefill_f8_fit<T, KV, D, G, 4>(&fit[2]);
     if (e != cudaSuccess) return e;
     int best = 0;
     double best_t = 0.;
@@ -745,12 +773,12 @@ cudaError_t run_prefill_f8(const DecodeParams &p, int groups, long long items, c
             best_t = t;
         }
     }
-    if (best == 0) return launch_prefill_f8<T, D, G, 1>(p, groups, items, fit[0], st);
-    if (best == 1) return launch_prefill_f8<T, D, G, 2>(p, groups, items, fit[1], st);
-    return launch_prefill_f8<T, D, G, 4>(p, groups, items, fit[2], st);
+    if (best == 0) return launch_prefill_f8<T, KV, D, G, 1>(p, groups, items, fit[0], st);
+    if (best == 1) return launch_prefill_f8<T, KV, D, G, 2>(p, groups, items, fit[1], st);
+    return launch_prefill_f8<T, KV, D, G, 4>(p, groups, items, fit[2], st);
 }
 
-template <typename T>
+template <typename T, typename KV = e4m3>
 cudaError_t dispatch_prefill_f8(const DecodeParams &p, int D, int G, int groups, cudaStream_t st) {
     // at most `groups` items a run, and one more than the full items of all rows
     // for each run (a run has at least mq_split_rows rows)
@@ -762,7 +790,7 @@ cudaError_t dispatch_prefill_f8(const DecodeParams &p, int D, int G, int groups,
     items *= p.num_kv_heads;
     if (items <= 0) return cudaSuccess;
 #define PA_CASE(DD, GG) \
-    if (D == DD && G == GG) return run_prefill_f8<T, DD, GG>(p, groups, items, st);
+    if (D == DD && G == GG) return run_prefill_f8<T, KV, DD, GG>(p, groups, items, st);
     PA_CASE(64, 1) PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
     PA_CASE(128, 1) PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
 #undef PA_CASE
