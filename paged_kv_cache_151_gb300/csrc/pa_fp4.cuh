@@ -54,6 +54,22 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// a times the low or the high half of s.
+__device__ __forceinline__ uint32_t mul_by_half(uint32_t a, uint32_t s, bool hi) {
+    const __half2 x = *reinterpret_cast<const __half2 *>(&a), y = *reinterpret_cast<const __half2 *>(&s);
+    const __half2 r = __hmul2(x, hi ? __high2half2(y) : __low2half2(y));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// d = a . b on the f16 tensor cores.
+__device__ __forceinline__ void mma_f16_first(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // A transposed 8 x 8 matrix of 16-bit elements: lane (g, t) gives row g, columns 2t
 // and 2t + 1, and gets rows 2t and 2t + 1 of column g.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
@@ -152,7 +168,8 @@ struct WarpAttnF4 {
 
     // Scores of a block's 16 tokens: v[n][0], [1]: token fp4_token(g) of rows 2t,
     // 2t + 1; [2], [3]: 8 tokens on.
-    __device__ __forceinline__ void scores(uint32_t kt, float (&v)[NT][4]) const {
+    template <int CHAINS>
+    __device__ __forceinline__ void scores(uint32_t kt, float2 (&v)[NT][2]) const {
         const int r0 = fp4_token(g);
         constexpr int W = D / 32;          // 32-bit words of codes of a row
         uint32_t w0[W], w1[W], s0, s1;
@@ -169,74 +186,97 @@ struct WarpAttnF4 {
             s0 = f16x2_from_e4m3x2(lds8(kt + OFF_SC + r0 * SCB + t));
             s1 = f16x2_from_e4m3x2(lds8(kt + OFF_SC + (r0 + 8) * SCB + t));
         }
-        // two chains of matrix products a tile
-        float c[NT][2][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[n][0][e] = c[n][1][e] = 0.f;
+        float c[NT][CHAINS][4];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             // the low group's scale for the first half of the run, then the high one's
-            const uint32_t sel = D == 128 && i >= W / 2 ? 0x3232 : 0x1010;
-            const uint32_t x0 = prmt(s0, s0, sel), x1 = prmt(s1, s1, sel);
+            const bool hi = D == 128 && i >= W / 2;
             uint32_t a[4], b[4];
             f16x2_from_e2m1x8(w0[i], a);
             f16x2_from_e2m1x8(w1[i], b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                a[e] = mul_f16x2(a[e], x0);
-                b[e] = mul_f16x2(b[e], x1);
+                a[e] = mul_by_half(a[e], s0, hi);
+                b[e] = mul_by_half(b[e], s1, hi);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                mma_f16(c[n][0], a[0], b[0], a[1], b[1], qb[n][2 * i][0], qb[n][2 * i][1]);
-                mma_f16(c[n][1], a[2], b[2], a[3], b[3], qb[n][2 * i + 1][0], qb[n][2 * i + 1][1]);
+                if (i == 0) mma_f16_first(c[n][0], a[0], b[0], a[1], b[1], qb[n][0][0], qb[n][0][1]);
+                else mma_f16(c[n][0], a[0], b[0], a[1], b[1], qb[n][2 * i][0], qb[n][2 * i][1]);
+                if (i == 0 && CHAINS > 1)
+                    mma_f16_first(c[n][CHAINS - 1], a[2], b[2], a[3], b[3], qb[n][1][0], qb[n][1][1]);
+                else
+                    mma_f16(c[n][CHAINS - 1], a[2], b[2], a[3], b[3], qb[n][2 * i + 1][0], qb[n][2 * i + 1][1]);
             }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[n][e] = c[n][0][e] + c[n][1][e];
+            for (int e = 0; e < 2; ++e) {
+                v[n][e] = make_float2(c[n][0][2 * e], c[n][0][2 * e + 1]);
+                if (CHAINS > 1)
+                    v[n][e] = add2(v[n][e], make_float2(c[n][CHAINS - 1][2 * e], c[n][CHAINS - 1][2 * e + 1]));
+            }
     }
 
-    // One block.  rows: tokens of it inside the sequence (1..16); pos0: the first
-    // one's position (multi-token queries).  scale_log2 carries K's head scale.
-    template <bool CAUSAL>
-    __device__ __forceinline__ void block(uint32_t kt, uint32_t vt, int rows, int pos0, float scale_log2) {
-        float sc[NT][4];
-        scores(kt, sc);
+    // NB neighbouring blocks of a sequence with tiles kt, vt.  rows: tokens of each
+    // that count (0..16, the first ones); pos0: the first one's position
+    // (multi-token queries).  scale_log2 carries K's head scale.
+    template <bool CAUSAL, int NB>
+    __device__ __forceinline__ void step(const uint32_t (&kt)[NB], const uint32_t (&vt)[NB],
+                                         const int (&rows)[NB], int pos0, float scale_log2) {
+        float2 sc[NB][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int b = 0; b < NB; ++b) scores<(NB * NT > 1 ? 1 : 2)>(kt[b], sc[b]);
+        const float2 sl = make_float2(scale_log2, scale_log2);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[n][e] *= scale_log2;
-        const int tok = fp4_token(g);
-        if constexpr (CAUSAL) {
-            bool cut = false;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) cut = cut || pos0 + 15 > min(lim[n][0], lim[n][1]);
-            if (__any_sync(0xffffffffu, cut)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[n][e] = pos0 + tok + 8 * (e >> 1) <= lim[n][e & 1] ? sc[n][e] : -INFINITY;
-            }
-        } else if (rows < 16) {
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[n][e] = tok + 8 * (e >> 1) < rows ? sc[n][e] : -INFINITY;
+                for (int e = 0; e < 2; ++e) sc[b][n][e] = mul2(sc[b][n][e], sl);
+        const int tok = fp4_token(g);
+        bool part = false;                 // some block is not whole
+#pragma unroll
+        for (int b = 0; b < NB; ++b) part = part || rows[b] < 16;
+        if constexpr (CAUSAL) {
+            bool cut = part;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cut = cut || pos0 + 16 * NB - 1 > min(lim[n][0], lim[n][1]);
+            if (__any_sync(0xffffffffu, cut)) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = tok + 8 * e, at = i < rows[b] ? pos0 + 16 * b + i : INT32_MAX;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            sc[b][n][e].x = at <= lim[n][0] ? sc[b][n][e].x : -INFINITY;
+                            sc[b][n][e].y = at <= lim[n][1] ? sc[b][n][e].y : -INFINITY;
+                        }
+                    }
+            }
+        } else if (part) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (tok + 8 * e >= rows[b]) sc[b][n][e] = make_float2(-INFINITY, -INFINITY);
         }
         bool above = false;
         float mx[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[n][h] = fmaxf(sc[n][h], sc[n][2 + h]);
-                above = above || mx[n][h] > m_run[n][h] + F8_TOP_LOG2;
+        for (int n = 0; n < NT; ++n) {
+            mx[n][0] = fmaxf(sc[0][n][0].x, sc[0][n][1].x);
+            mx[n][1] = fmaxf(sc[0][n][0].y, sc[0][n][1].y);
+            if constexpr (NB > 1) {
+                mx[n][0] = max3f(mx[n][0], sc[NB - 1][n][0].x, sc[NB - 1][n][1].x);
+                mx[n][1] = max3f(mx[n][1], sc[NB - 1][n][0].y, sc[NB - 1][n][1].y);
             }
+            above = above || mx[n][0] > m_run[n][0] + F8_TOP_LOG2 || mx[n][1] > m_run[n][1] + F8_TOP_LOG2;
+        }
         if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -256,19 +296,24 @@ struct WarpAttnF4 {
                     }
                 }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[NB][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float a = m_run[n][0] == -INFINITY ? 0.f : m_run[n][0];   // a row that sees nothing yet
-            const float b = m_run[n][1] == -INFINITY ? 0.f : m_run[n][1];
-            const uint32_t p0 = Mma<__half>::pack(ex2(sc[n][0] - a), ex2(sc[n][1] - b));
-            const uint32_t p1 = Mma<__half>::pack(ex2(sc[n][2] - a), ex2(sc[n][3] - b));
-            add_halves(l_run[n][0], l_run[n][1], p0);      // the weights as they are used
-            add_halves(l_run[n][0], l_run[n][1], p1);
-            pb[n][0] = transpose8(p0);
-            pb[n][1] = transpose8(p1);
+            float2 nm;                     // minus the level; a row that sees nothing yet: 0
+            nm.x = m_run[n][0] == -INFINITY ? 0.f : -m_run[n][0];
+            nm.y = m_run[n][1] == -INFINITY ? 0.f : -m_run[n][1];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 x = add2(sc[b][n][e], nm);
+                    const uint32_t w = Mma<__half>::pack(ex2(x.x), ex2(x.y));
+                    add_halves(l_run[n][0], l_run[n][1], w);       // the weights as they are used
+                    pb[b][n][e] = transpose8(w);
+                }
         }
-        values(vt, rows, pb);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) values(vt[b], rows[b], pb[b]);
     }
 
     __device__ __forceinline__ void values(uint32_t vt, int rows, const uint32_t (&pb)[NT][2]) {
@@ -286,7 +331,7 @@ struct WarpAttnF4 {
                 s[i] = lds8(vt + OFF_SC + tok[i] * SCB + (g >> 1));
             }
         }
-        // rows past the sequence hold anything; their weight is 0, so what must not
+        // rows that do not count hold anything; their weight is 0, so what must not
         // stay is a scale that is NaN
         if (rows < 16) {
 #pragma unroll

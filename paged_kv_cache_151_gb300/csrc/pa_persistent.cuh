@@ -286,7 +286,7 @@ __host__ __device__ constexpr bool use_tc() { return sizeof(T) == 2; }
 #define PA_F4_BLOCKS_PER_SM 4
 #endif
 #ifndef PA_F4_MULTI_BLOCKS_PER_SM
-#define PA_F4_MULTI_BLOCKS_PER_SM 3
+#define PA_F4_MULTI_BLOCKS_PER_SM 2
 #endif
 
 // What a warp pays to enter a unit (load its query, park or write its
@@ -640,6 +640,12 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     int c0 = 0, ui_cur, pb_cur, ui_nxt, pb_nxt;
     fetch(lane, ui_cur, pb_cur);
     fetch(32 + lane, ui_nxt, pb_nxt);
+    // E2M1 caches: lane i holds where the tiles of block win + i start (-1: outside
+    // the pool) and what the block 32 later is read from; the blocks outside the pool
+    // of this window and of the one before.
+    long long tile_at = -1;
+    int win = 0;
+    unsigned bad_now = 0, bad_before = 0;
     auto of = [&](int k, int &ui, int &pb) {      // warp-uniform k
         const int kk = k - c0;
         const int a = __shfl_sync(0xffffffffu, ui_cur, kk & 31);
@@ -671,13 +677,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
             return;
         }
         unsigned char *dst = my_stages + (size_t)(k % S) * 2 * TILE;
-        if constexpr (F4) {
-            // whole tiles, codes and scales in one run each
-            const size_t off = ((size_t)pbk * Hkv + units[ui].j) * TILE;
-            mbar_arrive_expect_tx(bar, 2 * TILE + extra);
-            bulk_g2s(dst, kbase + off, TILE, bar, pol);
-            bulk_g2s(dst + TILE, vbase + off, TILE, bar, pol);
-        } else if constexpr (F8) {
+        if constexpr (F8) {
             // whole 16-row tiles, one box of 16 rows x D bytes each
             const int z = pbk * Hkv + units[ui].j;
             mbar_arrive_expect_tx(bar, 2 * TILE + extra);
@@ -706,6 +706,37 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         }
     };
 
+    // E2M1 caches: window win of the stream, from the entries that are here, and the
+    // entries of the next one on their way
+    auto take_window = [&](int ui, int pb) {
+        const bool in = win + lane < n_mine, good = in && pb >= 0 && (long long)pb < p.num_blocks;
+        tile_at = good ? ((long long)pb * Hkv + units[ui].j) * TILE : -1;
+        bad_before = bad_now;
+        bad_now = __ballot_sync(0xffffffffu, in && !good);
+        fetch(win + 32 + lane, ui_nxt, pb_nxt);
+    };
+    // block k (all lanes; in order) into stage st: the lane that holds its place copies
+    auto issue4 = [&](int k, int st) {
+        if (k == win + 32) {
+            win = k;
+            take_window(ui_nxt, pb_nxt);
+        }
+        if (lane == (k & 31)) {
+            uint64_t *bar = &my_bars[st];
+            if (tile_at < 0) {
+                set_error(p.err, ERR_BLOCK_ID);
+                mbar_arrive(bar);
+            } else {
+                // whole tiles, codes and scales in one run each
+                unsigned char *dst = my_stages + (size_t)st * 2 * TILE;
+                mbar_arrive_expect_tx(bar, 2 * TILE + (k == 0 ? stall : 0u));
+                bulk_g2s(dst, kbase + tile_at, TILE, bar, pol);
+                bulk_g2s(dst + TILE, vbase + tile_at, TILE, bar, pol);
+            }
+        }
+    };
+    if constexpr (F4) take_window(ui_cur, pb_cur);
+
     // Everything above reads only seq_lens, query_start and block_tables.
     // The caches (and q, out) are touched only after the kernel before this
     // one in the stream -- typically the cache write of the same step, which
@@ -729,9 +760,13 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
 
     const int pre = n_mine < S ? n_mine : S;
     for (int k = 0; k < pre; ++k) {
-        int ui, pbk;
-        of(k, ui, pbk);
-        if (lane == 0) issue(k, ui, pbk);
+        if constexpr (F4) {
+            issue4(k, k);
+        } else {
+            int ui, pbk;
+            of(k, ui, pbk);
+            if (lane == 0) issue(k, ui, pbk);
+        }
     }
 
     W wa;
@@ -960,6 +995,75 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     float unit_scale = p.scale_log2;               // score scale (x K's scale for E4M3)
     int k_done = 0;
     bool ok = true;
+    if constexpr (F4) {
+        // unit by unit, two blocks of it at a time
+        const uint32_t s_base = smem_u32(my_stages);
+        int k = 0, st = 0;
+        uint32_t ph = 0;                           // stage of block k, its phase
+        for (int ui = n_mine > 0 ? locate(my_lo) : 0; k < n_mine; ++ui) {
+            const int k_end = min(n_mine, cum[ui + 1] - my_lo);
+            if (k_end <= k) continue;              // a unit without blocks
+            cur = ui;
+            const UnitRec &u = units[ui];
+            if constexpr (MQ) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    wa.load_row(n, q_row(u, 16 * u.part + 8 * n + (lane >> 2)));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = 16 * u.part + 8 * n + 2 * (lane & 3) + h;
+                        wa.lim[n][h] = r < u.nq * G ? u.L - u.nq + r / G : -1;
+                    }
+                }
+            } else {
+                const T *qs = reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
+                              (long long)u.j * G * D;
+                wa.load_row(0, (lane >> 2) < G ? qs + (lane >> 2) * D : nullptr);
+            }
+            unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
+            int pos = pos_of(k, ui);
+            const int L = u.L;
+            while (k < k_end) {
+                const bool two = k + 1 < k_end;
+                const int st1 = st + 1 == S ? 0 : st + 1;
+                const uint32_t ph1 = st1 ? ph : ph ^ 1;
+                bool waited = mbar_wait_bounded(&my_bars[st], ph, p.err);
+                if (two) waited = waited && mbar_wait_bounded(&my_bars[st1], ph1, p.err);
+                if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
+                auto rows_at = [&](int kk, int at) -> int {        // blocks outside the pool: none
+                    const unsigned bad = (kk ^ win) >= 32 ? bad_before : bad_now;
+                    return (bad >> (kk & 31)) & 1 ? 0 : min(16, L - at);
+                };
+                const uint32_t a0 = s_base + st * 2 * TILE, a1 = s_base + st1 * 2 * TILE;
+                if (two) {
+                    const uint32_t kt[2] = {a0, a1}, vt[2] = {a0 + TILE, a1 + TILE};
+                    const int rows[2] = {rows_at(k, pos), rows_at(k + 1, pos + 16)};
+                    wa.template step<MQ, 2>(kt, vt, rows, pos, unit_scale);
+                } else {
+                    const uint32_t kt[1] = {a0}, vt[1] = {a0 + TILE};
+                    const int rows[1] = {rows_at(k, pos)};
+                    wa.template step<MQ, 1>(kt, vt, rows, pos, unit_scale);
+                }
+                __syncwarp();                      // every lane is done with the stages
+                if (k + S < n_mine) issue4(k + S, st);
+                if (two && k + 1 + S < n_mine) issue4(k + 1 + S, st1);
+                if (two) {
+                    k += 2;
+                    pos += 32;
+                    st = st1 + 1 == S ? 0 : st1 + 1;
+                    ph = st ? ph1 : ph1 ^ 1;
+                } else {
+                    k += 1;
+                    pos += 16;
+                    st = st1;
+                    ph = ph1;
+                }
+            }
+            k_done = k;
+            if (!ok) break;
+            if (k < n_mine) leave_unit(ui, false);
+        }
+    } else
     for (int k = 0; k < n_mine; ++k) {
         if (k - c0 == 32) {
             c0 += 32;
@@ -972,25 +1076,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         if (ui != cur) {
             if (cur >= 0) leave_unit(cur, false);
             cur = ui;
-            if constexpr (F4) {
-                const UnitRec &u = units[ui];
-                if constexpr (MQ) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        wa.load_row(n, q_row(u, 16 * u.part + 8 * n + (lane >> 2)));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int r = 16 * u.part + 8 * n + 2 * (lane & 3) + h;
-                            wa.lim[n][h] = r < u.nq * G ? u.L - u.nq + r / G : -1;
-                        }
-                    }
-                } else {
-                    const T *qs = reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
-                                  (long long)u.j * G * D;
-                    wa.load_row(0, (lane >> 2) < G ? qs + (lane >> 2) * D : nullptr);
-                }
-                unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
-            } else if constexpr (MQ) {
+            if constexpr (MQ) {
                 const UnitRec &u = units[ui];
                 const int r_lo = 16 * u.part + (lane >> 2), r_hi = r_lo + 8;
                 wa.load_q(q_row(u, r_lo), q_row(u, r_hi), u.L - u.nq + r_lo / G, u.L - u.nq + r_hi / G);
@@ -1023,7 +1109,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
             if constexpr (TC) {
                 // tail rows hold other tokens' data: the one-token block math
                 // drops them in registers; the others clear them in the tile
-                if (F8 || (MQ && !F4)) {
+                if (F8 || MQ) {
                     if (rows < 16) {
                         if constexpr (F8) W::zero_rows(Kt + TILE, rows, lane);
                         else WarpAttnTC<T, D, G>::zero_rows(Kt + TILE, rows, lane);
@@ -1033,8 +1119,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                         __syncwarp();
                     }
                 }
-                if constexpr (F4) wa.template block<MQ>(smem_u32(Kt), smem_u32(Kt + TILE), rows, pos_of(k, ui), unit_scale);
-                else if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
+                if constexpr (MQ) wa.block(smem_u32(Kt), smem_u32(Kt + TILE), pos_of(k, ui), unit_scale);
                 else wa.block(smem_u32(Kt), smem_u32(Kt + TILE), rows, unit_scale);
             } else {
                 wa.block(Kt, Kt + TILE, rows, Sc, Pb, Al);
