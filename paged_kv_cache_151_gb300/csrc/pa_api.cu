@@ -105,7 +105,10 @@ cudaError_t run_split(const pa::DecodeParams &p, int dtype, int D, int G, dim3 g
 #define PA_F8_CLUSTER 4
 #endif
 #ifndef PA_F4_CLUSTER
-#define PA_F4_CLUSTER 4
+#define PA_F4_CLUSTER 2
+#endif
+#ifndef PA_F4_MULTI_CLUSTER
+#define PA_F4_MULTI_CLUSTER 2
 #endif
 
 cudaError_t run_persistent(const pa::DecodeParams &p, int dtype, int D, int G, bool partial,
@@ -726,8 +729,8 @@ int decode_multi_codes(
     }
     const long long unit_bound = (long long)num_seqs * num_kv_heads * ((small_rows + 15) / 16);
     const cudaError_t e =
-        f4 ? (dtype == PA_BF16 ? pa::decode_multi_fp4_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
-                               : pa::decode_multi_fp4_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st))
+        f4 ? (dtype == PA_BF16 ? pa::decode_multi_fp4_bf16(p, head_dim, G, unit_bound, PA_F4_MULTI_CLUSTER, st)
+                               : pa::decode_multi_fp4_f16(p, head_dim, G, unit_bound, PA_F4_MULTI_CLUSTER, st))
            : (dtype == PA_BF16 ? pa::decode_multi_fp8_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
                                : pa::decode_multi_fp8_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st));
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;

@@ -31,6 +31,9 @@ __host__ __device__ constexpr int tile_bytes() {
     return std::is_same<KV, e2m1>::value ? 9 * D : 16 * D * (int)sizeof(KV);
 }
 
+// A condition whose code the loop should not step over.
+__device__ __forceinline__ bool rarely(bool c) { return __builtin_expect(c, 0); }
+
 // The eight E2M1 codes of w as f16 pairs, byte i in r[i] (low half: low code).
 __device__ __forceinline__ void f16x2_from_e2m1x8(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
@@ -117,10 +120,11 @@ __device__ __forceinline__ int fp4_token(int r) { return r ^ ((r >> 2) & 1); }
 //
 // A row's reference level moves only when a score exceeds it by more than
 // F8_TOP_LOG2, as in WarpAttnF8x16; (m, l, acc) are to that level.
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int R>
 struct WarpAttnF4 {
     static_assert(sizeof(T) == 2, "q and out are 16-bit");
     static_assert(D == 64 || D == 128, "head_dim");
+    static_assert(NT == 1 || R == 8, "rows of a tile: 8, or the G heads of one token");
     static constexpr int KS = D / 16;      // k-steps of the score product
     static constexpr int MT = D / 16;      // 16-row tiles of the value product
     static constexpr int DL = D / 8;       // elements of a lane in it
@@ -130,7 +134,9 @@ struct WarpAttnF4 {
     uint32_t qb[NT][KS][2];                // f16 B fragments
     // acc[n][mt]: elements DL g + 2mt (0, 1) and + 1 (2, 3) of rows 2t and 2t + 1
     float acc[NT][MT][4];
-    float m_run[NT][2], l_run[NT][2];      // level; this lane's part of the sum
+    // a row's level as what is added to its scores (minus it; 0 before the first one)
+    // and the score that moves it (-inf before); this lane's part of its sum
+    float down[NT][2], limit[NT][2], l_run[NT][2];
     int lim[NT][2];                        // last visible position, -1: no such row (multi-token queries)
 
     __device__ __forceinline__ void init(int lane_) {
@@ -143,7 +149,8 @@ struct WarpAttnF4 {
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m_run[n][0] = m_run[n][1] = -INFINITY;
+            down[n][0] = down[n][1] = 0.f;
+            limit[n][0] = limit[n][1] = -INFINITY;
             l_run[n][0] = l_run[n][1] = 0.f;
 #pragma unroll
             for (int j = 0; j < MT; ++j)
@@ -154,10 +161,9 @@ struct WarpAttnF4 {
 
     // query row g of tile n (nullptr: no such row)
     __device__ __forceinline__ void load_row(int n, const T *q) {
-        constexpr int W = D / 32;          // 16-byte words of a lane
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const uint4 x = q ? *reinterpret_cast<const uint4 *>(q + (D / 4) * t + 8 * i)
+        for (int i = 0; i < D / 32; ++i) {
+            const uint4 x = q ? __ldg(reinterpret_cast<const uint4 *>(q + (D / 4) * t + 8 * i))
                               : make_uint4(0, 0, 0, 0);
             qb[n][2 * i][0] = WarpAttnF8<T, D, 1>::to_f16x2(x.x);
             qb[n][2 * i][1] = WarpAttnF8<T, D, 1>::to_f16x2(x.y);
@@ -243,7 +249,7 @@ struct WarpAttnF4 {
             bool cut = part;
 #pragma unroll
             for (int n = 0; n < NT; ++n) cut = cut || pos0 + 16 * NB - 1 > min(lim[n][0], lim[n][1]);
-            if (__any_sync(0xffffffffu, cut)) {
+            if (rarely(__any_sync(0xffffffffu, cut))) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -256,7 +262,7 @@ struct WarpAttnF4 {
                         }
                     }
             }
-        } else if (part) {
+        } else if (rarely(part)) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -275,9 +281,9 @@ struct WarpAttnF4 {
                 mx[n][0] = max3f(mx[n][0], sc[NB - 1][n][0].x, sc[NB - 1][n][1].x);
                 mx[n][1] = max3f(mx[n][1], sc[NB - 1][n][0].y, sc[NB - 1][n][1].y);
             }
-            above = above || mx[n][0] > m_run[n][0] + F8_TOP_LOG2 || mx[n][1] > m_run[n][1] + F8_TOP_LOG2;
+            above = above || mx[n][0] > limit[n][0] || mx[n][1] > limit[n][1];
         }
-        if (__any_sync(0xffffffffu, above)) {
+        if (rarely(__any_sync(0xffffffffu, above))) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -285,9 +291,11 @@ struct WarpAttnF4 {
                     float m = mx[n][h];
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    const float m_new = m > m_run[n][h] + F8_TOP_LOG2 ? m - F8_BELOW_LOG2 : m_run[n][h];
-                    const float alpha = m_new == m_run[n][h] ? 1.f : ex2(m_run[n][h] - m_new);
-                    m_run[n][h] = m_new;
+                    if (!(m > limit[n][h])) continue;
+                    const float to = F8_BELOW_LOG2 - m;
+                    const float alpha = limit[n][h] == -INFINITY ? 0.f : ex2(to - down[n][h]);
+                    down[n][h] = to;
+                    limit[n][h] = m + (F8_TOP_LOG2 - F8_BELOW_LOG2);
                     l_run[n][h] *= alpha;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
@@ -299,9 +307,7 @@ struct WarpAttnF4 {
         uint32_t pb[NB][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float2 nm;                     // minus the level; a row that sees nothing yet: 0
-            nm.x = m_run[n][0] == -INFINITY ? 0.f : -m_run[n][0];
-            nm.y = m_run[n][1] == -INFINITY ? 0.f : -m_run[n][1];
+            const float2 nm = make_float2(down[n][0], down[n][1]);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -333,7 +339,7 @@ struct WarpAttnF4 {
         }
         // rows that do not count hold anything; their weight is 0, so what must not
         // stay is a scale that is NaN
-        if (rows < 16) {
+        if (rarely(rows < 16)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[i] = tok[i] < rows ? s[i] : 0u;
         }
@@ -366,45 +372,125 @@ struct WarpAttnF4 {
             {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l_run[n][h] += __shfl_xor_sync(0xffffffffu, l_run[n][h], o);
-                // only NaN seen: a level that a merge does not take for an empty partial
-                if (m_run[n][h] == -INFINITY && l_run[n][h] != 0.f) m_run[n][h] = 0.f;
             }
     }
 
-    // merge slot: Mw, Lw [rows], Aw [rows][D]; rows: 8 n + 2t + h below `rows`
-    __device__ __forceinline__ void store_partial(float *Mw, float *Lw, float *Aw, int rows) const {
+    // The level of a row, -inf where it has none: nothing seen yet, if the sum is 0
+    // (with a sum, of NaN, one that a merge does not take for an empty partial).
+    __device__ __forceinline__ float level(int n, int h) const {
+        return limit[n][h] == -INFINITY && l_run[n][h] == 0.f ? -INFINITY : -down[n][h];
+    }
+
+    // A partial, of 8 NT (NT = 1: R) rows of D floats: the accumulators as the lanes
+    // hold them, (m, l) of the rows behind them; every warp's lie alike, so a merge
+    // adds up what the same lane has stored.
+    static constexpr int ROWS = NT > 1 ? 8 * NT : R;
+    static constexpr int LANES = R > 1 ? 4 * R : 8;        // that hold rows
+    __device__ __forceinline__ bool holds() const { return 2 * t < R; }
+    __device__ __forceinline__ int slot(int n, int mt) const {     // in floats
+        return ((n * MT + mt) * LANES + (R > 1 ? g * (R / 2) + t : g)) * (R > 1 ? 4 : 2);
+    }
+    __device__ __forceinline__ void store_partial(float *P) const {
+        if (!holds()) return;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 8 * n + 2 * t + h;
-                if (r >= rows) continue;
+            for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (R > 1)
+                    *reinterpret_cast<float4 *>(P + slot(n, mt)) =
+                        make_float4(acc[n][mt][0], acc[n][mt][1], acc[n][mt][2], acc[n][mt][3]);
+                else
+                    *reinterpret_cast<float2 *>(P + slot(n, mt)) = make_float2(acc[n][mt][0], acc[n][mt][2]);
+            }
+#pragma unroll
+            for (int h = 0; h < (R > 1 ? 2 : 1); ++h) {
                 if (g == 0) {
-                    Mw[r] = m_run[n][h];
-                    Lw[r] = l_run[n][h];
+                    P[ROWS * D + 8 * n + 2 * t + h] = level(n, h);
+                    P[ROWS * D + ROWS + 8 * n + 2 * t + h] = l_run[n][h];
+                }
+            }
+        }
+    }
+
+    // The state becomes the merge of the partials that each(f) calls f(addr) for, in
+    // that order and twice: addr a partial in the cluster's shared memory.
+    template <typename Each>
+    __device__ __forceinline__ void merge(Each &&each) {
+        constexpr int HS = R > 1 ? 2 : 1;
+        float top[NT][2];
+        reset();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+        if (!holds()) return;
+        each([&](uint32_t P) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < HS; ++h)
+                    top[n][h] = fmaxf(top[n][h], ld_dsmem_f32(P + (ROWS * D + 8 * n + 2 * t + h) * 4));
+        });
+        each([&](uint32_t P) {
+            float4 a[NT][MT];
+            float f[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                f[n][1] = 0.f;
+#pragma unroll
+                for (int h = 0; h < HS; ++h) {
+                    const float m = ld_dsmem_f32(P + (ROWS * D + 8 * n + 2 * t + h) * 4);
+                    const float l = ld_dsmem_f32(P + (ROWS * D + ROWS + 8 * n + 2 * t + h) * 4);
+                    f[n][h] = m == -INFINITY ? 0.f : ex2(m - top[n][h]);
+                    l_run[n][h] = fmaf(f[n][h], l, l_run[n][h]);
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<float2 *>(Aw + r * D + DL * g + 2 * mt) =
-                        make_float2(acc[n][mt][h], acc[n][mt][2 + h]);
+                for (int mt = 0; mt < MT; ++mt) {
+                    if constexpr (R > 1) {
+                        a[n][mt] = ld_dsmem_f32x4(P + slot(n, mt) * 4);
+                    } else {
+                        a[n][mt].x = ld_dsmem_f32(P + slot(n, mt) * 4);
+                        a[n][mt].z = ld_dsmem_f32(P + slot(n, mt) * 4 + 4);
+                        a[n][mt].y = a[n][mt].w = 0.f;
+                    }
+                }
             }
-    }
-
-    // After finish(): f(row, d, v0, v1, first, m, l) for the normalised outputs at d,
-    // d + 1 of the rows below `rows` that exist.
-    template <typename Fn>
-    __device__ __forceinline__ void for_each_result(int rows, Fn &&f) const {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    acc[n][mt][0] = fmaf(f[n][0], a[n][mt].x, acc[n][mt][0]);
+                    acc[n][mt][1] = fmaf(f[n][1], a[n][mt].y, acc[n][mt][1]);
+                    acc[n][mt][2] = fmaf(f[n][0], a[n][mt].z, acc[n][mt][2]);
+                    acc[n][mt][3] = fmaf(f[n][1], a[n][mt].w, acc[n][mt][3]);
+                }
+        });
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 8 * n + 2 * t + h;
-                if (r >= rows || (NT > 1 && lim[n][h] < 0)) continue;
-                const float l = l_run[n][h], inv = l > 0.f ? 1.f / l : 0.f;
+            for (int h = 0; h < HS; ++h)
+                if (top[n][h] != -INFINITY) {
+                    down[n][h] = -top[n][h];
+                    limit[n][h] = top[n][h];
+                }
+    }
+
+    // After finish(): f(row, d, v, m, l) with the normalised outputs v[0 .. D/8) at d ..
+    // of the rows that exist.
+    template <typename Fn>
+    __device__ __forceinline__ void for_each_row(Fn &&f) const {
+        if (!holds()) return;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    f(r, DL * g + 2 * mt, acc[n][mt][h] * inv, acc[n][mt][2 + h] * inv, g == 0 && mt == 0,
-                      m_run[n][h], l);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < (R > 1 ? 2 : 1); ++h) {
+                if (NT > 1 && lim[n][h] < 0) continue;
+                const float l = l_run[n][h], inv = l > 0.f ? 1.f / l : 0.f;
+                float v[DL];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    v[2 * mt] = acc[n][mt][h] * inv;
+                    v[2 * mt + 1] = acc[n][mt][2 + h] * inv;
+                }
+                f(8 * n + 2 * t + h, DL * g, v, level(n, h), l);
             }
     }
 };

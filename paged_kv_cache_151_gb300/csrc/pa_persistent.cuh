@@ -282,11 +282,11 @@ __host__ __device__ constexpr bool use_tc() { return sizeof(T) == 2; }
 #ifndef PA_F8_BLOCKS_PER_SM
 #define PA_F8_BLOCKS_PER_SM 3
 #endif
-#ifndef PA_F4_BLOCKS_PER_SM
-#define PA_F4_BLOCKS_PER_SM 4
+#ifndef PA_F4_WARPS
+#define PA_F4_WARPS 8
 #endif
-#ifndef PA_F4_MULTI_BLOCKS_PER_SM
-#define PA_F4_MULTI_BLOCKS_PER_SM 2
+#ifndef PA_F4_MULTI_WARPS
+#define PA_F4_MULTI_WARPS 8
 #endif
 
 // What a warp pays to enter a unit (load its query, park or write its
@@ -305,6 +305,7 @@ __host__ __device__ constexpr bool use_tc() { return sizeof(T) == 2; }
 #endif
 template <typename KV, int MODE>
 __host__ __device__ constexpr int persistent_warps() {
+    if (std::is_same<KV, e2m1>::value) return MODE == MODE_MULTI ? PA_F4_MULTI_WARPS : PA_F4_WARPS;
     return (sizeof(KV) == 2 && (MODE == MODE_DECODE || MODE == MODE_MULTI)) ? PA_DECODE_WARPS : 4;
 }
 
@@ -315,7 +316,7 @@ __host__ __device__ constexpr int persistent_warps() {
 // either way).
 template <typename KV, int NW, int MODE>
 __host__ __device__ constexpr int persistent_blocks_per_sm() {
-    if (std::is_same<KV, e2m1>::value) return MODE == MODE_MULTI ? PA_F4_MULTI_BLOCKS_PER_SM : PA_F4_BLOCKS_PER_SM;
+    if (std::is_same<KV, e2m1>::value) return NW >= 8 ? (NW >= 16 || MODE == MODE_MULTI ? 1 : 2) : (MODE == MODE_MULTI ? 2 : 4);
     return sizeof(KV) == 1 ? (MODE == MODE_MULTI ? 2 : PA_F8_BLOCKS_PER_SM) : (NW >= 8 ? 1 : 2);
 }
 
@@ -334,13 +335,13 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     // of the cluster merge it together instead, a row each, once all are done: one
     // warp would read 16 partials of 16 rows through distributed shared memory,
     // some 25 us of a batch of one.
-    constexpr bool SPREAD = SCALED && MQ;
+    constexpr bool SPREAD = F8 && MQ;
     constexpr int SPREAD_PARTS = 4;
     static_assert(!MQ || TC, "multi-token queries use the tensor-core path");
     static_assert(SCALED || std::is_same<KV, T>::value, "cache type");
     static_assert(!SCALED || TC, "E4M3 and E2M1 caches: 16-bit q");
     using W = std::conditional_t<
-        F4, WarpAttnF4<T, D, MQ ? 2 : 1>, std::conditional_t<
+        F4, WarpAttnF4<T, D, MQ ? 2 : 1, MQ ? 8 : G>, std::conditional_t<
         F8, std::conditional_t<MQ, WarpAttnF8x16<T, D>, WarpAttnF8<T, D, G>>,
         std::conditional_t<MQ, WarpAttnTC16<T, D>,
                            std::conditional_t<TC, WarpAttnTC<T, D, G>, WarpAttn<T, D, G>>>>>;
@@ -380,7 +381,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     // Behind the prefill kernel there may be no short run at all: leave before the
     // set-up then (every block of the grid finds the same), once that kernel is
     // done.  A bad length or range takes the long way, which flags it.
-    if constexpr (SPREAD) {
+    if constexpr (SCALED && MQ) {
         if (p.mq_split_rows > 0) {
             bool some = false;
             for (int i = tid; i < B; i += NT) {
@@ -426,7 +427,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         const int a = p.query_start[s], b = p.query_start[s + 1];
         return a >= 0 && b >= a && b <= p.num_q_rows && b - a <= p.max_query_len && b - a <= L;
     };
-    int Bp = NT;
+    int Bp = NT < 128 ? NT : 128;
     while (Bp < B) Bp <<= 1;
     uint32_t *keys = reinterpret_cast<uint32_t *>(stages);           // [Bp]
     int *start = reinterpret_cast<int *>(stages + (size_t)Bp * 4);   // [B]
@@ -715,21 +716,24 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         bad_now = __ballot_sync(0xffffffffu, in && !good);
         fetch(win + 32 + lane, ui_nxt, pb_nxt);
     };
-    // block k (all lanes; in order) into stage st: the lane that holds its place copies
-    auto issue4 = [&](int k, int st) {
-        if (k == win + 32) {
+    // blocks k and, with two, k + 1 (all lanes; in order) into stages st and st1: the
+    // lanes that hold their places copy
+    auto issue4 = [&](int k, int st, int st1, bool two) {
+        if (rarely(k == win + 32)) {
             win = k;
             take_window(ui_nxt, pb_nxt);
         }
-        if (lane == (k & 31)) {
-            uint64_t *bar = &my_bars[st];
-            if (tile_at < 0) {
+        const int i = lane - (k & 31);
+        if (i == 0 || (two && i == 1)) {
+            const int to = i ? st1 : st;
+            uint64_t *bar = &my_bars[to];
+            if (rarely(tile_at < 0)) {
                 set_error(p.err, ERR_BLOCK_ID);
                 mbar_arrive(bar);
             } else {
                 // whole tiles, codes and scales in one run each
-                unsigned char *dst = my_stages + (size_t)st * 2 * TILE;
-                mbar_arrive_expect_tx(bar, 2 * TILE + (k == 0 ? stall : 0u));
+                unsigned char *dst = my_stages + (size_t)to * 2 * TILE;
+                mbar_arrive_expect_tx(bar, 2 * TILE + (k + i == 0 ? stall : 0u));
                 bulk_g2s(dst, kbase + tile_at, TILE, bar, pol);
                 bulk_g2s(dst + TILE, vbase + tile_at, TILE, bar, pol);
             }
@@ -761,7 +765,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     const int pre = n_mine < S ? n_mine : S;
     for (int k = 0; k < pre; ++k) {
         if constexpr (F4) {
-            issue4(k, k);
+            issue4(k, k, k, false);
         } else {
             int ui, pbk;
             of(k, ui, pbk);
@@ -827,12 +831,64 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         }
     };
 
+    // E2M1: the causal limits of unit u's rows, and its result from the warp's state.
+    auto set_rows = [&](const UnitRec &u) {
+        if constexpr (F4 && MQ) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = 16 * u.part + 8 * n + 2 * (lane & 3) + h;
+                    wa.lim[n][h] = r < u.nq * G ? u.L - u.nq + r / G : -1;
+                }
+        }
+    };
+    auto write_unit = [&](const UnitRec &u) {
+        if constexpr (F4) {
+            constexpr int DL = D / 8;
+            const float vsc = v_scale_of(u);
+            wa.for_each_row([&](int r, int d, const float (&v)[DL], float m, float l) {
+                if constexpr (PARTIAL) {
+                    const long long row = ((long long)u.s * H + u.j * G + r) * p.max_parts + u.part;
+                    float *o = p.part_o + row * D + d;
+#pragma unroll
+                    for (int e = 0; e < DL; e += 4)
+                        *reinterpret_cast<float4 *>(o + e) =
+                            make_float4(v[e] * vsc, v[e + 1] * vsc, v[e + 2] * vsc, v[e + 3] * vsc);
+                    if (d == 0) {
+                        p.part_m[row] = m * LN2;      // natural units
+                        p.part_l[row] = l;
+                    }
+                } else {
+                    T *o = reinterpret_cast<T *>(p.out) + out_row(u, r) * D + d;
+#pragma unroll
+                    for (int e = 0; e < DL; e += 8)
+                        *reinterpret_cast<uint4 *>(o + e) =
+                            make_uint4(Mma<T>::pack(v[e] * vsc, v[e + 1] * vsc),
+                                       Mma<T>::pack(v[e + 2] * vsc, v[e + 3] * vsc),
+                                       Mma<T>::pack(v[e + 4] * vsc, v[e + 5] * vsc),
+                                       Mma<T>::pack(v[e + 6] * vsc, v[e + 7] * vsc));
+                }
+            });
+        }
+    };
+
     // Merge every partial of unit `ui` (in warp order) and write the unit's
     // result; run by the last of the unit's warps to arrive.
     auto merge_unit = [&](int ui) {
         const UnitRec u = units[ui];
         const int g_first = owner(cum[ui]), g_last = owner(cum[ui] + u.nb - 1);
-        {
+        if constexpr (F4) {
+            set_rows(u);
+            wa.merge([&](auto &&f) {
+                for (int w = g_first; w <= g_last; ++w) {
+                    if (range_lo(w) == range_lo(w + 1)) continue;
+                    const float *pw = part_of(w, (w == g_last && w != g_first) ? 0 : 1);
+                    f(map_to_rank(pw, (uint32_t)(w / NW)));
+                }
+            });
+            write_unit(u);
+        } else {
             // Merge the unit's partials in warp order with a running maximum.
             // A lane owns chunks lane, lane + 32, ... (E outputs each), taken
             // CG at a time; all loads of one partial for those chunks are
@@ -930,8 +986,11 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         int shared_unit = -1;
         if (!from_before && !to_after) {
             // a unit only this warp touched: write its result from registers
+            if constexpr (F4) {
+                write_unit(u);
+            } else {
             const float vsc = v_scale_of(u);
-            auto write = [&](int g, int d, float v0, float v1, bool first, float m, float l) {
+            wa.for_each_result([&](int g, int d, float v0, float v1, bool first, float m, float l) {
                 v0 *= vsc;
                 v1 *= vsc;
                 if constexpr (PARTIAL) {
@@ -946,13 +1005,12 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                     T *o = reinterpret_cast<T *>(p.out) + out_row(u, g) * D + d;
                     store_pair<T>(o, v0, v1);
                 }
-            };
-            if constexpr (F4) wa.for_each_result(ROWS, write);
-            else wa.for_each_result(write);
+            });
+            }
         } else {
             float *mine = part_of(gw, (from_before && !to_after) ? 0 : 1);
             // partial layout: O[ROWS][D], M[ROWS], L[ROWS]
-            if constexpr (F4) wa.store_partial(mine + ROWS * D, mine + ROWS * D + ROWS, mine, ROWS);
+            if constexpr (F4) wa.store_partial(mine);
             else wa.store_partial(mine + ROWS * D, mine + ROWS * D + ROWS, mine);
             shared_unit = ui;
         }
@@ -1007,19 +1065,13 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
             const UnitRec &u = units[ui];
             if constexpr (MQ) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    wa.load_row(n, q_row(u, 16 * u.part + 8 * n + (lane >> 2)));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = 16 * u.part + 8 * n + 2 * (lane & 3) + h;
-                        wa.lim[n][h] = r < u.nq * G ? u.L - u.nq + r / G : -1;
-                    }
-                }
+                for (int n = 0; n < 2; ++n) wa.load_row(n, q_row(u, 16 * u.part + 8 * n + (lane >> 2)));
             } else {
                 const T *qs = reinterpret_cast<const T *>(p.q) + (long long)u.s * p.q_seq_stride +
                               (long long)u.j * G * D;
                 wa.load_row(0, (lane >> 2) < G ? qs + (lane >> 2) * D : nullptr);
             }
+            set_rows(u);
             unit_scale = p.scale_log2 * __ldg(p.k_scale + u.j);
             int pos = pos_of(k, ui);
             const int L = u.L;
@@ -1027,26 +1079,36 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                 const bool two = k + 1 < k_end;
                 const int st1 = st + 1 == S ? 0 : st + 1;
                 const uint32_t ph1 = st1 ? ph : ph ^ 1;
-                bool waited = mbar_wait_bounded(&my_bars[st], ph, p.err);
-                if (two) waited = waited && mbar_wait_bounded(&my_bars[st1], ph1, p.err);
-                if (!__all_sync(0xffffffffu, waited)) { ok = false; break; }
-                auto rows_at = [&](int kk, int at) -> int {        // blocks outside the pool: none
-                    const unsigned bad = (kk ^ win) >= 32 ? bad_before : bad_now;
-                    return (bad >> (kk & 31)) & 1 ? 0 : min(16, L - at);
-                };
+                bool here = mbar_try_wait(&my_bars[st], ph) && (!two || mbar_try_wait(&my_bars[st1], ph1));
+                if (rarely(!__all_sync(0xffffffffu, here))) {
+                    here = mbar_wait_bounded(&my_bars[st], ph, p.err) &&
+                           (!two || mbar_wait_bounded(&my_bars[st1], ph1, p.err));
+                    if (!__all_sync(0xffffffffu, here)) { ok = false; break; }
+                }
                 const uint32_t a0 = s_base + st * 2 * TILE, a1 = s_base + st1 * 2 * TILE;
-                if (two) {
+                auto lost = [&](int kk) -> bool {  // a block outside the pool
+                    return ((((kk ^ win) >= 32 ? bad_before : bad_now) >> (kk & 31)) & 1) != 0;
+                };
+                if (__builtin_expect(two, 1)) {
                     const uint32_t kt[2] = {a0, a1}, vt[2] = {a0 + TILE, a1 + TILE};
-                    const int rows[2] = {rows_at(k, pos), rows_at(k + 1, pos + 16)};
+                    int rows[2] = {16, min(16, L - pos - 16)};     // only a last block is not whole
+                    if (rarely((bad_now | bad_before) != 0)) {
+                        if (lost(k)) rows[0] = 0;
+                        if (lost(k + 1)) rows[1] = 0;
+                    }
                     wa.template step<MQ, 2>(kt, vt, rows, pos, unit_scale);
                 } else {
                     const uint32_t kt[1] = {a0}, vt[1] = {a0 + TILE};
-                    const int rows[1] = {rows_at(k, pos)};
+                    const int rows[1] = {lost(k) ? 0 : min(16, L - pos)};
                     wa.template step<MQ, 1>(kt, vt, rows, pos, unit_scale);
                 }
                 __syncwarp();                      // every lane is done with the stages
-                if (k + S < n_mine) issue4(k + S, st);
-                if (two && k + 1 + S < n_mine) issue4(k + 1 + S, st1);
+                const int kn = k + S;
+                if (kn < n_mine) {
+                    const bool more = two && kn + 1 < n_mine, apart = (kn & 31) == 31;
+                    issue4(kn, st, st1, more && !apart);
+                    if (rarely(more && apart)) issue4(kn + 1, st1, st1, false);
+                }
                 if (two) {
                     k += 2;
                     pos += 32;
