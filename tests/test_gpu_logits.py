@@ -157,13 +157,14 @@ def test_in_place(cuda_lib):
 
 
 def test_rows_of_wider_tensors(cuda_lib):
+    """Rows that start elsewhere: their sums are taken in another order, so the bound
+    of check holds and not equality."""
     c = Case(8, [2, 3], 1001, pad=0)
-    want = c.run(cuda_lib)
     x = torch.full((5, 1313), float("nan"), device="cuda")
     out = torch.full((5, 1237), 3.0, device="cuda")
     x[:, 5:1006] = c.x.cuda()
     c.run(cuda_lib, out=out[:, 7:1008], x=x[:, 5:1006])
-    assert torch.equal(out[:, 7:1008], want)
+    c.check(out[:, 7:1008])
     assert (out[:, :7] == 3).all() and (out[:, 1008:] == 3).all()
 
 
