@@ -106,6 +106,7 @@ struct Fp4RowsParams {
     const int64_t *slot_mapping;              // [num_tokens]
     int64_t num_tokens, num_slots, k_stride, v_stride;
     int num_kv_heads, head_dim;
+    unsigned num_items;                       // of a launch: groups of 16 of its tokens' rows
     unsigned int *err;
 };
 cudaError_t reshape_and_cache_fp4(const Fp4RowsParams &p, int dtype, cudaStream_t st);
