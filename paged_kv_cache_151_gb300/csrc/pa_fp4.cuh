@@ -386,6 +386,7 @@ struct WarpAttnF4 {
     // adds up what the same lane has stored.
     static constexpr int ROWS = NT > 1 ? 8 * NT : R;
     static constexpr int LANES = R > 1 ? 4 * R : 8;        // that hold rows
+    static constexpr int HS = R > 1 ? 2 : 1;               // rows of a lane in a tile
     __device__ __forceinline__ bool holds() const { return 2 * t < R; }
     __device__ __forceinline__ int slot(int n, int mt) const {     // in floats
         return ((n * MT + mt) * LANES + (R > 1 ? g * (R / 2) + t : g)) * (R > 1 ? 4 : 2);
@@ -412,57 +413,96 @@ struct WarpAttnF4 {
         }
     }
 
-    // The state becomes the merge of the partials that each(f) calls f(addr) for, in
-    // that order and twice: addr a partial in the cluster's shared memory.
-    template <typename Each>
-    __device__ __forceinline__ void merge(Each &&each) {
-        constexpr int HS = R > 1 ? 2 : 1;
-        float top[NT][2];
+    // The state becomes the merge of partials: merge_begin, merge_levels of all of
+    // them, merge_add of all of them, merge_end.  Lane i of `which` gives where a partial
+    // lies in the cluster's shared memory; they are taken in the lanes' order, the loads
+    // of two (of four, for the levels) in flight.
+    float top[NT][2];
+    __device__ __forceinline__ void merge_begin() {
         reset();
 #pragma unroll
         for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
-        if (!holds()) return;
-        each([&](uint32_t P) {
+    }
+    __device__ __forceinline__ void merge_levels(uint32_t at, unsigned which) {
+        while (which) {
+            uint32_t P[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 4; ++i) {          // the last ones again where there are no more
+                const int l = __ffs(which) - 1;
+                P[i] = l >= 0 ? __shfl_sync(0xffffffffu, at, l & 31) : P[i ? i - 1 : 0];
+                which &= which - 1;
+            }
+            if (holds()) {
+                float m[4][NT][2];
 #pragma unroll
-                for (int h = 0; h < HS; ++h)
-                    top[n][h] = fmaxf(top[n][h], ld_dsmem_f32(P + (ROWS * D + 8 * n + 2 * t + h) * 4));
-        });
-        each([&](uint32_t P) {
-            float4 a[NT][MT];
-            float f[NT][2];
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < HS; ++h) m[i][n][h] = ld_dsmem_f32(P[i] + (ROWS * D + 8 * n + 2 * t + h) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < HS; ++h) top[n][h] = fmaxf(top[n][h], m[i][n][h]);
+            }
+        }
+    }
+    __device__ __forceinline__ void merge_add(uint32_t at, unsigned which) {
+        while (which) {
+            const int l0 = __ffs(which) - 1;
+            which &= which - 1;
+            const int l1 = __ffs(which) - 1;       // -1: a single one
+            which &= which - 1;
+            uint32_t P[2];
+            P[0] = __shfl_sync(0xffffffffu, at, l0);
+            P[1] = __shfl_sync(0xffffffffu, at, l1 & 31);
+            if (!holds()) continue;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                f[n][1] = 0.f;
+                float m[2][2], l[2][2];
+                float4 a[2][MT];
 #pragma unroll
-                for (int h = 0; h < HS; ++h) {
-                    const float m = ld_dsmem_f32(P + (ROWS * D + 8 * n + 2 * t + h) * 4);
-                    const float l = ld_dsmem_f32(P + (ROWS * D + ROWS + 8 * n + 2 * t + h) * 4);
-                    f[n][h] = m == -INFINITY ? 0.f : ex2(m - top[n][h]);
-                    l_run[n][h] = fmaf(f[n][h], l, l_run[n][h]);
+                for (int i = 0; i < 2; ++i) {
+                    if (i == 1 && l1 < 0) break;
+#pragma unroll
+                    for (int h = 0; h < HS; ++h) {
+                        m[i][h] = ld_dsmem_f32(P[i] + (ROWS * D + 8 * n + 2 * t + h) * 4);
+                        l[i][h] = ld_dsmem_f32(P[i] + (ROWS * D + ROWS + 8 * n + 2 * t + h) * 4);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        if constexpr (R > 1) {
+                            a[i][mt] = ld_dsmem_f32x4(P[i] + slot(n, mt) * 4);
+                        } else {
+                            a[i][mt].x = ld_dsmem_f32(P[i] + slot(n, mt) * 4);
+                            a[i][mt].z = ld_dsmem_f32(P[i] + slot(n, mt) * 4 + 4);
+                            a[i][mt].y = a[i][mt].w = 0.f;
+                        }
+                    }
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if constexpr (R > 1) {
-                        a[n][mt] = ld_dsmem_f32x4(P + slot(n, mt) * 4);
-                    } else {
-                        a[n][mt].x = ld_dsmem_f32(P + slot(n, mt) * 4);
-                        a[n][mt].z = ld_dsmem_f32(P + slot(n, mt) * 4 + 4);
-                        a[n][mt].y = a[n][mt].w = 0.f;
+                for (int i = 0; i < 2; ++i) {
+                    if (i == 1 && l1 < 0) break;
+                    float f[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < HS; ++h) {
+                        f[h] = m[i][h] == -INFINITY ? 0.f : ex2(m[i][h] - top[n][h]);
+                        l_run[n][h] = fmaf(f[h], l[i][h], l_run[n][h]);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[n][mt][0] = fmaf(f[0], a[i][mt].x, acc[n][mt][0]);
+                        acc[n][mt][1] = fmaf(f[1], a[i][mt].y, acc[n][mt][1]);
+                        acc[n][mt][2] = fmaf(f[0], a[i][mt].z, acc[n][mt][2]);
+                        acc[n][mt][3] = fmaf(f[1], a[i][mt].w, acc[n][mt][3]);
                     }
                 }
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    acc[n][mt][0] = fmaf(f[n][0], a[n][mt].x, acc[n][mt][0]);
-                    acc[n][mt][1] = fmaf(f[n][1], a[n][mt].y, acc[n][mt][1]);
-                    acc[n][mt][2] = fmaf(f[n][0], a[n][mt].z, acc[n][mt][2]);
-                    acc[n][mt][3] = fmaf(f[n][1], a[n][mt].w, acc[n][mt][3]);
-                }
-        });
+        }
+    }
+    __device__ __forceinline__ void merge_end() {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -427,7 +427,7 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         const int a = p.query_start[s], b = p.query_start[s + 1];
         return a >= 0 && b >= a && b <= p.num_q_rows && b - a <= p.max_query_len && b - a <= L;
     };
-    int Bp = NT < 128 ? NT : 128;
+    int Bp = 32;
     while (Bp < B) Bp <<= 1;
     uint32_t *keys = reinterpret_cast<uint32_t *>(stages);           // [Bp]
     int *start = reinterpret_cast<int *>(stages + (size_t)Bp * 4);   // [B]
@@ -468,7 +468,8 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         if (warp == 0) {
             if (Bp == 256) warp_bitonic_sort<8>(keys, sort_tmp);
             else if (Bp == 128) warp_bitonic_sort<4>(keys, sort_tmp);
-            else warp_bitonic_sort<2>(keys, sort_tmp);
+            else if (Bp == 64) warp_bitonic_sort<2>(keys, sort_tmp);
+            else warp_bitonic_sort<1>(keys, sort_tmp);
         }
         __syncthreads();
         keys = sort_tmp;
@@ -581,27 +582,38 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
                                                     reinterpret_cast<long long *>(wtot), &tot);
     const int cum_q = (int)(ex & 0xffffffffLL), nz_before = (int)(ex >> 32);
     const int run = (int)(tot & 0xffffffffLL), nz = (int)(tot >> 32);
-    if (tid < nu) cum[tid] = cum_q;
+    // (units with blocks before unit q, for the cuts: in the sort scratch's place, which
+    // every thread is done with)
+    int *nzb = reinterpret_cast<int *>(stages);
+    if (tid < nu) {
+        cum[tid] = cum_q;
+        nzb[tid] = nz_before;
+    }
     if (tid == 0) {
         cum[nu] = run;
         bound[0] = 0;
         bound[NWC] = run;
     }
+    __syncthreads();
+    // cut g falls at floor(g * vtot / NWC), by thread g; the unit it falls in is the last
+    // one that starts at or before it (a unit without blocks starts with the next one)
     const long long vtot = 4LL * run + (long long)nz * UNIT_COST;
-    if (tid < nu && nb_q > 0) {
-        const long long vs = 4LL * cum_q + (long long)nz_before * UNIT_COST;
-        const long long ve = vs + 4LL * nb_q + UNIT_COST;
-        // cuts g with floor(g * vtot / NWC) in [vs, ve)
-        int g = (int)((vs * NWC + vtot - 1) / vtot);
-        const long long g_end = (ve * NWC + vtot - 1) / vtot;
-        if (g < 1) g = 1;
-        for (; g < g_end && g < NWC; ++g) {
-            const long long o = (long long)g * vtot / NWC - vs;
-            bound[g] = o < UNIT_COST ? cum_q : min(cum_q + nb_q, cum_q + (int)((o - UNIT_COST) / 4));
+    for (int g = 1 + tid; g < NWC; g += NT) {
+        const long long at = (NWC & (NWC - 1)) == 0 ? ((long long)g * vtot) >> (31 - __clz(NWC))
+                                                    : (long long)g * vtot / NWC;
+        int lo = 0, hi = nu - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (4LL * cum[mid] + (long long)nzb[mid] * UNIT_COST <= at) lo = mid; else hi = mid - 1;
         }
+        int cut = run;
+        if (nz > 0) {
+            const int c = cum[lo], e = cum[lo + 1];
+            const long long o = at - (4LL * c + (long long)nzb[lo] * UNIT_COST);
+            cut = o < UNIT_COST ? c : min(e, c + (int)((o - UNIT_COST) / 4));
+        }
+        bound[g] = cut;
     }
-    if (nz == 0)
-        for (int g = 1 + tid; g < NWC; g += NT) bound[g] = run;
     // the sort scratch in the stage region is overwritten by bulk copies next
     fence_proxy_async_smem();
     __syncthreads();
@@ -873,22 +885,48 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         }
     };
 
+    // The warps that hold unit ui: the first one, and how many of them have blocks
+    // (every lane takes 32nd of the warps).
+    auto span = [&](int ui, int &first, int &last, int &parts) {
+        const int f0 = cum[ui], f1 = cum[ui] + units[ui].nb - 1;
+        first = last = -1;
+        int held = 0;
+        for (int g0 = 0; g0 < NWC; g0 += 32) {
+            const int g = g0 + lane, lo = g < NWC ? bound[g] : INT32_MAX, hi = g < NWC ? bound[g + 1] : 0;
+            first += __popc(__ballot_sync(0xffffffffu, lo <= f0));
+            last += __popc(__ballot_sync(0xffffffffu, lo <= f1));
+            held += __popc(__ballot_sync(0xffffffffu, lo < hi && lo <= f1 && hi > f0));
+        }
+        parts = held;
+    };
+
     // Merge every partial of unit `ui` (in warp order) and write the unit's
     // result; run by the last of the unit's warps to arrive.
     auto merge_unit = [&](int ui) {
         const UnitRec u = units[ui];
-        const int g_first = owner(cum[ui]), g_last = owner(cum[ui] + u.nb - 1);
+        int g_first, g_last;
         if constexpr (F4) {
+            int parts;
+            span(ui, g_first, g_last, parts);
             set_rows(u);
-            wa.merge([&](auto &&f) {
-                for (int w = g_first; w <= g_last; ++w) {
-                    if (range_lo(w) == range_lo(w + 1)) continue;
-                    const float *pw = part_of(w, (w == g_last && w != g_first) ? 0 : 1);
-                    f(map_to_rank(pw, (uint32_t)(w / NW)));
+            // 32 partials at a time, each lane knowing where one of them is
+            wa.merge_begin();
+            for (int pass = 0; pass < 2; ++pass) {
+                for (int w0 = g_first; w0 <= g_last; w0 += 32) {
+                    const int w = w0 + lane;
+                    const bool here = w <= g_last && bound[min(w, NWC - 1)] < bound[min(w, NWC - 1) + 1];
+                    uint32_t at = 0;
+                    if (here) at = map_to_rank(part_of(w, (w == g_last && w != g_first) ? 0 : 1), (uint32_t)(w / NW));
+                    const unsigned which = __ballot_sync(0xffffffffu, here);
+                    if (pass == 0) wa.merge_levels(at, which);
+                    else wa.merge_add(at, which);
                 }
-            });
+            }
+            wa.merge_end();
             write_unit(u);
         } else {
+            g_first = owner(cum[ui]);
+            g_last = owner(cum[ui] + u.nb - 1);
             // Merge the unit's partials in warp order with a running maximum.
             // A lane owns chunks lane, lane + 32, ... (E outputs each), taken
             // CG at a time; all loads of one partial for those chunks are
@@ -1024,6 +1062,25 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
             return;
         }
         if (pending < 0 && shared_unit < 0) return;
+        if constexpr (F4) {
+            // as below, the spans found by the whole warp
+            int first_p = 0, parts_p = 0, first_u = 0, parts_u = 0, last;
+            if (pending >= 0) span(pending, first_p, last, parts_p);
+            if (shared_unit >= 0) span(shared_unit, first_u, last, parts_u);
+            int old = -1;
+            if (lane < 2) {
+                fence_acq_rel_cluster();           // the parked partials are visible first
+                const int unit = lane ? shared_unit : pending, g = lane ? first_u : first_p;
+                if (unit >= 0) old = atom_add_acq_rel_dsmem(map_to_rank(&arrive[g % NW], g / NW), 1);
+            }
+            const bool last_p = pending >= 0 && __shfl_sync(0xffffffffu, old, 0) == parts_p - 1;
+            const bool last_u = shared_unit >= 0 && __shfl_sync(0xffffffffu, old, 1) == parts_u - 1;
+            if (last_p || last_u) fence_acq_rel_cluster();
+            if (last_p) merge_unit(pending);
+            if (last_u) merge_unit(shared_unit);
+            pending = -1;
+            return;
+        }
         int old_p = 0, old_u = 0;
         if (lane == 0) {
             fence_acq_rel_cluster();               // the parked partials are visible first
