@@ -415,14 +415,24 @@ struct WarpAttnF4 {
 
     // The state becomes the merge of partials: merge_begin, merge_levels of all of
     // them, merge_add of all of them, merge_end.  Lane i of `which` gives where a partial
-    // lies in the cluster's shared memory; they are taken in the lanes' order, the loads
-    // of two (of four, for the levels) in flight.
+    // lies in shared memory (FAR: the cluster's); they are taken in the lanes' order, the
+    // loads of two (of four, for the levels) in flight.
+    template <bool FAR> __device__ __forceinline__ static float get(uint32_t at) {
+        if constexpr (FAR) return ld_dsmem_f32(at);
+        else return __uint_as_float(lds32(at));
+    }
+    template <bool FAR> __device__ __forceinline__ static float4 get4(uint32_t at) {
+        if constexpr (FAR) return ld_dsmem_f32x4(at);
+        const uint4 v = lds128(at);
+        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    }
     float top[NT][2];
     __device__ __forceinline__ void merge_begin() {
         reset();
 #pragma unroll
         for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
     }
+    template <bool FAR>
     __device__ __forceinline__ void merge_levels(uint32_t at, unsigned which) {
         while (which) {
             uint32_t P[4];
@@ -439,7 +449,7 @@ struct WarpAttnF4 {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int h = 0; h < HS; ++h) m[i][n][h] = ld_dsmem_f32(P[i] + (ROWS * D + 8 * n + 2 * t + h) * 4);
+                        for (int h = 0; h < HS; ++h) m[i][n][h] = get<FAR>(P[i] + (ROWS * D + 8 * n + 2 * t + h) * 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -449,6 +459,7 @@ struct WarpAttnF4 {
             }
         }
     }
+    template <bool FAR>
     __device__ __forceinline__ void merge_add(uint32_t at, unsigned which) {
         while (which) {
             const int l0 = __ffs(which) - 1;
@@ -468,16 +479,16 @@ struct WarpAttnF4 {
                     if (i == 1 && l1 < 0) break;
 #pragma unroll
                     for (int h = 0; h < HS; ++h) {
-                        m[i][h] = ld_dsmem_f32(P[i] + (ROWS * D + 8 * n + 2 * t + h) * 4);
-                        l[i][h] = ld_dsmem_f32(P[i] + (ROWS * D + ROWS + 8 * n + 2 * t + h) * 4);
+                        m[i][h] = get<FAR>(P[i] + (ROWS * D + 8 * n + 2 * t + h) * 4);
+                        l[i][h] = get<FAR>(P[i] + (ROWS * D + ROWS + 8 * n + 2 * t + h) * 4);
                     }
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         if constexpr (R > 1) {
-                            a[i][mt] = ld_dsmem_f32x4(P[i] + slot(n, mt) * 4);
+                            a[i][mt] = get4<FAR>(P[i] + slot(n, mt) * 4);
                         } else {
-                            a[i][mt].x = ld_dsmem_f32(P[i] + slot(n, mt) * 4);
-                            a[i][mt].z = ld_dsmem_f32(P[i] + slot(n, mt) * 4 + 4);
+                            a[i][mt].x = get<FAR>(P[i] + slot(n, mt) * 4);
+                            a[i][mt].z = get<FAR>(P[i] + slot(n, mt) * 4 + 4);
                             a[i][mt].y = a[i][mt].w = 0.f;
                         }
                     }

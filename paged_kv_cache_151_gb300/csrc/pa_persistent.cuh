@@ -583,8 +583,11 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
     const int cum_q = (int)(ex & 0xffffffffLL), nz_before = (int)(ex >> 32);
     const int run = (int)(tot & 0xffffffffLL), nz = (int)(tot >> 32);
     // (units with blocks before unit q, for the cuts: in the sort scratch's place, which
-    // every thread is done with)
+    // every thread is done with; the scan's scratch becomes E2M1's counters of a block's
+    // warps that are done with a unit, by the first of them)
     int *nzb = reinterpret_cast<int *>(stages);
+    int *arrive_here = wtot;
+    if (tid < NW) arrive_here[tid] = 0;
     if (tid < nu) {
         cum[tid] = cum_q;
         nzb[tid] = nz_before;
@@ -885,48 +888,87 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         }
     };
 
-    // The warps that hold unit ui: the first one, and how many of them have blocks
-    // (every lane takes 32nd of the warps).
-    auto span = [&](int ui, int &first, int &last, int &parts) {
-        const int f0 = cum[ui], f1 = cum[ui] + units[ui].nb - 1;
-        first = last = -1;
-        int held = 0;
-        for (int g0 = 0; g0 < NWC; g0 += 32) {
-            const int g = g0 + lane, lo = g < NWC ? bound[g] : INT32_MAX, hi = g < NWC ? bound[g + 1] : 0;
-            first += __popc(__ballot_sync(0xffffffffu, lo <= f0));
-            last += __popc(__ballot_sync(0xffffffffu, lo <= f1));
-            held += __popc(__ballot_sync(0xffffffffu, lo < hi && lo <= f1 && hi > f0));
+    // E2M1.  Which warps of block c hold parts of the stream's [f0, f1] (bits; all lanes).
+    static_assert(!F4 || NW <= 32, "a lane per warp");
+    auto holders = [&](int c, int f0, int f1) -> unsigned {
+        const int w = c * NW + (lane < NW ? lane : 0), lo = bound[w], hi = bound[w + 1];
+        return __ballot_sync(0xffffffffu, lane < NW && lo < hi && lo <= f1 && hi > f0);
+    };
+    // Warp g's partial of the unit that is [f0, f1] of the stream.
+    auto partial_at = [&](int g, int f0, int f1) -> float * {
+        return part_of(g, f0 < bound[g] && f1 < bound[g + 1] ? 0 : 1);
+    };
+    // A unit that several warps share, once this one has parked its partial: the last
+    // warp of a block to arrive merges the block's partials, and if the unit crosses
+    // blocks leaves the result in the place of the first of them, where the last
+    // block's finds it.  (Straight over all partials of a cluster, 16 through distributed
+    // shared memory took one warp 8400 clocks: a round trip there is 650.)
+    auto finish_shared = [&](int ui) {
+        if constexpr (F4) {
+        const UnitRec u = units[ui];
+        const int f0 = cum[ui], f1 = f0 + u.nb - 1;
+        const unsigned here = holders(rank, f0, f1);
+        const unsigned blocks = __ballot_sync(0xffffffffu, lane < C && bound[min(lane, C - 1) * NW] <= f1 &&
+                                                  bound[(min(lane, C - 1) + 1) * NW] > f0 &&
+                                                  bound[min(lane, C - 1) * NW] < bound[(min(lane, C - 1) + 1) * NW]);
+        const int first = __ffs(here) - 1;
+        __syncwarp();
+        if (here & (here - 1)) {
+            int old = 0;
+            if (lane == 0) {
+                __threadfence_block();             // the parked partial is visible first
+                old = atomicAdd(&arrive_here[first], 1);
+            }
+            if (__shfl_sync(0xffffffffu, old, 0) != __popc(here) - 1) return;
+            __threadfence_block();                 // and so are the others'
+            __syncwarp();
+            wa.merge_begin();
+            const uint32_t at = (here >> lane) & 1 ? smem_u32(partial_at(rank * NW + lane, f0, f1)) : 0u;
+            wa.template merge_levels<false>(at, here);
+            wa.template merge_add<false>(at, here);
+            wa.merge_end();
+            if (!(blocks & (blocks - 1))) {
+                set_rows(u);
+                write_unit(u);
+                wa.reset();
+                return;
+            }
+            __syncwarp();
+            wa.store_partial(partial_at(rank * NW + first, f0, f1));
+            wa.reset();
+            __syncwarp();
         }
-        parts = held;
+        const int c0 = __ffs(blocks) - 1;
+        const int starts = __ffs(holders(c0, f0, f1)) - 1;
+        int old = 0;
+        if (lane == 0) {
+            fence_acq_rel_cluster();
+            old = atom_add_acq_rel_dsmem(map_to_rank(&arrive[starts], (uint32_t)c0), 1);
+        }
+        if (__shfl_sync(0xffffffffu, old, 0) != __popc(blocks) - 1) return;
+        fence_acq_rel_cluster();
+        uint32_t at = 0;
+        if ((blocks >> lane) & 1) {
+            int w = lane == c0 ? c0 * NW + starts : lane * NW;     // its first warp with blocks
+            while (bound[w + 1] == bound[w]) ++w;
+            at = map_to_rank(partial_at(w, f0, f1), (uint32_t)lane);
+        }
+        wa.merge_begin();
+        wa.template merge_levels<true>(at, blocks);
+        wa.template merge_add<true>(at, blocks);
+        wa.merge_end();
+        set_rows(u);
+        write_unit(u);
+        wa.reset();
+        }
     };
 
     // Merge every partial of unit `ui` (in warp order) and write the unit's
     // result; run by the last of the unit's warps to arrive.
     auto merge_unit = [&](int ui) {
         const UnitRec u = units[ui];
-        int g_first, g_last;
-        if constexpr (F4) {
-            int parts;
-            span(ui, g_first, g_last, parts);
-            set_rows(u);
-            // 32 partials at a time, each lane knowing where one of them is
-            wa.merge_begin();
-            for (int pass = 0; pass < 2; ++pass) {
-                for (int w0 = g_first; w0 <= g_last; w0 += 32) {
-                    const int w = w0 + lane;
-                    const bool here = w <= g_last && bound[min(w, NWC - 1)] < bound[min(w, NWC - 1) + 1];
-                    uint32_t at = 0;
-                    if (here) at = map_to_rank(part_of(w, (w == g_last && w != g_first) ? 0 : 1), (uint32_t)(w / NW));
-                    const unsigned which = __ballot_sync(0xffffffffu, here);
-                    if (pass == 0) wa.merge_levels(at, which);
-                    else wa.merge_add(at, which);
-                }
-            }
-            wa.merge_end();
-            write_unit(u);
-        } else {
-            g_first = owner(cum[ui]);
-            g_last = owner(cum[ui] + u.nb - 1);
+        const int g_first = owner(cum[ui]), g_last = owner(cum[ui] + u.nb - 1);
+        {
             // Merge the unit's partials in warp order with a running maximum.
             // A lane owns chunks lane, lane + 32, ... (E outputs each), taken
             // CG at a time; all loads of one partial for those chunks are
@@ -1063,22 +1105,10 @@ decode_persistent_kernel(const __grid_constant__ DecodeParams p) {
         }
         if (pending < 0 && shared_unit < 0) return;
         if constexpr (F4) {
-            // as below, the spans found by the whole warp
-            int first_p = 0, parts_p = 0, first_u = 0, parts_u = 0, last;
-            if (pending >= 0) span(pending, first_p, last, parts_p);
-            if (shared_unit >= 0) span(shared_unit, first_u, last, parts_u);
-            int old = -1;
-            if (lane < 2) {
-                fence_acq_rel_cluster();           // the parked partials are visible first
-                const int unit = lane ? shared_unit : pending, g = lane ? first_u : first_p;
-                if (unit >= 0) old = atom_add_acq_rel_dsmem(map_to_rank(&arrive[g % NW], g / NW), 1);
-            }
-            const bool last_p = pending >= 0 && __shfl_sync(0xffffffffu, old, 0) == parts_p - 1;
-            const bool last_u = shared_unit >= 0 && __shfl_sync(0xffffffffu, old, 1) == parts_u - 1;
-            if (last_p || last_u) fence_acq_rel_cluster();
-            if (last_p) merge_unit(pending);
-            if (last_u) merge_unit(shared_unit);
+            const int p_unit = pending;
             pending = -1;
+            if (p_unit >= 0) finish_shared(p_unit);
+            if (shared_unit >= 0) finish_shared(shared_unit);
             return;
         }
         int old_p = 0, old_u = 0;
