@@ -111,6 +111,19 @@ cudaError_t run_split(const pa::DecodeParams &p, int dtype, int D, int G, dim3 g
 #define PA_F4_MULTI_CLUSTER 2
 #endif
 
+// Blocks of a cluster over E2M1 caches (eight warps a block; `per_sm` of them on an SM).
+// Two deal a batch's units evenly; where the units leave SMs idle, larger clusters share
+// each one's keys, if the tables are long enough to leave a warp eight blocks.  (One
+// sequence, 8 KV heads: over 4000 keys 20 us with two blocks and 15 with eight, over 64000
+// 179, 54 with eight and 45 with sixteen; over 2000 14.5 either way.)
+int f4_cluster(long long units, int32_t max_blocks, int base, int per_sm, int most) {
+    int sms = pa::sm_count_of_current_device();
+    if (sms <= 0) sms = 152;
+    int c = base;
+    while (c < most && units * c * 2 <= (long long)per_sm * sms && max_blocks >= 64 * c) c *= 2;
+    return c;
+}
+
 cudaError_t run_persistent(const pa::DecodeParams &p, int dtype, int D, int G, bool partial,
                            long long unit_bound, cudaStream_t st) {
     const int cluster = partial ? 1 : PA_DECODE_CLUSTER;
@@ -615,7 +628,7 @@ int decode_codes_common(int32_t kv_dtype, void *out, const void *q, const void *
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int G = num_heads / num_kv_heads;
     const bool f4 = kv_dtype == PA_E2M1;
-    const int cluster = partial ? 1 : f4 ? PA_F4_CLUSTER : PA_F8_CLUSTER;
+    const int cluster = partial ? 1 : f4 ? f4_cluster(unit_bound, max_blocks_per_seq, PA_F4_CLUSTER, 2, 16) : PA_F8_CLUSTER;
     cudaError_t e;
     if (f4)
         e = dtype == PA_BF16 ? pa::decode_fp4_bf16(p, head_dim, G, partial, unit_bound, cluster, st)
@@ -728,9 +741,10 @@ int decode_multi_codes(
         if (e != cudaSuccess) return PA_ERR_CUDA;
     }
     const long long unit_bound = (long long)num_seqs * num_kv_heads * ((small_rows + 15) / 16);
+    const int f4c = f4_cluster(unit_bound, max_blocks_per_seq, PA_F4_MULTI_CLUSTER, 1, 8);
     const cudaError_t e =
-        f4 ? (dtype == PA_BF16 ? pa::decode_multi_fp4_bf16(p, head_dim, G, unit_bound, PA_F4_MULTI_CLUSTER, st)
-                               : pa::decode_multi_fp4_f16(p, head_dim, G, unit_bound, PA_F4_MULTI_CLUSTER, st))
+        f4 ? (dtype == PA_BF16 ? pa::decode_multi_fp4_bf16(p, head_dim, G, unit_bound, f4c, st)
+                               : pa::decode_multi_fp4_f16(p, head_dim, G, unit_bound, f4c, st))
            : (dtype == PA_BF16 ? pa::decode_multi_fp8_bf16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st)
                                : pa::decode_multi_fp8_f16(p, head_dim, G, unit_bound, PA_MULTI_CLUSTER, st));
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;

@@ -374,3 +374,12 @@ def test_offsets_past_32_bits(cuda_lib):
     # (2^-4) bound an element's error by a third of the group's largest
     big16 = x.float().unflatten(-1, (-1, 16)).abs().amax(-1, keepdim=True)
     assert ((y.float() - x.float()).unflatten(-1, (-1, 16)).abs() <= big16 / 3).all()
+
+
+@pytest.mark.parametrize("lens,n", [([3000], [1]), ([9000, 5], [1, 1]), ([20000], [1]), ([70000], [1]),
+                                    ([4100], [4]), ([9000, 40, 2500], [3, 1, 8]), ([30000], [7])])
+def test_few_long_sequences_over_large_clusters(cuda_lib, lens, n):
+    """Few units and long tables: clusters of up to 16 blocks share a unit's keys."""
+    for H, Hkv, D in ((8, 2, 128), (8, 1, 64), (4, 4, 128)):
+        b = Batch(lens[0] + D, lens, n, H, Hkv, D, "bf16")
+        b.check(b.decode(cuda_lib) if max(n) == 1 else b.multi(cuda_lib))
