@@ -131,8 +131,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_logits_kernel(const __g
     const int v0 = rank * run - lead, v1 = min(V, v0 + run);
     const uint32_t *mask = p.allowed ? p.allowed + (int64_t)r * p.allowed_stride : nullptr;
 
-    // The logits first: they are on their way while the sequence and its history are
-    // looked up.  The tile at t0: quad i NT + tid of it (-inf outside the row).
+    // The tile at t0: quad i NT + tid of it (-inf outside the row).
     constexpr bool NARROW = sizeof(T) == 2;     // widened only when the rest is here
     Quad<T> raw[NARROW ? Q : 1];
     float x[EPT];
@@ -155,8 +154,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_logits_kernel(const __g
     };
     // the tile's words of the mask are here once the block has met behind this
     auto words_here = [&]() { asm volatile("cp.async.wait_all;" ::: "memory"); };
-    load(v0, min(v1, v0 + TILE));
-
     const int s = sequence_of(p.query_start, p.num_seqs, r, lane);
     if (s < 0) return;                                      // the whole cluster: no such row
     if (C > 1) cluster_arrive();                            // this block runs (see cluster_wait below)
@@ -174,6 +171,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_logits_kernel(const __g
         b0 = p.bias_start[s];
         b1 = p.bias_start[s + 1];
     }
+    // The logits behind these few words (in front of them they hold them up, as the memory
+    // answers in order: 3 us of a block's 14), and on their way while the history is
+    // counted.
+    load(v0, min(v1, v0 + TILE));
     if (len < 0 || len > p.history_stride || asked < 0 || asked > len) {
         if (rank == 0 && tid == 0) set_error(p.err, ERR_SEQ_LEN);
         len = max(0, (int)min((int64_t)len, p.history_stride));
