@@ -10,6 +10,7 @@ if that is impossible the call fails loudly -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -19,6 +20,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_tensors = None                    # the compiled checks of tensors (binding/tensors.cpp)
 
 PA_F32, PA_BF16, PA_F16, PA_E4M3, PA_E2M1 = 0, 1, 2, 3, 4
 _DTYPE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float16: PA_F16}
@@ -44,10 +46,15 @@ def library_path() -> str:
 
 def load():
     """Load ``libpa.so`` (building it first if it is absent)."""
-    global _lib
+    global _lib, _tensors
     with _lock:
         if _lib is not None:
             return _lib
+        if _tensors is None:
+            at = _build.build_tensors()
+            found = importlib.util.spec_from_file_location("_tensors", at)
+            _tensors = importlib.util.module_from_spec(found)
+            found.loader.exec_module(_tensors)
         path = _build.LIB_PATH
         if not os.path.exists(path):
             path = _build.build()
@@ -160,19 +167,30 @@ def _stream(stream=None):
 # the current stream's handle without building a stream object where torch
 # offers that.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device_now():
+    """The current device; -1 where there is none (no tensor is on it then)."""
+    try:
+        return _get_device()
+    except RuntimeError:
+        return -1
 
 
 def _here(names, tensors):
     """The current device, on which every tensor has to be."""
     try:
-        devs = {t.get_device() for t in tensors}
+        dev = tensors[0].get_device()
+        if dev >= 0 and dev == _device_now():
+            for t in tensors:
+                if t.get_device() != dev:
+                    break
+            else:
+                return dev
     except AttributeError:
-        devs = ()
-    if len(devs) == 1:
-        dev = devs.pop()
-        if dev >= 0 and dev == torch.cuda.current_device():
-            return dev
-    for n, t in zip(names.split(), tensors):
+        pass
+    for n, t in zip(names.split() if isinstance(names, str) else names, tensors):
         _dev(t, n)
     raise ValueError("tensors are not on the current device")
 
@@ -664,13 +682,13 @@ def pa_decode_partitioned_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_
     _check("pa_decode_partitioned_fp8", rc)
 
 
-def _decode_multi_codes(fn, caches, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                        seq_lens, query_start, max_query_len, scale, num_kv_heads, stream):
-    """Multi-token attention over caches of codes: checks, and the call of ``fn``;
-    ``caches`` checks the caches and gives their dimensions."""
+def pa_decode_multi_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                        query_start, max_query_len, scale, num_kv_heads, stream=None):
+    """pa_decode_multi over E4M3 caches: several new tokens per sequence, causal
+    among themselves."""
     dev = _here("out q k_cache v_cache k_scale v_scale block_tables seq_lens query_start",
                 (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, query_start))
-    N, Hkv, bs, D = caches(k_cache, v_cache, k_scale, v_scale)
+    N, Hkv, bs, D = _fp8_caches(k_cache, v_cache, k_scale, v_scale)
     if num_kv_heads != Hkv:
         raise ValueError("num_kv_heads does not match the cache")
     shape, st = q.shape, q.stride()
@@ -692,158 +710,113 @@ def _decode_multi_codes(fn, caches, out, q, k_cache, v_cache, k_scale, v_scale, 
     if query_start.dtype is not i32 or query_start.shape != (B + 1,) or \
             not query_start.is_contiguous():
         raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
-    rc = fn(
+    rc = (_lib or load()).pa_decode_multi_fp8(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
         query_start.data_ptr(), B, shape[0], max_query_len, shape[1], Hkv, D, N, bs, tables[1],
         st[0], scale, _DTYPE[dt], _stream_of(stream, dev))
     if rc:
-        raise PAError(fn.__name__, rc)
+        raise PAError("pa_decode_multi_fp8", rc)
 
 
-def pa_decode_multi_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
-                        query_start, max_query_len, scale, num_kv_heads, stream=None):
-    """pa_decode_multi over E4M3 caches: several new tokens per sequence, causal
-    among themselves."""
-    _decode_multi_codes((_lib or load()).pa_decode_multi_fp8, _fp8_caches, out, q, k_cache, v_cache,
-                        k_scale, v_scale, block_tables, seq_lens, query_start, max_query_len, scale,
-                        num_kv_heads, stream)
+# ---- calls whose tensors are checked by the compiled binding ----------------
+#
+# A description of a call's tensors is checked in one call (binding/tensors.cpp), which
+# gives their addresses, sizes, row distances and type codes.
+
+_specs = {}
+
+
+def _spec(name, text):
+    """The check of ``name``'s tensors, made when it is first called."""
+    s = _specs.get(name)
+    if s is None:
+        load()
+        s = _specs[name] = _tensors.Spec(text)
+    return s
 
 
 # ---- FP4 (E2M1) cache ------------------------------------------------------
 
-def _fp4_caches(k_cache, v_cache, k_scale, v_scale):
-    """(num_blocks, num_kv_heads, block size, head_dim) of E2M1 caches, checked
-    together with their scales (not their device)."""
-    shape = k_cache.shape
-    if len(shape) != 4 or shape != v_cache.shape or shape[2] != 9:
-        raise ValueError("FP4 caches must both be [num_blocks, num_kv_heads, 9, head_dim]")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("caches must be contiguous")
-    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
-        raise ValueError("FP4 caches hold codes and scales as bytes (uint8 tensors)")
-    Hkv = shape[1]
-    if k_scale.dtype is not torch.float32 or k_scale.shape != (Hkv,) or \
-            not k_scale.is_contiguous():
-        raise ValueError("k_scale must be a contiguous float32 [num_kv_heads]")
-    if v_scale.dtype is not torch.float32 or v_scale.shape != (Hkv,) or \
-            not v_scale.is_contiguous():
-        raise ValueError("v_scale must be a contiguous float32 [num_kv_heads]")
-    return shape[0], Hkv, 16, shape[3]
-
-
-def _fp4_rows(fn, names, k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream):
-    kn, vn = names
-    dev = _here(f"{kn} {vn} k_cache v_cache k_scale v_scale slot_mapping",
-                (k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping))
-    N, Hkv, bs, D = _fp4_caches(k_cache, v_cache, k_scale, v_scale)
-    shape, code = k.shape, _DTYPE.get(k.dtype)
-    if len(shape) != 3 or shape != v.shape or shape[1] != Hkv or shape[2] != D:
-        raise ValueError(f"{kn} and {vn} must be [num_tokens, num_kv_heads, head_dim]")
-    if code is None or v.dtype is not k.dtype:
-        raise ValueError(f"{kn} and {vn} must share a dtype in {{float32, bfloat16, float16}}")
-    T = shape[0]
-    k_st, v_st = _heads(k, kn, D), _heads(v, vn, D)
-    if T <= 1:                 # a single token's stride is never used
-        k_st = v_st = Hkv * D
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,) or \
-            not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be a contiguous int64 [num_tokens]")
-    rc = fn(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D, k_st, v_st, N, bs, code,
-            _stream_of(stream, dev))
-    if rc:
-        raise PAError(fn.__name__, rc)
+_FP4 = "k_cache:u8[N,K,9,D] v_cache:u8[N,K,9,D] k_scale:f32[K] v_scale:f32[K]"
+_WRITE4 = f"k:T[T,K,D]~ v:T[T,K,D]~ {_FP4} slot_mapping:i64[T]"
+_GATHER4 = f"k_out:T[T,K,D]~ v_out:T[T,K,D]~ {_FP4} slot_mapping:i64[T]"
+_DECODE4 = f"out:H[B,Q,D] q:H[B,Q,D]~ {_FP4} block_tables:i32[B,W] seq_lens:i32[B]"
+_PARTS4 = _DECODE4 + " workspace:u8[S]"
+_MULTI4 = (f"out:H[R,Q,D] q:H[R,Q,D]~ {_FP4} block_tables:i32[B,W] seq_lens:i32[B] "
+           "query_start:i32[B+1]")
 
 
 def pa_reshape_and_cache_fp4(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, stream=None):
     """Write k[t], v[t] ([T, H_kv, D] in f32/bf16/f16) into E2M1 caches (uint8
     [num_blocks, H_kv, 9, D]: the codes of 16 rows, then their scales)."""
-    _fp4_rows((_lib or load()).pa_reshape_and_cache_fp4, ("k", "v"), k, v, k_cache, v_cache,
-              k_scale, v_scale, slot_mapping, stream)
+    dev = _device_now()
+    *p, T, K, D, N, k_st, v_st, code = _spec(
+        "write4", _WRITE4)(
+        dev, k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping)
+    rc = _lib.pa_reshape_and_cache_fp4(*p, T, K, D, k_st, v_st, N, 16, code, _stream_of(stream, dev))
+    if rc:
+        raise PAError("pa_reshape_and_cache_fp4", rc)
 
 
 def pa_gather_cache_fp4(k_out, v_out, k_cache, v_cache, k_scale, v_scale, slot_mapping,
                         stream=None):
     """The rows of E2M1 caches at the given slots, as values: k_out[t] and v_out[t]
     ([T, H_kv, D] in f32/bf16/f16) for slot_mapping[t] >= 0."""
-    _fp4_rows((_lib or load()).pa_gather_cache_fp4, ("k_out", "v_out"), k_out, v_out, k_cache,
-              v_cache, k_scale, v_scale, slot_mapping, stream)
-
-
-def _decode_fp4(fn, extra, names, tensors, out, q, k_cache, v_cache, k_scale, v_scale,
-                block_tables, seq_lens, scale, num_kv_heads, stream):
-    """Decode over E2M1 caches: checks, and the call of ``fn`` with the arguments
-    ``extra`` of its form."""
-    dev = _here("out q k_cache v_cache k_scale v_scale block_tables seq_lens" + names,
-                (out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, *tensors))
-    N, Hkv, bs, D = _fp4_caches(k_cache, v_cache, k_scale, v_scale)
-    if num_kv_heads != Hkv:
-        raise ValueError("num_kv_heads does not match the cache")
-    shape, st, dt = q.shape, q.stride(), q.dtype
-    if len(shape) != 3 or shape[2] != D or st[2] != 1 or st[1] != D:
-        raise ValueError("q must be [num_seqs, num_heads, head_dim] with contiguous heads")
-    if out.shape != shape or not out.is_contiguous() or out.dtype is not dt:
-        raise ValueError("out must be a contiguous tensor shaped and typed like q")
-    if dt is not torch.bfloat16 and dt is not torch.float16:
-        raise ValueError("q must be bfloat16 or float16")
-    B, i32 = shape[0], torch.int32
-    tables = block_tables.shape
-    if block_tables.dtype is not i32 or len(tables) != 2 or tables[0] != B or \
-            not block_tables.is_contiguous():
-        raise ValueError("block_tables must be a contiguous int32 [num_seqs, max_blocks]")
-    if seq_lens.dtype is not i32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous():
-        raise ValueError("seq_lens must be a contiguous int32 [num_seqs]")
-    rc = fn(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            B, shape[1], Hkv, D, N, bs, tables[1], st[0], scale, _DTYPE[dt], *extra,
-            _stream_of(stream, dev))
+    dev = _device_now()
+    *p, T, K, D, N, k_st, v_st, code = _spec(
+        "gather4", _GATHER4)(
+        dev, k_out, v_out, k_cache, v_cache, k_scale, v_scale, slot_mapping)
+    rc = _lib.pa_gather_cache_fp4(*p, T, K, D, k_st, v_st, N, 16, code, _stream_of(stream, dev))
     if rc:
-        raise PAError(fn.__name__, rc)
+        raise PAError("pa_gather_cache_fp4", rc)
 
 
 def pa_decode_fp4(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
                   num_kv_heads, stream=None):
     """Decode-step paged attention over E2M1 caches into ``out``."""
-    _decode_fp4((_lib or load()).pa_decode_fp4, (), "", (), out, q, k_cache, v_cache, k_scale,
-                v_scale, block_tables, seq_lens, scale, num_kv_heads, stream)
+    dev = _device_now()
+    *p, B, Q, D, N, K, W, q_st, code = _spec("decode4", _DECODE4)(
+        dev, out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens)
+    if num_kv_heads != K:
+        raise ValueError("num_kv_heads does not match the cache")
+    rc = _lib.pa_decode_fp4(*p, B, Q, K, D, N, 16, W, q_st, scale, code, _stream_of(stream, dev))
+    if rc:
+        raise PAError("pa_decode_fp4", rc)
 
 
 def pa_decode_partitioned_fp4(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
                               scale, num_kv_heads, partition_size, max_seq_len, workspace,
                               stream=None):
-    """Split-KV decode over E2M1 caches (workspace as pa_decode_partitioned)."""
-    if not isinstance(workspace, torch.Tensor):
-        raise TypeError("workspace must be a torch.Tensor")
-    extra = (partition_size, max_seq_len, workspace.data_ptr(),
-             workspace.numel() * workspace.element_size())
-    _decode_fp4((_lib or load()).pa_decode_partitioned_fp4, extra, " workspace", (workspace,), out,
-                q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale, num_kv_heads,
-                stream)
+    """Split-KV decode over E2M1 caches (workspace as pa_decode_partitioned, uint8)."""
+    dev = _device_now()
+    *p, ws, B, Q, D, N, K, W, S, q_st, code = _spec("parts4", _PARTS4)(
+        dev, out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, workspace)
+    if num_kv_heads != K:
+        raise ValueError("num_kv_heads does not match the cache")
+    rc = _lib.pa_decode_partitioned_fp4(*p, B, Q, K, D, N, 16, W, q_st, scale, code,
+                                        partition_size, max_seq_len, ws, S, _stream_of(stream, dev))
+    if rc:
+        raise PAError("pa_decode_partitioned_fp4", rc)
 
 
 def pa_decode_multi_fp4(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
                         query_start, max_query_len, scale, num_kv_heads, stream=None):
     """pa_decode_multi over E2M1 caches: several new tokens per sequence, causal
     among themselves."""
-    _decode_multi_codes((_lib or load()).pa_decode_multi_fp4, _fp4_caches, out, q, k_cache, v_cache,
-                        k_scale, v_scale, block_tables, seq_lens, query_start, max_query_len, scale,
-                        num_kv_heads, stream)
+    dev = _device_now()
+    *p, R, Q, D, N, K, B, W, q_st, code = _spec(
+        "multi4", _MULTI4)(
+        dev, out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, query_start)
+    if num_kv_heads != K:
+        raise ValueError("num_kv_heads does not match the cache")
+    rc = _lib.pa_decode_multi_fp4(*p, B, R, max_query_len, Q, K, D, N, 16, W, q_st, scale, code,
+                                  _stream_of(stream, dev))
+    if rc:
+        raise PAError("pa_decode_multi_fp4", rc)
 
 
 # ---- maps of a step, built on the device -----------------------------------
-
-def _ints(t, name, shape):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 {list(shape)}")
-    return t.data_ptr()
-
-
-def _table(t, name):
-    if t.dtype is not torch.int32 or t.dim() != 2 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous 2-D int32 tensor")
-    return t.shape
-
 
 def pa_build_step(block_tables, seq_lens, query_start, positions, slot_mapping, request_tables,
                   request_blocks, request_ids, context_lens, new_lens, free_blocks, free_count,
@@ -855,33 +828,17 @@ def pa_build_step(block_tables, seq_lens, query_start, positions, slot_mapping, 
     [R, width], ``request_blocks`` [R]) grow from the end of the first
     ``free_count`` ([1]) entries of ``free_blocks`` (None for both: tables are
     complete).  A sequence that cannot be served has seq_len 0 and slots -1."""
-    none = context_lens
-    dev = _here("context_lens block_tables seq_lens query_start positions slot_mapping "
-                "request_tables request_blocks request_ids new_lens free_blocks free_count",
-                (context_lens, block_tables, seq_lens, query_start, positions, slot_mapping,
-                 request_tables, request_blocks, none if request_ids is None else request_ids,
-                 none if new_lens is None else new_lens,
-                 none if free_blocks is None else free_blocks,
-                 none if free_count is None else free_count))
-    B, W = _table(block_tables, "block_tables")
-    R, RW = _table(request_tables, "request_tables")
-    T, i64 = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1, torch.int64
-    for t, n in ((positions, "positions"), (slot_mapping, "slot_mapping")):
-        if t.dtype is not i64 or t.shape != (T,) or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous int64 [num_rows]")
     if (free_blocks is None) != (free_count is None):
         raise ValueError("free_blocks and free_count come together")
-    F = 0 if free_blocks is None else free_blocks.numel()
-    rc = (_lib or load()).pa_build_step(
-        block_tables.data_ptr(), _ints(seq_lens, "seq_lens", (B,)),
-        _ints(query_start, "query_start", (B + 1,)), positions.data_ptr(), slot_mapping.data_ptr(),
-        request_tables.data_ptr(), _ints(request_blocks, "request_blocks", (R,)),
-        None if request_ids is None else _ints(request_ids, "request_ids", (B,)),
-        _ints(context_lens, "context_lens", (B,)),
-        None if new_lens is None else _ints(new_lens, "new_lens", (B,)),
-        None if free_blocks is None else _ints(free_blocks, "free_blocks", (F,)),
-        None if free_count is None else _ints(free_count, "free_count", (1,)),
-        B, R, W, RW, T, F, num_blocks, 16, _stream_of(stream, dev))
+    dev = _device_now()
+    *p, B, W, T, R, V, F = _spec(
+        "build", "block_tables:i32[B,W] seq_lens:i32[B] query_start:i32[B+1] positions:i64[T] "
+                 "slot_mapping:i64[T] request_tables:i32[R,V] request_blocks:i32[R] "
+                 "request_ids:i32[B]? context_lens:i32[B] new_lens:i32[B]? free_blocks:i32[F]? "
+                 "free_count:i32[1]?")(
+        dev, block_tables, seq_lens, query_start, positions, slot_mapping, request_tables,
+        request_blocks, request_ids, context_lens, new_lens, free_blocks, free_count)
+    rc = _lib.pa_build_step(*p, B, R, W, V, T, F, num_blocks, 16, _stream_of(stream, dev))
     if rc:
         raise PAError("pa_build_step", rc)
 
@@ -890,18 +847,12 @@ def pa_trim_blocks(request_tables, request_blocks, request_ids, keep_lens, free_
                    stream=None):
     """Blocks of the requests ``request_ids`` (int32 [B]; None: request s) past
     ``keep_lens`` ([B]) tokens go back to the end of the free list."""
-    dev = _here("keep_lens request_tables request_blocks free_blocks free_count request_ids",
-                (keep_lens, request_tables, request_blocks, free_blocks, free_count,
-                 keep_lens if request_ids is None else request_ids))
-    R, RW = _table(request_tables, "request_tables")
-    if keep_lens.dim() != 1:
-        raise ValueError("keep_lens must be a contiguous int32 [num_seqs]")
-    B, F = keep_lens.shape[0], free_blocks.numel()
-    rc = (_lib or load()).pa_trim_blocks(
-        request_tables.data_ptr(), _ints(request_blocks, "request_blocks", (R,)),
-        None if request_ids is None else _ints(request_ids, "request_ids", (B,)),
-        _ints(keep_lens, "keep_lens", (B,)), _ints(free_blocks, "free_blocks", (F,)),
-        _ints(free_count, "free_count", (1,)), B, R, RW, F, 16, _stream_of(stream, dev))
+    dev = _device_now()
+    *p, R, V, B, F = _spec(
+        "trim", "request_tables:i32[R,V] request_blocks:i32[R] request_ids:i32[B]? "
+                "keep_lens:i32[B] free_blocks:i32[F] free_count:i32[1]")(
+        dev, request_tables, request_blocks, request_ids, keep_lens, free_blocks, free_count)
+    rc = _lib.pa_trim_blocks(*p, B, R, V, F, 16, _stream_of(stream, dev))
     if rc:
         raise PAError("pa_trim_blocks", rc)
 
@@ -922,68 +873,20 @@ def pa_process_logits(out, logits, query_start, tokens=None, history=None, promp
     ``bias_tokens`` and ``bias_values`` hold sequence s's biases at bias_start[s] ..
     bias_start[s+1]-1; bit v % 32 of ``allowed`` (int32 [T, ceil(V / 32)]) at v / 32
     allows token v."""
-    given = [logits if t is None else t
-             for t in (tokens, history, prompt_lens, history_lens, repetition, frequency, presence,
-                       bias_start, bias_tokens, bias_values, allowed, temperature)]
-    dev = _here("logits out query_start tokens history prompt_lens history_lens repetition "
-                "frequency presence bias_start bias_tokens bias_values allowed temperature",
-                (logits, out, query_start, *given))
-    shape, dt = logits.shape, logits.dtype
-    code, out_code = _DTYPE.get(dt), _DTYPE.get(out.dtype)
-    if code is None or len(shape) != 2:
-        raise ValueError("logits must be [num_rows, vocab] in {float32, bfloat16, float16}")
-    if out.shape != shape or (out.dtype is not dt and out.dtype is not torch.float32):
-        raise ValueError("out must be shaped like logits, in float32 or logits' dtype")
-    T, V = shape
-    l_st, one = logits.stride()
-    o_st, o_one = out.stride()
-    if (one != 1 or o_one != 1) and V > 1 and T:
-        raise ValueError("logits and out must have contiguous rows")
-    if T <= 1:                 # a single row's stride is never used
-        l_st = o_st = V
-    i32, f32 = torch.int32, torch.float32
-    if query_start.dtype is not i32 or query_start.dim() != 1 or not query_start.is_contiguous() or             not query_start.shape[0]:
-        raise ValueError("query_start must be a contiguous int32 [num_seqs + 1]")
-    B = query_start.shape[0] - 1
-    tok = None if tokens is None else _ints(tokens, "tokens", (T,))
-    hist = pl = hl = None
-    h_st = 0
-    if history is not None:
-        if history.dtype is not i32 or history.dim() != 2 or history.shape[0] != B or                 not history.is_contiguous():
-            raise ValueError("history must be a contiguous int32 [num_seqs, length]")
-        if history_lens is None:
-            raise ValueError("a history needs history_lens")
-        hist, h_st, hl = history.data_ptr(), history.shape[1], _ints(history_lens, "history_lens", (B,))
-        pl = None if prompt_lens is None else _ints(prompt_lens, "prompt_lens", (B,))
-    ptrs = []
-    for t, n in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence"),
-                 (temperature, "temperature")):
-        if t is None:
-            ptrs.append(None)
-            continue
-        if t.dtype is not f32 or t.shape != (B,) or not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous float32 [num_seqs]")
-        ptrs.append(t.data_ptr())
-    bs = bt = bv = None
-    n_bias = 0
-    if bias_start is not None:
-        if bias_tokens is None or bias_values is None:
-            raise ValueError("bias_start, bias_tokens and bias_values come together")
-        n_bias = bias_tokens.numel()
-        if bias_values.dtype is not f32 or bias_values.shape != (n_bias,) or                 not bias_values.is_contiguous():
-            raise ValueError("bias_values must be a contiguous float32 like bias_tokens")
-        bs, bt = _ints(bias_start, "bias_start", (B + 1,)), _ints(bias_tokens, "bias_tokens", (n_bias,))
-        bv = bias_values.data_ptr()
-    mask, m_st = None, 0
-    if allowed is not None:
-        if allowed.dtype is not i32 or allowed.dim() != 2 or allowed.shape[0] != T or \
-                not allowed.is_contiguous():
-            raise ValueError("allowed must be a contiguous int32 [num_rows, ceil(vocab / 32)]")
-        mask, m_st = allowed.data_ptr(), allowed.shape[1]
-    rc = (_lib or load()).pa_process_logits(
-        out.data_ptr(), logits.data_ptr(), query_start.data_ptr(), tok, hist, pl, hl, ptrs[0],
-        ptrs[1], ptrs[2], bs, bt, bv, mask, ptrs[3], B, T, V, l_st, o_st, h_st, m_st, n_bias,
-        1 if probs else 0, code, out_code, _stream_of(stream, dev))
+    if history is not None and history_lens is None:
+        raise ValueError("a history needs history_lens")
+    if bias_start is not None and (bias_tokens is None or bias_values is None):
+        raise ValueError("bias_start, bias_tokens and bias_values come together")
+    dev = _device_now()
+    *p, T, V, B, L, E, M, o_st, l_st, code, out_code = _spec(
+        "logits", "out:O[T,V]~ logits:T[T,V]~ query_start:i32[B+1] tokens:i32[T]? history:i32[B,L]? "
+                  "prompt_lens:i32[B]? history_lens:i32[B]? repetition:f32[B]? frequency:f32[B]? "
+                  "presence:f32[B]? bias_start:i32[B+1]? bias_tokens:i32[E]? bias_values:f32[E]? "
+                  "allowed:i32[T,M]? temperature:f32[B]?")(
+        dev, out, logits, query_start, tokens, history, prompt_lens, history_lens, repetition,
+        frequency, presence, bias_start, bias_tokens, bias_values, allowed, temperature)
+    rc = _lib.pa_process_logits(*p, B, T, V, l_st, o_st, L, M, E, 1 if probs else 0, code, out_code,
+                                _stream_of(stream, dev))
     if rc:
         raise PAError("pa_process_logits", rc)
 
