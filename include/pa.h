@@ -542,7 +542,8 @@ int pa_decode_multi_fp8(void *out, const void *q, const void *k_cache,
  * quotient rounded to binary32 and then to nearest, ties to even, saturating at 448;
  * code = E2M1(y / scale), likewise, saturating at 6.  A scale of 0 (max |y| at most
  * 6 * 2^-10) has codes of 0; an infinite y is 6 * 448; a NaN makes its group NaN.
- * Requirements as pa_reshape_and_cache_fp8, and head_dim <= 1024.
+ * Requirements as pa_reshape_and_cache_fp8, and head_dim <= 1024; of two tokens with
+ * the same slot a group may get the codes of one and the scale of the other.
  *
  * pa_gather_cache_fp4 -- the rows at the given slots as values: k_out[t] and
  * v_out[t] ([num_tokens, num_kv_heads, head_dim] of `dtype`, strides as for k and
@@ -640,8 +641,10 @@ int pa_decode_multi_fp4(void *out, const void *q, const void *k_cache,
  * bounds -- context + new past 16 * the narrower table, rows past num_rows -- with
  * PA_DEVERR_SEQ_LEN (query_start stays within num_rows).  A table entry outside
  * [0, num_blocks) gives slot -1 and PA_DEVERR_BLOCK_ID, a free_count outside [0,
- * free_capacity] the latter too.  A request named twice in a step has undefined
- * contents.  num_seqs <= 65535.  Calls on one state must be ordered by the caller.
+ * free_capacity] the latter too.  A request id of -1 pads the batch: it is not served,
+ * and nothing is flagged.  With a request named twice no sequence is served
+ * (PA_DEVERR_SEQ_LEN).  num_seqs <= 65535, and num_requests <= 2^19 with request_ids.
+ * Calls on one state must be ordered by the caller.
  */
 int pa_build_step(int32_t *block_tables, int32_t *seq_lens, int32_t *query_start,
                   int64_t *positions, int64_t *slot_mapping,
@@ -660,8 +663,9 @@ int pa_build_step(int32_t *block_tables, int32_t *seq_lens, int32_t *query_start
  * put behind the first free_count[0] entries of free_blocks so that the first
  * sequence's first one is taken next -- a step built and trimmed to its context
  * leaves the list as it was -- and request_blocks and free_count follow.  A bad id or
- * length changes nothing of its request (PA_DEVERR_SEQ_LEN); if the blocks do not
- * fit into free_capacity nothing changes at all (PA_DEVERR_BLOCK_ID).
+ * length changes nothing of its request (PA_DEVERR_SEQ_LEN; an id of -1 pads, without
+ * it); if a request is named twice (PA_DEVERR_SEQ_LEN) or the blocks do not fit into
+ * free_capacity (PA_DEVERR_BLOCK_ID) nothing changes at all.
  */
 int pa_trim_blocks(const int32_t *request_tables, int32_t *request_blocks,
                    const int32_t *request_ids, const int32_t *keep_lens,

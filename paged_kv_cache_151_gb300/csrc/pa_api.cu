@@ -891,7 +891,8 @@ int pa_build_step(int32_t *block_tables, int32_t *seq_lens, int32_t *query_start
         return PA_ERR_INVALID_ARG;
     if (block_size != 16) return PA_ERR_UNSUPPORTED;
     if (num_seqs > 65535 || num_blocks > (int64_t)INT32_MAX || num_rows > (int64_t)INT32_MAX ||
-        free_capacity > (int64_t)INT32_MAX || max_blocks_per_seq > (1 << 26) || request_width > (1 << 26))
+        free_capacity > (int64_t)INT32_MAX || max_blocks_per_seq > (1 << 26) || request_width > (1 << 26) ||
+        (request_ids && num_requests > (1 << 19)))
         return PA_ERR_UNSUPPORTED;
     if (!query_start || (num_rows > 0 && (!positions || !slot_mapping))) return PA_ERR_INVALID_ARG;
     if (num_seqs > 0 && (!seq_lens || !context_lens || !request_blocks ||
@@ -920,7 +921,8 @@ int pa_trim_blocks(const int32_t *request_tables, int32_t *request_blocks,
     if (num_seqs < 0 || num_requests < 0 || request_width < 0 || free_capacity < 0)
         return PA_ERR_INVALID_ARG;
     if (block_size != 16) return PA_ERR_UNSUPPORTED;
-    if (num_seqs > 65535 || free_capacity > (int64_t)INT32_MAX || request_width > (1 << 26))
+    if (num_seqs > 65535 || free_capacity > (int64_t)INT32_MAX || request_width > (1 << 26) ||
+        (request_ids && num_requests > (1 << 19)))
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!request_blocks || !keep_lens || !free_blocks || !free_count ||

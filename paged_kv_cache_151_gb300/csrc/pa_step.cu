@@ -17,7 +17,10 @@
 // blocks does everything in one launch, since the state is updated in place: every
 // block runs the prefix sums over all sequences itself (they are read once from
 // HBM and seven times from L2), then handles a run of the sequences; counts are written
-// behind a cluster barrier that every block's reads precede.
+// behind a cluster barrier that every block's reads precede.  A request named twice
+// would be given blocks twice, or give them back twice, so every block marks the
+// requests in a bit map in shared memory on the way, and nothing is served if a mark
+// was there already.
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -70,9 +73,21 @@ __device__ __forceinline__ void scan2(int64_t &a, int64_t &b, int64_t &ta, int64
     tb = sh[1][ST_WARPS - 1];
 }
 
+// Words of the map of the requests that a call names.
+__host__ __device__ __forceinline__ int map_words(const StepParams &p) {
+    return p.request_ids ? (p.num_requests + 31) / 32 : 0;
+}
+
+// Whether request `id` is marked already; marks it.
+__device__ __forceinline__ bool mark(uint32_t *map, int id) {
+    const uint32_t bit = 1u << (id & 31);
+    return (atomicOr(&map[id >> 5], bit) & bit) != 0;
+}
+
 // What the step wants for sequence s.
 struct Want {
     int id, ctx, rows, held;
+    bool id_ok;
     int64_t need;                          // blocks to take, -1: a bad id or length
 };
 
@@ -81,11 +96,11 @@ __device__ __forceinline__ Want want_of(const StepParams &p, int s) {
     w.id = p.request_ids ? p.request_ids[s] : s;
     w.ctx = p.context_lens[s];
     w.rows = p.new_lens ? p.new_lens[s] : 1;
-    const bool id_ok = w.id >= 0 && w.id < p.num_requests;
-    w.held = id_ok ? p.request_blocks[w.id] : 0;
+    w.id_ok = w.id >= 0 && w.id < p.num_requests;
+    w.held = w.id_ok ? p.request_blocks[w.id] : 0;
     const int64_t end = (int64_t)w.ctx + w.rows;
     const int width = min(p.max_blocks, p.request_width);
-    const bool ok = id_ok && w.ctx >= 0 && w.rows >= 0 && end <= (int64_t)width * 16 &&
+    const bool ok = w.id_ok && w.ctx >= 0 && w.rows >= 0 && end <= (int64_t)width * 16 &&
                     w.held >= 0 && w.held <= p.request_width;
     w.rows = max(w.rows, 0);
     w.need = ok ? max(blocks_for(end) - w.held, 0) : -1;
@@ -102,12 +117,15 @@ __global__ void __launch_bounds__(ST_THREADS, 1) build_step_kernel(const __grid_
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Seq *seqs = reinterpret_cast<Seq *>(smem_raw);         // [run + 1]
     __shared__ int64_t sh[2][ST_WARPS];
-    __shared__ int sh_taken, sh_long;
+    __shared__ int sh_taken, sh_long, sh_twice;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     const int B = p.num_seqs;
     const int lo = (int)((int64_t)B * rank / C), hi = (int)((int64_t)B * (rank + 1) / C);
-    if (tid == 0) sh_taken = sh_long = 0;
+    uint32_t *named = reinterpret_cast<uint32_t *>(seqs + B / C + 2);
+    for (int i = tid; i < map_words(p); i += ST_THREADS) named[i] = 0;
+    if (tid == 0) sh_taken = sh_long = sh_twice = 0;
+    __syncthreads();
 
     int count = p.free_count ? *p.free_count : 0;
     if (count < 0 || count > p.free_capacity) {
@@ -121,17 +139,20 @@ __global__ void __launch_bounds__(ST_THREADS, 1) build_step_kernel(const __grid_
     int64_t rows = 0, need = 0, all_rows, all_need;
     for (int s = s0; s < s1; ++s) {
         const Want w = want_of(p, s);
+        if (p.request_ids && w.id_ok && mark(named, w.id)) sh_twice = 1;
         rows += w.rows;
         need += w.need > 0 ? w.need : 0;
     }
     scan2(rows, need, all_rows, all_need, sh);
-    unsigned bad = 0;
+    const bool twice = sh_twice;           // nothing is served
+    unsigned bad = twice ? ERR_SEQ_LEN : 0;
     int taken = 0;                         // blocks that the last granted sequence reaches to
     for (int s = s0; s < s1; ++s) {
         const Want w = want_of(p, s);
         const int64_t end = need + (w.need > 0 ? w.need : 0), row_end = rows + w.rows;
         bool ok = w.need >= 0 && row_end <= p.num_rows;
-        if (!ok) bad |= ERR_SEQ_LEN;
+        if (!ok && !(p.request_ids && w.id == -1 && row_end <= p.num_rows)) bad |= ERR_SEQ_LEN;
+        ok = ok && !twice;
         if (ok && w.need > 0) {
             if (end <= count) {
                 taken = (int)end;
@@ -232,10 +253,15 @@ __global__ void __launch_bounds__(ST_THREADS, 1) trim_blocks_kernel(const __grid
     extern __shared__ __align__(16) unsigned char smem_raw[];
     int4 *seqs = reinterpret_cast<int4 *>(smem_raw);       // id, kept, given back, place
     __shared__ int64_t sh[2][ST_WARPS];
+    __shared__ int sh_twice;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     const int B = p.num_seqs;
     const int lo = (int)((int64_t)B * rank / C), hi = (int)((int64_t)B * (rank + 1) / C);
+    uint32_t *named = reinterpret_cast<uint32_t *>(seqs + B / C + 2);
+    for (int i = tid; i < map_words(p); i += ST_THREADS) named[i] = 0;
+    if (tid == 0) sh_twice = 0;
+    __syncthreads();
     const int count0 = *p.free_count;
     const bool count_ok = count0 >= 0 && count0 <= p.free_capacity;
     const int64_t count = count_ok ? count0 : p.free_capacity;     // nothing fits then
@@ -247,7 +273,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) trim_blocks_kernel(const __grid
         const bool id_ok = id >= 0 && id < p.num_requests;
         const int held = id_ok ? p.request_blocks[id] : 0;
         if (!id_ok || len < 0 || held < 0 || held > p.request_width) {
-            keep = -1;
+            keep = p.request_ids && id == -1 ? 0 : -1;
             return 0;
         }
         keep = min(held, blocks_for(len));
@@ -259,11 +285,13 @@ __global__ void __launch_bounds__(ST_THREADS, 1) trim_blocks_kernel(const __grid
     for (int s = s0; s < s1; ++s) {
         int id, keep;
         back += back_of(s, id, keep);
+        if (p.request_ids && id >= 0 && id < p.num_requests && mark(named, id)) sh_twice = 1;
     }
     scan2(back, none, all_back, all_none, sh);
-    const bool fits = count_ok && count + all_back <= p.free_capacity;
-    if (!fits && rank == 0 && tid == 0) set_error(p.err, ERR_BLOCK_ID);
-    bool bad = false;
+    bool bad = sh_twice;
+    bool fits = count_ok && count + all_back <= p.free_capacity;
+    if (!fits && !bad && rank == 0 && tid == 0) set_error(p.err, ERR_BLOCK_ID);
+    fits = fits && !bad;                   // a request named twice: nothing changes
     for (int s = s0; s < s1; ++s) {
         int id, keep;
         const int n = back_of(s, id, keep);
@@ -289,20 +317,23 @@ __global__ void __launch_bounds__(ST_THREADS, 1) trim_blocks_kernel(const __grid
     if (rank == 0 && tid == 0) *p.free_count = (int)(count + all_back);
 }
 
+// Shared memory of a run's records.
+size_t records(const StepParams &p, int C) { return ((size_t)p.num_seqs / C + 2) * 16; }
+
 // Blocks of the cluster: one for every few sequences or thousand rows.
 int cluster_of(const StepParams &p) {
     const int64_t work = p.num_rows + 32 * (int64_t)p.num_seqs;
     int C = 1;
     while (C < ST_CLUSTER && work > (int64_t)C * 1024) C *= 2;
     // a run's records have to fit into shared memory
-    while (C < ST_CLUSTER && ((int64_t)p.num_seqs / C + 2) * 16 > 40 * 1024) C *= 2;
+    while (C < ST_CLUSTER && records(p, C) > 40 * 1024) C *= 2;
     return C;
 }
 
 template <typename Kernel>
 cudaError_t launch(Kernel kern, const StepParams &p, cudaStream_t st) {
     const int C = cluster_of(p);
-    const size_t smem = ((size_t)p.num_seqs / C + 2) * 16;
+    const size_t smem = records(p, C) + (size_t)map_words(p) * 4;      // <= 131 + 65 KB
     if (smem > 46 * 1024) {                 // beside the static part
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;

@@ -85,6 +85,11 @@ def blocks_for(n):
     return -(-int(n) // 16)
 
 
+def named_twice(ids, R):
+    ids = [] if ids is None else [int(i) for i in ids if 0 <= i < R]
+    return len(set(ids)) < len(ids)
+
+
 def build_step(st, ids, ctx, new, width, num_rows, num_blocks):
     """One step, sequence by sequence; st: dict of request_tables, request_blocks,
     free_blocks, free_count (numpy, changed in place; free_blocks None: no list).
@@ -98,6 +103,9 @@ def build_step(st, ids, ctx, new, width, num_rows, num_blocks):
     pos, slots = np.zeros(num_rows, np.int64), np.full(num_rows, -1, np.int64)
     total, asked, taken, flags = 0, 0, 0, 0
     old_tables, old_blocks = st["request_tables"].copy(), st["request_blocks"].copy()
+    twice = named_twice(ids, R)
+    if twice:
+        flags |= 0x2
     for s in range(B):
         i = s if ids is None else int(ids[s])
         c, n = int(ctx[s]), 1 if new is None else int(new[s])
@@ -111,11 +119,13 @@ def build_step(st, ids, ctx, new, width, num_rows, num_blocks):
             asked += need
         if not ok or total + rows > num_rows:
             ok = False
-            flags |= 0x2
+            if ids is None or i != -1 or total + rows > num_rows:
+                flags |= 0x2
         elif need and asked > count:
             ok = False
             flags |= 0x40
         table = None
+        ok = ok and not twice
         if ok:
             table = [int(x) for x in old_tables[i]]
             for k in range(need):
@@ -152,13 +162,18 @@ def trim(st, ids, keep):
     """Blocks past keep given back, in place; returns the error flags."""
     R, RW = st["request_tables"].shape
     flags, back = 0, []
+    twice = named_twice(ids, R)
     for s in range(len(keep)):
         i = s if ids is None else int(ids[s])
+        if ids is not None and i == -1:
+            continue
         if not 0 <= i < R or keep[s] < 0 or not 0 <= st["request_blocks"][i] <= RW:
             flags |= 0x2
             continue
         k = min(int(st["request_blocks"][i]), blocks_for(keep[s]))
         back.append((i, k, [int(x) for x in st["request_tables"][i, k:st["request_blocks"][i]]]))
+    if twice:
+        return flags | 0x2
     given = [b for _, _, bs in back for b in bs]
     count = int(st["free_count"][0])
     if count + len(given) > len(st["free_blocks"]):

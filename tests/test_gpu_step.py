@@ -180,6 +180,54 @@ def test_trim_with_bad_entries(cuda_lib):
     assert cuda_lib.pa_device_error(clear=True) == cuda_lib.PA_DEVERR_SEQ_LEN
 
 
+@pytest.mark.parametrize("B", [3, 900, 3000])
+def test_a_request_named_twice_refuses_the_call(cuda_lib, B):
+    """Else its blocks would be taken, or given back, twice."""
+    r = np.random.default_rng(B)
+    ids = r.permutation(B + 5)[:B]
+    S = State(14, B + 5, 6, r.integers(0, 4, B + 5), 4 * B)
+    ids[B - 1] = ids[B // 3]
+    o = both(cuda_lib, S, ids, r.integers(0, 40, B), r.integers(0, 3, B), 6, 3 * B,
+             flags=cuda_lib.PA_DEVERR_SEQ_LEN)
+    assert not o["lens"].any() and (o["slots"] == -1).all()
+    cuda_lib.pa_trim_blocks(S.g["request_tables"], S.g["request_blocks"], i32(ids), i32(np.zeros(B)),
+                            S.g["free_blocks"], S.g["free_count"])
+    assert ps.trim(S.st, ids, np.zeros(B)) == 0x2
+    S.same()
+    assert cuda_lib.pa_device_error(clear=True) == cuda_lib.PA_DEVERR_SEQ_LEN
+
+
+@pytest.mark.parametrize("B", [4, 2000])
+def test_padded_entries(cuda_lib, B):
+    r = np.random.default_rng(B)
+    ids = np.where(np.arange(B) % 4 == 1, -1, np.arange(B))
+    S = State(15, B, 6, np.full(B, 2), 4 * B)
+    o = both(cuda_lib, S, ids, r.integers(17, 33, B), np.where(ids < 0, 0, r.integers(1, 5, B)), 6, 5 * B)
+    assert (o["lens"].cpu().numpy()[ids < 0] == 0).all()
+    cuda_lib.pa_trim_blocks(S.g["request_tables"], S.g["request_blocks"], i32(ids), i32(np.full(B, 16)),
+                            S.g["free_blocks"], S.g["free_count"])
+    assert ps.trim(S.st, ids, np.full(B, 16)) == 0
+    S.same()
+    assert cuda_lib.pa_device_error(clear=True) == 0
+
+
+def test_the_most_sequences_and_requests(cuda_lib):
+    """65535 sequences of 2^19 requests: the largest records and map of named ones."""
+    R, B = 1 << 19, 65535
+    r = np.random.default_rng(16)
+    held = np.zeros(R, int)
+    ids = r.permutation(R)[:B]
+    held[ids] = r.integers(0, 3, B)
+    S = State(16, R, 3, held, B)
+    ctx = np.maximum(held[ids] * 16 - r.integers(0, 16, B), 0)
+    new = (r.random(B) < 0.5).astype(int)
+    both(cuda_lib, S, ids, ctx, new, 3, B)
+    cuda_lib.pa_trim_blocks(S.g["request_tables"], S.g["request_blocks"], i32(ids), i32(ctx),
+                            S.g["free_blocks"], S.g["free_count"])
+    assert ps.trim(S.st, ids, ctx) == 0
+    S.same()
+
+
 def test_an_empty_step(cuda_lib):
     S = State(12, 2, 4, [1, 1], 2)
     both(cuda_lib, S, np.zeros(0, int), np.zeros(0, int), np.zeros(0, int), 4, 5)

@@ -167,6 +167,7 @@ def test_step_checks(lib):
     for i in range(12, 19):
         assert status(f, b, **{f"_{i}": -1}) == -1
     assert status(f, b, _19=32) == -2 and status(f, b, _12=65536) == -2 and status(f, b, _18=2**31) == -2
+    assert status(f, b, _13=2**19 + 1) == -2
     for i in (0, 1, 2, 3, 4, 5, 6, 8, 10, 11):     # not request_ids and new_lens
         assert status(f, b, **{f"_{i}": None}) == -1
     t = [P] * 6 + [4, 9, 6, 50, 16, None]
@@ -176,7 +177,7 @@ def test_step_checks(lib):
         assert status(f, t, **{f"_{i}": -1}) == -1
     for i in (0, 1, 3, 4, 5):
         assert status(f, t, **{f"_{i}": None}) == -1
-    assert status(f, t, _10=8) == -2
+    assert status(f, t, _10=8) == -2 and status(f, t, _7=2**19 + 1) == -2
 
 
 def test_logits_checks(lib):
