@@ -978,7 +978,10 @@ int pa_process_logits(void *out, const void *logits, const int32_t *query_start,
     p.history_stride = history_stride; p.allowed_stride = allowed_stride; p.num_bias = num_bias;
     p.num_seqs = num_seqs; p.num_rows = num_rows; p.vocab = vocab_size; p.probs = probs != 0;
     if (pa::device_error_ptr(&p.err) != cudaSuccess) return PA_ERR_CUDA;
-    const cudaError_t e = pa::process_logits(p, dtype, out_dtype, static_cast<cudaStream_t>(stream));
+    const auto call = dtype == PA_F32    ? pa::process_logits_f32
+                      : dtype == PA_BF16 ? pa::process_logits_bf16
+                                         : pa::process_logits_f16;
+    const cudaError_t e = call(p, out_dtype, static_cast<cudaStream_t>(stream));
     if (e == cudaErrorNotSupported) return PA_ERR_UNSUPPORTED;
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -140,9 +140,12 @@ struct LogitsParams {
     const float *temperature;                 // [num_seqs], nullptr: 1
     int64_t logits_stride, out_stride, history_stride, allowed_stride, num_bias;
     int num_seqs, num_rows, vocab, probs;
+    int run;                                  // elements of a block's run, at most
     unsigned int *err;
 };
-cudaError_t process_logits(const LogitsParams &p, int dtype, int out_dtype, cudaStream_t st);
+cudaError_t process_logits_f32(const LogitsParams &p, int out_dtype, cudaStream_t st);
+cudaError_t process_logits_bf16(const LogitsParams &p, int out_dtype, cudaStream_t st);
+cudaError_t process_logits_f16(const LogitsParams &p, int out_dtype, cudaStream_t st);
 
 // verification of drafted tokens (pa_verify.cu); strides in elements
 struct VerifyParams {

