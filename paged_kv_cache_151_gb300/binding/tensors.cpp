@@ -174,7 +174,7 @@ PyObject *spec_call(PyObject *self, PyObject *args, PyObject *kwargs) {
     }
 }
 
-PyObject *spec_new(PyTypeObject *type, PyObject *args, PyObject *kwargs) {
+PyObject *make(PyTypeObject *type, PyObject *args, PyObject *kwargs) {
     const char *text;
     if (kwargs || !PyArg_ParseTuple(args, "s", &text)) return nullptr;
     auto *self = reinterpret_cast<Spec *>(type->tp_alloc(type, 0));
@@ -239,6 +239,15 @@ PyObject *spec_new(PyTypeObject *type, PyObject *args, PyObject *kwargs) {
         return nullptr;
     }
     return reinterpret_cast<PyObject *>(self);
+}
+
+PyObject *spec_new(PyTypeObject *type, PyObject *args, PyObject *kwargs) {
+    try {
+        return make(type, args, kwargs);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_MemoryError, e.what());
+        return nullptr;
+    }
 }
 
 void spec_dealloc(PyObject *self_) {

@@ -235,15 +235,15 @@ __device__ __forceinline__ void forbid(const uint32_t *bits, int w0, int v, floa
 
 // What a thread counts first, loaded ahead: some of the history's tokens, a draft and
 // an entry of the biases.
-constexpr int LG_AHEAD = 2;                // history loads of a thread in flight
-struct Tokens {
-    int32_t h[LG_AHEAD], draft, entry;
+// AHEAD: history loads of a thread in flight.
+template <int AHEAD> struct Tokens {
+    int32_t h[AHEAD], draft, entry;
     float value;                           // of the entry; for the warp that adds the biases up
     template <int NT>
     __device__ __forceinline__ void read(const LogitsParams &p, const Words &q, const int32_t *hist, int r) {
         const int tid = threadIdx.x;
 #pragma unroll
-        for (int e = 0; e < LG_AHEAD; ++e) h[e] = tid + e * NT < q.len ? hist[tid + e * NT] : -1;
+        for (int e = 0; e < AHEAD; ++e) h[e] = tid + e * NT < q.len ? hist[tid + e * NT] : -1;
         draft = p.tokens && q.penalise && q.first + 1 + tid <= r ? p.tokens[q.first + 1 + tid] : -1;
         entry = q.b0 + tid < q.b1 ? p.bias_tokens[q.b0 + tid] : -1;
         value = tid < 32 && q.b0 + tid < q.b1 ? p.bias_values[q.b0 + tid] : 0.f;
@@ -252,9 +252,9 @@ struct Tokens {
 
 // The words of the tokens of elements t0 .. t1 of a row: its history, the drafts
 // before it, its biases.  Returns whether a token lies outside the vocabulary.
-template <int NT>
+template <int NT, int AHEAD>
 __device__ __forceinline__ bool count_tokens(const LogitsParams &p, const Words &q, const int32_t *hist, int r,
-                                             int t0, int t1, uint32_t *counts, Tokens &k) {
+                                             int t0, int t1, uint32_t *counts, Tokens<AHEAD> &k) {
     const int tid = threadIdx.x, lo = max(t0, 0);
     bool bad = false;
     auto add = [&](int32_t v, bool prompt) {
@@ -264,15 +264,15 @@ __device__ __forceinline__ bool count_tokens(const LogitsParams &p, const Words 
             else atomicAdd(&counts[v - t0], 1u);
         }
     };
-    for (int i = tid; i < q.len; i += LG_AHEAD * NT) {
-        int32_t next[LG_AHEAD];
+    for (int i = tid; i < q.len; i += AHEAD * NT) {
+        int32_t next[AHEAD];
 #pragma unroll
-        for (int e = 0; e < LG_AHEAD; ++e) {
-            const int at = i + (LG_AHEAD + e) * NT;
+        for (int e = 0; e < AHEAD; ++e) {
+            const int at = i + (AHEAD + e) * NT;
             next[e] = at < q.len ? hist[at] : -1;
         }
 #pragma unroll
-        for (int e = 0; e < LG_AHEAD; ++e) {
+        for (int e = 0; e < AHEAD; ++e) {
             if (i + e * NT < q.len) add(k.h[e], i + e * NT < q.asked);
             k.h[e] = next[e];
         }
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_logits_kernel(const __g
 
     // counts of the tile's tokens: prompt and bias flags, times in the output
     const int32_t *hist = p.history ? p.history + (int64_t)s * p.history_stride : nullptr;
-    Tokens k;
+    Tokens<4> k;
     auto build = [&](int t0, int t1) {
         k.read<NT>(p, q, hist, r);
 #pragma unroll
@@ -595,12 +595,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_logits_kernel(const __g
 // into shared memory by a bulk copy and its mask and its sequence's words by small ones,
 // and its tokens are counted while the blocks exchange the first one's sums; counts are
 // cleared as they are read.  237 rows of 131071 (bf16 to f32, a history of 4000, biases,
-// masks, probabilities) take 80 us where a row a cluster at a time took 94, 256 rows of
+// masks, probabilities) take 82 us where a row a cluster at a time took 94, 256 rows of
 // 50021 (f32, no probabilities) 33 us instead of 38.  What is left of a row's 26 thousand
 // clocks (two blocks of 512 an SM): 5 the penalties and masks, 5 the counting, 3 each the
 // joining of the warps' sums and the stores.  Registers are the limit: with 250 bytes
 // of spills the same loop took 95 us, so what the next row needs stays in shared memory,
-// and two loads of the history are in flight, not four (82.5) or eight (90).
+// and two loads of the history are in flight (80.4 us), not four (82.5) or eight (90).
 template <typename T, typename O, int NT, int EPT, bool PROBS>
 __global__ void __launch_bounds__(NT, 1024 / NT) process_rows_kernel(const __grid_constant__ LogitsParams p, int C) {
     constexpr int TILE = NT * EPT, WARPS = NT / 32, Q = EPT / 4, ES = (int)sizeof(T);
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_rows_kernel(const __gri
         if (w.mask && w.v1 > max(w.v0, 0)) fetch_mask<NT>(bits, w.mask, w.v0, w.v1);
     };
     auto history_of = [&](int s) { return p.history ? p.history + (int64_t)s * p.history_stride : nullptr; };
-    auto count_row = [&](const Words &q, const Part<T, O> &w, int r, int s, Tokens &k) {
+    auto count_row = [&](const Words &q, const Part<T, O> &w, int r, int s, Tokens<2> &k) {
         if (counting && q.count && count_tokens<NT>(p, q, history_of(s), r, w.v0, w.v1, counts, k) && rank == 0)
             set_error(p.err, ERR_TOKEN);
         if (tid < 32) {
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_rows_kernel(const __gri
         __syncthreads();
         ask_words(r + step, sequence(r + step));
         if (s >= 0) {
-            Tokens k;
+            Tokens<2> k;
             k.read<NT>(p, words[0], history_of(s), r);
             count_row(words[0], w, r, s, k);
         }
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) process_rows_kernel(const __gri
         }
         if (s2 >= 0) {
             const Part<T, O> w2(p, r2, rank, C);
-            Tokens k;
+            Tokens<2> k;
             k.read<NT>(p, words[now ^ 1], history_of(s2), r2);
             put_edge(w2, r2);
             count_row(words[now ^ 1], w2, r2, s2, k);
