@@ -36,6 +36,8 @@ constexpr int ST_WARPS = ST_THREADS / 32;
 constexpr int ST_CLUSTER = 8;
 // entries of a table that one warp copies; longer tables are shared by the block
 constexpr int ST_WARP_ENTRIES = 512;
+// sequences that a warp takes side by side
+constexpr int SIDE = 4;
 
 __device__ __forceinline__ int blocks_for(int64_t tokens) { return (int)((tokens + 15) >> 4); }
 
@@ -202,10 +204,36 @@ __global__ void __launch_bounds__(ST_THREADS, 1) build_step_kernel(const __grid_
             if (e >= q.held) req[e] = b;
         }
     };
-    for (int i = warp; i < hi - lo; i += ST_WARPS) {
-        if (seqs[i].held < 0) continue;
-        const int n = blocks_for((int64_t)seqs[i].ctx + rows_of(i));
-        table(i, 0, min(n, ST_WARP_ENTRIES), lane, 32);
+    // (four sequences' first entries at a time: one after the other each waited for its
+    // id and for its table)
+    for (int i0 = warp; i0 < hi - lo; i0 += ST_WARPS * SIDE) {
+        int n[SIDE], b[SIDE][2];
+        int64_t id[SIDE];
+#pragma unroll
+        for (int j = 0; j < SIDE; ++j) {
+            const int i = i0 + j * ST_WARPS;
+            const bool some = i < hi - lo && seqs[i].held >= 0;
+            n[j] = some ? min(blocks_for((int64_t)seqs[i].ctx + rows_of(i)), ST_WARP_ENTRIES) : 0;
+            id[j] = some && p.request_ids ? p.request_ids[lo + i] : lo + i;
+        }
+#pragma unroll
+        for (int j = 0; j < SIDE; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (lane + 32 * h < n[j])
+                    b[j][h] = entry(seqs[i0 + j * ST_WARPS], p.request_tables + id[j] * p.request_width, lane + 32 * h);
+#pragma unroll
+        for (int j = 0; j < SIDE; ++j) {
+            const int i = i0 + j * ST_WARPS;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int e = lane + 32 * h;
+                if (e >= n[j]) continue;
+                p.block_tables[(int64_t)(lo + i) * p.max_blocks + e] = b[j][h];
+                if (e >= seqs[i].held) p.request_tables[id[j] * p.request_width + e] = b[j][h];
+            }
+            if (n[j] > 64) table(i, 64, n[j], lane, 32);
+        }
     }
     if (sh_long) {
         for (int i = 0; i < hi - lo; ++i) {
@@ -217,15 +245,15 @@ __global__ void __launch_bounds__(ST_THREADS, 1) build_step_kernel(const __grid_
 
     // ---- positions and slots of this run's rows
     const int r0 = seqs[0].row, r1 = seqs[hi - lo].row;
-    for (int r = r0 + tid; r < r1 && hi > lo; r += ST_THREADS) {
+    auto place = [&](int r, int64_t &pos, int64_t &slot) {
         int a = 0, b = hi - lo - 1;        // the last sequence that starts at or before r
         while (a < b) {
             const int mid = (a + b + 1) >> 1;
             if (seqs[mid].row <= r) a = mid; else b = mid - 1;
         }
         const Seq q = seqs[a];
-        const int64_t pos = (int64_t)q.ctx + (r - q.row);
-        int64_t slot = -1;
+        pos = (int64_t)q.ctx + (r - q.row);
+        slot = -1;
         if (q.held >= 0) {
             const int s = lo + a;
             const int32_t id = p.request_ids ? p.request_ids[s] : s;
@@ -233,6 +261,10 @@ __global__ void __launch_bounds__(ST_THREADS, 1) build_step_kernel(const __grid_
             if (blk >= 0 && blk < p.num_blocks) slot = (int64_t)blk * 16 + (pos & 15);
             else set_error(p.err, ERR_BLOCK_ID);
         }
+    };
+    for (int r = r0 + tid; r < r1 && hi > lo; r += ST_THREADS) {
+        int64_t pos, slot;
+        place(r, pos, slot);
         p.positions[r] = pos;
         p.slot_mapping[r] = slot;
     }
@@ -306,11 +338,22 @@ __global__ void __launch_bounds__(ST_THREADS, 1) trim_blocks_kernel(const __grid
     if (C > 1) cluster_arrive();           // this block has read the counts
     __syncthreads();
     if (fits) {
-        for (int i = warp; i < hi - lo; i += ST_WARPS) {
-            const int4 q = seqs[i];
-            const int32_t *req = p.request_tables + (int64_t)q.x * p.request_width + q.y;
-            int32_t *to = p.free_blocks + (count + all_back - 1 - q.w);
-            for (int e = lane; e < q.z; e += 32) to[-e] = req[e];
+        for (int i0 = warp; i0 < hi - lo; i0 += ST_WARPS * SIDE) {
+            int4 q[SIDE];                  // (side by side, as in the building)
+            int32_t b[SIDE];
+#pragma unroll
+            for (int j = 0; j < SIDE; ++j) {
+                const int i = i0 + j * ST_WARPS;
+                q[j] = i < hi - lo ? seqs[i] : make_int4(0, 0, 0, 0);
+                if (lane < q[j].z) b[j] = p.request_tables[(int64_t)q[j].x * p.request_width + q[j].y + lane];
+            }
+#pragma unroll
+            for (int j = 0; j < SIDE; ++j) {
+                const int32_t *req = p.request_tables + (int64_t)q[j].x * p.request_width + q[j].y;
+                int32_t *to = p.free_blocks + (count + all_back - 1 - q[j].w);
+                if (lane < q[j].z) to[-lane] = b[j];
+                for (int e = lane + 32; e < q[j].z; e += 32) to[-e] = req[e];
+            }
         }
     }
     if (C > 1) cluster_wait();
