@@ -21,7 +21,7 @@
 // would be given blocks twice, or give them back twice, so every block marks the
 // requests in a bit map in shared memory on the way, and nothing is served if a mark
 // was there already.  Building a step of 256 sequences with five rows each takes 6 us
-// and its trim 6, of 3001 requests with 33649 rows 33 us together: a launch, and one
+// and its trim 6, of 3001 requests with 33649 rows 29 us together: a launch, and one
 // after the other the loads of ids, lengths, counts and tables with a cluster's
 // barrier, some eight trips to memory.
 #include "pa_common.cuh"
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(ST_THREADS, 1) build_step_kernel(const __grid_
         }
     };
     // (four sequences' first entries at a time: one after the other each waited for its
-    // id and for its table)
+    // id and for its table, 33.7 us for 3001 requests where it is 29.3)
     for (int i0 = warp; i0 < hi - lo; i0 += ST_WARPS * SIDE) {
         int n[SIDE], b[SIDE][2];
         int64_t id[SIDE];
